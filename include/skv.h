@@ -335,6 +335,61 @@ SKV_API skv_status skv_attend(skv_ctx *ctx, const int32_t *req_ids_dev, int32_t 
                               const int32_t *slots_dev, void *out_dev, float *lse_dev, float sm_scale,
                               skv_stream_t stream);
 
+/* KV rows in 4 bits.  A context whose row_bytes is SKV_Q4_ROW_BYTES can hold
+ * packed rows: publish, write back, extend, assemble and prefetch move rows as
+ * bytes and work on them as they are, at 336 instead of 1152 bytes a token
+ * over the host link.  skv_pack_rows makes packed rows from bf16 rows,
+ * skv_unpack_rows reads them back, skv_attend_q4 attends over a hot buffer of
+ * them.
+ *
+ * The packed row of 576 values x[0..576), in 36 groups of 16:
+ *   bytes [0, 288)    e2m1 codes: value 2j in the low half of byte j, 2j + 1 in
+ *                     the high half;
+ *   bytes [288, 324)  one e4m3 scale a group;
+ *   byte 324          e + 127, e the row's exponent;
+ *   bytes [325, 336)  zeros.
+ * It stands for the values code * scale * 2^e, which bf16 holds exactly.  For
+ * group g let a_g = max |x|; a group that holds a NaN or an infinity has a_g = 0
+ * here, a NaN scale and zero codes, and all of it reads back as NaN.
+ *   e       least integer with 2688 * 2^e >= max_g a_g (2688 = 448 * 6, the
+ *           largest e4m3 times the largest e2m1), kept in [-100, 116];
+ *   scale_g a_g * 2^-e / 6, rounded to e4m3;
+ *   code_i  x_i * 2^-e / scale_g, rounded to e2m1 (0 where scale_g is 0).
+ * Roundings are to nearest, ties to even, and saturate.
+ * Source: the pages give no row format; what bounds them, data movement between
+ * the tiers, is what 4 bits a value relieve ([talk] agenda item 3). */
+#define SKV_Q4_ROW_BYTES 336
+
+/* Pack n rows: row i (576 bf16) at rows + i * rows_stride bytes becomes the
+ * packed row at packed + i * 336; with values not null, the bf16 values it stands
+ * for go to values + i * 1152 as well (what a later step will read, e.g. for
+ * this step's own attention over the new token).  Memory the context's device
+ * can address (device, or pinned host memory), 16-byte aligned; packed and
+ * values do not overlap the rows.  rows_stride is a multiple of 16 in [1152,
+ * 2^24]; 0 <= n <= 2^32; n == 0 enqueues nothing.  Needs no packed rows in ctx,
+ * which only gives the device.  Captures into a CUDA graph. */
+SKV_API skv_status skv_pack_rows(skv_ctx *ctx, const void *rows, int64_t rows_stride, int64_t n, void *packed,
+                                 void *values, skv_stream_t stream);
+
+/* Unpack n rows: the values that the packed row at packed + i * 336 stands for
+ * go to values + i * 1152 as 576 bf16 (exact for rows that skv_pack_rows made;
+ * a row of zero bytes reads as zeros).  Memory, alignment and n as for
+ * skv_pack_rows. */
+SKV_API skv_status skv_unpack_rows(skv_ctx *ctx, const void *packed, int64_t n, void *values, skv_stream_t stream);
+
+/* skv_attend over a hot buffer of packed rows: the same arguments, layouts,
+ * masking, errors and ordering, with keys_j the values that the packed hot row
+ * at slots[unit][j] stands for.  Requires row_bytes == SKV_Q4_ROW_BYTES.  The
+ * rows are turned into bf16 on their way into shared memory (exactly), so the
+ * products are skv_attend's.  When a call has fewer units than the device has
+ * SM pairs (or than skv_set_attend_sms leaves it), each unit's keys are split
+ * over several pairs and the partial results, in scratch the context owns, are
+ * joined by a second kernel; the sums are then taken in another order, so
+ * results may differ in rounding with the SM count (never from call to call). */
+SKV_API skv_status skv_attend_q4(skv_ctx *ctx, const int32_t *req_ids_dev, int32_t B, int32_t layer, const void *q_dev,
+                                 const int32_t *slots_dev, void *out_dev, float *lse_dev, float sm_scale,
+                                 skv_stream_t stream);
+
 /* Read the sticky device error word into *bits (SKV_DEVERR_* mask, 0 = none)
  * and clear it.  Synchronises `stream`.
  * Source: the pages are silent on invalid input; this library's reading is

@@ -8,7 +8,8 @@ The binding is loaded on first use of any exported name, so that
 using the API without the library raises ImportError (there is no fallback).
 """
 _EXPORTS = ("Config", "Context", "SkvError", "SKV_DEVERR_BAD_INDEX", "SKV_DEVERR_BAD_REQUEST",
-            "SKV_DEVERR_CONTEXT_FULL", "SKV_DEVERR_DUPLICATE", "LIB_PATH", "skv")
+            "SKV_DEVERR_CONTEXT_FULL", "SKV_DEVERR_DUPLICATE", "SKV_Q4_ROW_BYTES",
+            "LIB_PATH", "skv")
 
 __all__ = list(_EXPORTS)
 

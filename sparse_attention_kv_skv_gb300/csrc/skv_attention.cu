@@ -49,6 +49,7 @@
 #include <cmath>
 #include <string>
 
+#include "q4.cuh"
 #include "skv_ctx.cuh"
 #include "tcgen05.cuh"
 
@@ -295,10 +296,122 @@ __device__ __forceinline__ void give_up(AttnCtl& c, uint32_t* err)
     }
 }
 
+// Packed rows only: how the units of a call are split along their keys.  Split
+// j of a unit is walked like a unit of its own, over blocks [j * blocks,
+// (j + 1) * blocks) of the unit's slot list (keys past its end are masked), and
+// leaves its normalised output and lse in `o` and `lse`; combine_kernel joins them.
+struct KeySplit {
+    int n;       // splits a unit (1: the kernel writes the results itself)
+    int blocks;  // key blocks a split
+    float* o;    // [units * n][512][128 heads]
+    float* lse;  // [units * n][128], log2 domain
+};
+
+constexpr int kPairChunks = 2;                              // 16-byte chunks of codes (32 dims each) a task takes of a row
+constexpr int kTaskRows = 32 / kPairChunks;                 // key rows a warp task covers
+constexpr int kTasks = kWinBoxes * (kBlk / kTaskRows);      // warp tasks a block (20): a 64-dim box of 16 rows each
+constexpr int kWarpTasks = (kTasks + kLoadWarps - 1) / kLoadWarps;
+
+// The loaders of packed rows: per key block, 20 tasks of 16 rows by one 64-dim
+// box of this CTA's window, spread over the seven warps.  Lane 2j + c reads 16
+// bytes of codes (32 dims) of row j, its two scales and the row's exponent,
+// and writes the 32 bf16 values where the swizzle puts them: a quarter warp
+// writes four rows by both halves of a 128-byte line, which the swizzle spreads
+// over all banks.  The slots of a block are fetched two blocks ahead and its
+// rows one block ahead (they are in flight while the previous block waits for
+// its stage and is written).  next_req(u) is the request of unit u or -1.
+template <typename ReqOf>
+__device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const Dev& d, const int32_t* __restrict__ slots,
+                                                 const KeySplit& sp, uint8_t* sK, int nst, int gtot, int cl, int ncl,
+                                                 int h, int lw, int lane, const volatile uint32_t* abort, ReqOf req_of)
+{
+    struct Slots {
+        int32_t a, b;  // slots of keys `lane` and 32 + `lane` of the block, -1 masked
+        int64_t row0;  // the unit's first hot row
+    };
+    struct Rows {
+        uint4 codes[kWarpTasks];
+        uint32_t meta[kWarpTasks];  // two scales, then the exponent byte
+    };
+    int u = cl - ncl, i = sp.blocks - 1;  // the block before the first
+    int key0 = 0;
+    int64_t row0 = 0;
+    const int32_t* sl = slots;
+    auto fetch = [&]() -> Slots {  // the next block's slots; called gtot times at most
+        if (++i == sp.blocks) {
+            int b, l;
+            int32_t r;
+            do {
+                u += ncl;
+                r = req_of(u, b, l);
+            } while (r < 0);
+            i = 0;
+            row0 = ((int64_t)r * d.L + l) * d.S;
+            sl = slots + (size_t)(u / sp.n) * d.k;
+            key0 = (u % sp.n) * sp.blocks * kBlk;
+        }
+        const int key = key0 + i * kBlk + lane;
+        const int32_t a = key < d.k ? sl[key] : -1, b = key + 32 < d.k ? sl[key + 32] : -1;
+        return Slots{a >= 0 && a < d.S ? a : -1, b >= 0 && b < d.S ? b : -1, row0};
+    };
+    auto request = [&](const Slots& s, Rows& w) {
+#pragma unroll
+        for (int x = 0; x < kWarpTasks; ++x) {
+            const int task = lw + kLoadWarps * x;
+            if (task < kTasks) {
+                const int rg = task & 3, chunk = 8 * h + kPairChunks * (task >> 2) + (lane & 1);
+                const int32_t slot = __shfl_sync(0xFFFFFFFFu, rg < 2 ? s.a : s.b, (kTaskRows * rg + (lane >> 1)) & 31);
+                w.codes[x] = make_uint4(0, 0, 0, 0);
+                w.meta[x] = 0u;  // a masked key reads as zeros
+                if (slot >= 0) {
+                    const uint8_t* p = d.hot + (size_t)(s.row0 + slot) * q4::kRowBytes;
+                    w.codes[x] = __ldg(reinterpret_cast<const uint4*>(p) + chunk);
+                    w.meta[x] = __ldg(reinterpret_cast<const uint16_t*>(p + q4::kScalesAt) + chunk) |
+                                (uint32_t)__ldg(p + q4::kExpAt) << 16;
+                }
+            }
+        }
+    };
+    Rows cur, nxt;
+    Slots s{-1, -1, 0};
+    if (gtot > 0) request(fetch(), cur);
+    if (gtot > 1) s = fetch();
+    for (int g = 0; g < gtot; ++g) {
+        if (g + 1 < gtot) request(s, nxt);
+        if (g + 2 < gtot) s = fetch();
+        const int st = g % nst;
+        if (g >= nst && !__all_sync(0xFFFFFFFFu, wait_phase(&c.empty[st], ((g / nst) - 1) & 1, abort))) return false;
+        uint8_t* stage = sK + st * kStageBytes;
+#pragma unroll
+        for (int x = 0; x < kWarpTasks; ++x) {
+            const int task = lw + kLoadWarps * x;
+            if (task < kTasks) {
+                const int row = kTaskRows * (task & 3) + (lane >> 1);
+                uint8_t* line = stage + (task >> 2) * kBoxBytes + row * 128;
+                const uint32_t f0 = q4::group_factor(cur.meta[x] & 0xFFu, cur.meta[x] >> 16);
+                const uint32_t f1 = q4::group_factor((cur.meta[x] >> 8) & 0xFFu, cur.meta[x] >> 16);
+                const uint32_t w[4] = {cur.codes[x].x, cur.codes[x].y, cur.codes[x].z, cur.codes[x].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4*>(line + (((4 * (lane & 1) + j) ^ (row & 7)) << 4)) =
+                        q4::decode8(w[j], j < 2 ? f0 : f1);
+            }
+        }
+        tc::fence_smem_async();  // the tensor core reads the stage
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&c.full[st]);
+        cur = nxt;
+    }
+    return true;
+}
+
+// kQ4: the hot buffer holds packed rows (q4.cuh) instead of bf16 rows; the key
+// stages hold the same bf16 values either way.
+template <bool kQ4>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap hot_map, Dev d, const int32_t* __restrict__ req_ids,
                   const uint16_t* __restrict__ q, const int32_t* __restrict__ slots, uint16_t* __restrict__ out,
-                  float* __restrict__ lse, float scale_log2, AttnLayout lay, int units, int withhold_keys)
+                  float* __restrict__ lse, float scale_log2, AttnLayout lay, int units, int withhold_keys, KeySplit ks)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     AttnCtl& c = *reinterpret_cast<AttnCtl*>(smem + lay.off_ctl);
@@ -307,10 +420,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;  // this cluster; clusters of the grid
     const uint32_t h = blockIdx.x & 1u, peer = h ^ 1u;     // rank in the cluster = value / score half
     const int k = d.k, S = d.S;
-    const int nblk = (k + kBlk - 1) / kBlk;
+    const int nblk = kQ4 ? ks.blocks : (k + kBlk - 1) / kBlk;
+    const int nsp = kQ4 ? ks.n : 1;  // `units` counts every split of a unit
     // The cluster serves units cl, cl + ncl, ... in order; blocks are numbered across them (g), so the
     // key pipeline, the exchanges and all phase arithmetic run on without a break between units.
     auto req_of = [&](int u, int& b, int& l) -> int32_t {
+        if constexpr (kQ4) u /= nsp;
         b = d.layer_sel >= 0 ? u : u / d.L;
         l = d.layer_sel >= 0 ? d.layer_sel : u % d.L;
         const int32_t r = req_ids[b];
@@ -360,7 +475,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     // warpgroup per sub-partition).
     if (warp >= kMmaWarp) {
         tc::regs_shrink<kServiceRegs>();
-        if (warp >= kLoadWarp0) {
+        if (kQ4 && warp >= kLoadWarp0) {
+            if constexpr (kQ4) {
+                const bool ok = load_packed_keys(c, d, slots, ks, sK, nst, gtot, cl, ncl, (int)h, warp - kLoadWarp0, lane,
+                                                 abort, req_of);
+                if (!ok && lane == 0) give_up(c, &d.ctl[CTL_ERR]);
+                __syncwarp();
+            }
+        } else if (warp >= kLoadWarp0) {
             // ---- loaders: seven warps share a block's 80 TMA copies (four key rows x one 64-dim box of
             // this CTA's 320-dim window; a masked slot is row -1, which reads zeros), lane j of warp w
             // issuing copy w + 7j -- TMA issue is paced per issuing thread, so the copies are spread over
@@ -517,7 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             int b, l;
             if (req_of(u, b, l) < 0) continue;
             {   // Q of the unit: this head's 288 score dims into columns [kColQ, kColQ + 144)
-                const uint4* qr = reinterpret_cast<const uint4*>(q + ((size_t)u * kHeads + hd) * kDim + h * kQKHalf);
+                const uint4* qr = reinterpret_cast<const uint4*>(q + ((size_t)(u / nsp) * kHeads + hd) * kDim + h * kQKHalf);
 #pragma unroll 3
                 for (int gq = 0; gq < kQKHalf / 32; ++gq) {  // 9 groups of 16 columns
                     uint4 a = qr[4 * gq], bq = qr[4 * gq + 1], cq4 = qr[4 * gq + 2], dq = qr[4 * gq + 3];
@@ -535,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 // warm L2 with the next unit's Q row a few blocks before it is loaded (earlier, the key rows
                 // streaming through L2 in the meantime would evict it)
                 if (i == (nblk > 3 ? nblk - 3 : 0) && u + ncl < units) {
-                    const uint8_t* nq = reinterpret_cast<const uint8_t*>(q + ((size_t)(u + ncl) * kHeads + hd) * kDim + h * kQKHalf);
+                    const uint8_t* nq = reinterpret_cast<const uint8_t*>(q + ((size_t)((u + ncl) / nsp) * kHeads + hd) * kDim + h * kQKHalf);
 #pragma unroll
                     for (int x = 0; x < 5; ++x) tc::prefetch_l2(nq + 128 * x);
                 }
@@ -592,15 +714,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         for (int u = cl; u < units; u += ncl) {
             int b, l;
             if (req_of(u, b, l) < 0) {  // not a request: zeros and lse = -inf, nothing else takes part
+                if (nsp > 1) {  // combine_kernel skips a split whose lse is -inf
+                    if (h == 0) ks.lse[(size_t)u * kHeads + hd] = -INFINITY;
+                    continue;
+                }
                 uint16_t* o = out + ((size_t)u * kHeads + hd) * 512 + h * kVHalf;
                 for (int cc = 0; cc < kVHalf; cc += 8) *reinterpret_cast<uint4*>(o + cc) = make_uint4(0, 0, 0, 0);
                 if (h == 0 && lse) lse[(size_t)u * kHeads + hd] = -INFINITY;
                 continue;
             }
             if (!ok) continue;
-            const int32_t* sl = slots + (size_t)u * k;
+            const int32_t* sl = slots + (size_t)(u / nsp) * k;
+            const int blk0 = kQ4 ? (u % nsp) * nblk : 0;  // the split's first block
             auto slot_of = [&](int i) -> int32_t {  // the slot of my key `lane` of block i
-                const int key = i * kBlk + kHalfBlk * (int)h + lane;
+                const int key = (blk0 + i) * kBlk + kHalfBlk * (int)h + lane;
                 return key < k ? sl[key] : -1;
             };
             float m_ref = -INFINITY;  // reference maximum (log2 domain) the exponentials use; equal in both CTAs
@@ -727,10 +854,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 // of this unit has completed and the peer writes a P tile only after every thread here
                 // has sent it the next block's maxima.  16-byte chunk c of staged row r sits at chunk
                 // position c ^ (r % 16), which keeps both passes free of bank conflicts.
+                if (nsp > 1) {
+                    // a split's result: fp32, columns outermost, so that a warp's stores are whole lines
+                    float* po = ks.o + ((size_t)u * 512 + h * kVHalf) * kHeads + hd;
+                    for (int c0 = 0; c0 < kVHalf; c0 += 32) {
+                        float ov[32];
+                        tc::tmem_ld32(tl + kColO + (uint32_t)c0, ov);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) po[(size_t)(c0 + j) * kHeads] = ov[j] * inv;
+                    }
+                    if (h == 0) ks.lse[(size_t)u * kHeads + hd] = l_all == 0.0f ? -INFINITY : m_ref + log2f(l_all);
+                }
                 uint8_t* stage = sP + 4096u * (uint32_t)warp;
                 uint16_t* orow = out + ((size_t)u * kHeads + (hd & ~31)) * 512 + h * kVHalf;  // the warp's first row
                 uint8_t* mine = stage + (lane >> 4) * kPBytes + (lane & 15) * 256;
-                for (int half = 0; half < 2; ++half) {
+                for (int half = 0; half < 2 && nsp == 1; ++half) {
 #pragma unroll
                     for (int c0 = 0; c0 < 128; c0 += 32) {
                         float ov[32];
@@ -751,7 +889,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (h == 0 && lse)
+                if (h == 0 && lse && nsp == 1)
                     lse[(size_t)u * kHeads + hd] = l_all > 0.0f ? (m_ref + log2f(l_all)) * 0.69314718055994531f : -INFINITY;
                 tc::fence_before_sync();
                 tc::mbar_arrive(&c.o_free);  // the next unit's first O += P V may overwrite the accumulator
@@ -775,6 +913,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         tc::fence_after_sync();
         tc::tmem_dealloc(tbase, kTmemCols);
     }
+}
+
+// The results of a unit's splits joined: with lse_i the splits' log2 sums and
+// M their maximum, out = sum 2^(lse_i - M) o_i / sum 2^(lse_i - M).  One CTA per
+// unit and 8 value columns, one thread per head; a split without a single key
+// (lse -inf) is skipped.
+constexpr int kJoinCols = 8;
+__global__ void __launch_bounds__(kHeads) combine_kernel(KeySplit sp, uint16_t* __restrict__ out, float* __restrict__ lse)
+{
+    const int u = blockIdx.y, c0 = blockIdx.x * kJoinCols, hd = threadIdx.x;
+    const float* ls = sp.lse + (size_t)u * sp.n * kHeads + hd;
+    const float* po = sp.o + ((size_t)u * sp.n * 512 + c0) * kHeads + hd;
+    float m = -INFINITY;
+    for (int i = 0; i < sp.n; ++i) m = fmaxf(m, ls[(size_t)i * kHeads]);
+    float acc[kJoinCols] = {}, total = 0.0f;
+#pragma unroll 2
+    for (int i = 0; i < sp.n; ++i) {
+        const float li = ls[(size_t)i * kHeads];
+        if (li == -INFINITY) continue;
+        const float w = ex2(li - m);
+        total += w;
+#pragma unroll
+        for (int j = 0; j < kJoinCols; ++j) acc[j] = fmaf(w, po[((size_t)i * 512 + j) * kHeads], acc[j]);
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    *reinterpret_cast<uint4*>(out + ((size_t)u * kHeads + hd) * 512 + c0) =
+        make_uint4(bf2(acc[0] * inv, acc[1] * inv), bf2(acc[2] * inv, acc[3] * inv), bf2(acc[4] * inv, acc[5] * inv),
+                   bf2(acc[6] * inv, acc[7] * inv));
+    if (blockIdx.x == 0 && lse)
+        lse[(size_t)u * kHeads + hd] = total == 0.0f ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
 }
 
 }  // namespace
@@ -817,7 +985,9 @@ cudaError_t prepare_attend(int* device_sms)
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(device_sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)  // a function attribute is per device: set on the device the context lives on
-        e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
+        e = cudaFuncSetAttribute(attend_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attend_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
     return e;
 }
 
@@ -831,9 +1001,41 @@ cudaError_t launch_attend(const void* hot_map, const Dev& d, const int32_t* req_
     const int units = call_units(d, B);
     const int use_sms = max_sms > 0 ? std::min(max_sms, device_sms) : device_sms;
     const int clusters = std::max(1, std::min(units, use_sms / 2));
-    attend_kernel<<<clusters * 2, kAttnThreads, lay.bytes, st>>>(
+    attend_kernel<false><<<clusters * 2, kAttnThreads, lay.bytes, st>>>(
         *static_cast<const CUtensorMap*>(hot_map), d, req_ids, static_cast<const uint16_t*>(q), slots,
-        static_cast<uint16_t*>(out), lse, sm_scale * 1.4426950408889634f, lay, units, withhold_keys ? 1 : 0);
+        static_cast<uint16_t*>(out), lse, sm_scale * 1.4426950408889634f, lay, units, withhold_keys ? 1 : 0, KeySplit{});
+    return cudaGetLastError();
+}
+
+size_t attend_q4_scratch_bytes(int device_sms)
+{
+    return (size_t)std::max(1, device_sms / 2) * (512 + 1) * kHeads * sizeof(float);
+}
+
+cudaError_t launch_attend_q4(const Dev& d, const int32_t* req_ids, int B, const void* q, const int32_t* slots, void* out,
+                             float* lse, float sm_scale, float* scratch, int max_sms, int device_sms, cudaStream_t st)
+{
+    const AttnLayout lay = attend_layout();
+    if (d.k > (int)kMaxTopk || lay.bytes > kSmemLimit || device_sms < 2) return cudaErrorInvalidValue;
+    const int units = call_units(d, B);
+    const int use_sms = max_sms > 0 ? std::min(max_sms, device_sms) : device_sms;
+    const int pairs = std::max(1, use_sms / 2), nblk = (d.k + kBlk - 1) / kBlk;
+    // Fewer units than clusters: each unit's keys are split over the idle ones, evenly and in whole
+    // blocks.  units * n <= pairs, which is what the scratch holds.
+    KeySplit sp{1, nblk, nullptr, nullptr};
+    if (pairs / units > 1) {
+        sp.blocks = (nblk + pairs / units - 1) / (pairs / units);
+        sp.n = (nblk + sp.blocks - 1) / sp.blocks;
+    }
+    if (sp.n > 1) {
+        sp.o = scratch;
+        sp.lse = scratch + (size_t)units * sp.n * 512 * kHeads;
+    }
+    const int clusters = std::min(units * sp.n, pairs);
+    attend_kernel<true><<<clusters * 2, kAttnThreads, lay.bytes, st>>>(
+        CUtensorMap{}, d, req_ids, static_cast<const uint16_t*>(q), slots, static_cast<uint16_t*>(out), lse,
+        sm_scale * 1.4426950408889634f, lay, units * sp.n, 0, sp);
+    if (sp.n > 1) combine_kernel<<<dim3(512 / kJoinCols, units), kHeads, 0, st>>>(sp, static_cast<uint16_t*>(out), lse);
     return cudaGetLastError();
 }
 
@@ -842,26 +1044,30 @@ cudaError_t launch_attend(const void* hot_map, const Dev& d, const int32_t* req_
 namespace {
 skv_status attend_impl(skv_ctx* ctx, const int32_t* req_ids_dev, int32_t B, int32_t layer, const void* q_dev,
                        const int32_t* slots_dev, void* out_dev, float* lse_dev, float sm_scale, skv_stream_t stream,
-                       bool withhold_keys, const char* what)
+                       bool withhold_keys, const char* what, bool q4 = false)
 {
     if (!ctx || B < 0 || B > ctx->cfg.max_batch || layer < -1 || layer >= ctx->cfg.num_layers ||
         !(sm_scale > 0.0f) || !std::isfinite(sm_scale))
         return SKV_ERR_INVALID_ARG;
     if (B == 0) return SKV_OK;
-    if (!req_ids_dev || !q_dev || !slots_dev || !out_dev || ctx->cfg.row_bytes != skv::kDim * 2)
+    if (!req_ids_dev || !q_dev || !slots_dev || !out_dev ||
+        ctx->cfg.row_bytes != (q4 ? skv::q4::kRowBytes : skv::kRowBytes))
         return SKV_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(q_dev) | reinterpret_cast<uintptr_t>(out_dev)) & 15u) return SKV_ERR_INVALID_ARG;
     int prev = -1;
     if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
     if (prev != ctx->cfg.device && cudaSetDevice(ctx->cfg.device) != cudaSuccess) return SKV_ERR_CUDA;
     cudaError_t e = cudaSuccess;
-    if (!ctx->hot_map_ready) {  // host-side encoding only: safe while a stream is being captured
+    if (!q4 && !ctx->hot_map_ready) {  // host-side encoding only: safe while a stream is being captured
         e = skv::encode_hot_map(ctx->d, &ctx->hot_map);
         ctx->hot_map_ready = e == cudaSuccess;
     }
     skv::Dev d = ctx->d;
     d.layer_sel = layer;
-    if (e == cudaSuccess)
+    if (q4)
+        e = skv::launch_attend_q4(d, req_ids_dev, B, q_dev, slots_dev, out_dev, lse_dev, sm_scale, ctx->q4_scratch,
+                                  ctx->attend_sms, ctx->device_sms, stream);
+    else if (e == cudaSuccess)
         e = skv::launch_attend(&ctx->hot_map, d, req_ids_dev, B, q_dev, slots_dev, out_dev, lse_dev, sm_scale,
                                ctx->attend_sms, ctx->device_sms, stream, withhold_keys);
     if (prev >= 0 && prev != ctx->cfg.device) cudaSetDevice(prev);
@@ -879,6 +1085,14 @@ extern "C" skv_status skv_attend(skv_ctx* ctx, const int32_t* req_ids_dev, int32
 {
     return attend_impl(ctx, req_ids_dev, B, layer, q_dev, slots_dev, out_dev, lse_dev, sm_scale, stream, false,
                        "skv_attend");
+}
+
+extern "C" skv_status skv_attend_q4(skv_ctx* ctx, const int32_t* req_ids_dev, int32_t B, int32_t layer,
+                                    const void* q_dev, const int32_t* slots_dev, void* out_dev, float* lse_dev,
+                                    float sm_scale, skv_stream_t stream)
+{
+    return attend_impl(ctx, req_ids_dev, B, layer, q_dev, slots_dev, out_dev, lse_dev, sm_scale, stream, false,
+                       "skv_attend_q4", true);
 }
 
 extern "C" skv_status skv_selftest_attend_timeout(skv_ctx* ctx, const int32_t* req_ids_dev, int32_t B,

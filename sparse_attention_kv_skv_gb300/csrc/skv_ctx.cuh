@@ -23,6 +23,7 @@ struct skv_ctx {
     int gather_grid = 0;
     CUtensorMap hot_map{};  // TMA view of the hot buffer for the attention consumer (built on first use)
     bool hot_map_ready = false;
+    float* q4_scratch = nullptr;  // partial results of skv_attend_q4 (contexts of packed rows only)
     int attend_sms = 0;     // SMs the attention kernel may occupy (0: all)
     int device_sms = 0;     // SMs of the context's device
     int pool_node_wanted = -1;   // host NUMA node the pool was asked to live on (-1: none)

@@ -86,8 +86,19 @@ cudaError_t encode_hot_map(const Dev& d, struct CUtensorMap_st* map);
 cudaError_t launch_attend(const void* hot_map, const Dev& d, const int32_t* req_ids, int B, const void* q,
                           const int32_t* slots, void* out, float* lse, float sm_scale, int max_sms, int device_sms,
                           cudaStream_t st, bool withhold_keys = false);
+// The same over a hot buffer of packed rows (q4.cuh).  Few units are split along their keys; the partial
+// results go to `scratch` (attend_q4_scratch_bytes(device_sms) bytes, one call at a time).
+size_t attend_q4_scratch_bytes(int device_sms);
+cudaError_t launch_attend_q4(const Dev& d, const int32_t* req_ids, int B, const void* q, const int32_t* slots, void* out,
+                             float* lse, float sm_scale, float* scratch, int max_sms, int device_sms, cudaStream_t st);
 // Once per context, on its device: the kernel's shared-memory attribute; *device_sms = the SM count.
 cudaError_t prepare_attend(int* device_sms);
+
+// Rows to 4 bits and back (q4.cuh); n >= 1.
+constexpr int64_t kMaxPackRows = (int64_t)1 << 32;    // a pool holds fewer
+constexpr int64_t kMaxPackStride = (int64_t)1 << 24;  // bytes; keeps n * stride far inside 64 bits
+cudaError_t launch_pack_rows(const void* rows, int64_t stride, int64_t n, void* packed, void* values, cudaStream_t st);
+cudaError_t launch_unpack_rows(const void* packed, int64_t n, void* values, cudaStream_t st);
 
 // Lifecycle kernels.
 cudaError_t launch_reset_request(const Dev& d, int r, int64_t len, int active, cudaStream_t st);

@@ -23,6 +23,7 @@
 #include <thread>
 #include <vector>
 
+#include "q4.cuh"
 #include "skv_ctx.cuh"
 
 using skv::Dev;
@@ -102,6 +103,7 @@ void free_ctx(skv_ctx* c)
     cudaFree(c->st_slots);
     cudaFree(c->st_hits);
     cudaFree(c->st_misses);
+    cudaFree(c->q4_scratch);
     if (c->host_word) cudaFreeHost(c->host_word);
     free_pool(c);
     delete c;
@@ -463,6 +465,8 @@ skv_status skv_create(const skv_config* cfg, skv_ctx** out)
     SKV_TRY(skv::prepare_step_kernels(c.topk, c.hot_slots, &x->gather_grid));
     SKV_TRY(skv::prepare_attend(&x->device_sms));
     SKV_TRY(skv::noalloc_prepare(c.device));
+    if (c.row_bytes == skv::q4::kRowBytes)  // skv_attend_q4 may be called on this context
+        SKV_ALLOC(cudaMalloc(&x->q4_scratch, skv::attend_q4_scratch_bytes(x->device_sms)));
     SKV_TRY(cudaDeviceSynchronize());
 #undef SKV_ALLOC
 #undef SKV_TRY
@@ -657,6 +661,34 @@ skv_status skv_assemble_host(skv_ctx* ctx, const int32_t* req_ids, int32_t B, co
     if (!d_hits) SKV_CUDA(cudaMemcpyAsync(hits, ctx->st_hits, units * 4, cudaMemcpyDeviceToHost, stream));
     if (!d_misses) SKV_CUDA(cudaMemcpyAsync(misses, ctx->st_misses, units * 4, cudaMemcpyDeviceToHost, stream));
     SKV_CUDA(cudaStreamSynchronize(stream));
+    return SKV_OK;
+}
+
+skv_status skv_pack_rows(skv_ctx* ctx, const void* rows, int64_t rows_stride, int64_t n, void* packed, void* values,
+                         skv_stream_t stream)
+{
+    if (!ctx || n < 0 || n > skv::kMaxPackRows) return SKV_ERR_INVALID_ARG;
+    if (n == 0) return SKV_OK;
+    if (!rows || !packed || rows_stride % 16 != 0 || rows_stride < 2 * skv::q4::kDim ||
+        rows_stride > skv::kMaxPackStride ||
+        ((reinterpret_cast<uintptr_t>(rows) | reinterpret_cast<uintptr_t>(packed) | reinterpret_cast<uintptr_t>(values)) &
+         15u))
+        return SKV_ERR_INVALID_ARG;
+    DeviceGuard g(ctx->cfg.device);
+    if (!g.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+    SKV_CUDA(skv::launch_pack_rows(rows, rows_stride, n, packed, values, stream));
+    return SKV_OK;
+}
+
+skv_status skv_unpack_rows(skv_ctx* ctx, const void* packed, int64_t n, void* values, skv_stream_t stream)
+{
+    if (!ctx || n < 0 || n > skv::kMaxPackRows) return SKV_ERR_INVALID_ARG;
+    if (n == 0) return SKV_OK;
+    if (!packed || !values || ((reinterpret_cast<uintptr_t>(packed) | reinterpret_cast<uintptr_t>(values)) & 15u))
+        return SKV_ERR_INVALID_ARG;
+    DeviceGuard g(ctx->cfg.device);
+    if (!g.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+    SKV_CUDA(skv::launch_unpack_rows(packed, n, values, stream));
     return SKV_OK;
 }
 

@@ -32,6 +32,8 @@ SKV_DEVERR_DUPLICATE = 4
 SKV_DEVERR_CONTEXT_FULL = 8
 SKV_DEVERR_TIMEOUT = 16
 
+SKV_Q4_ROW_BYTES = 336
+
 
 class skv_config(ctypes.Structure):
     _fields_ = [
@@ -78,6 +80,9 @@ def _load():
         "skv_selftest_mma": [vp, vp, vp, i32, i32, i32, vp],
         "skv_attend": [vp, vp, i32, i32, vp, vp, vp, vp, ctypes.c_float, vp],
         "skv_selftest_attend_timeout": [vp, vp, i32, vp, vp, vp, vp],
+        "skv_attend_q4": [vp, vp, i32, i32, vp, vp, vp, vp, ctypes.c_float, vp],
+        "skv_pack_rows": [vp, vp, i64, i64, vp, vp, vp],
+        "skv_unpack_rows": [vp, vp, i64, vp, vp],
         "skv_pool_placement": [vp, P(i32), P(i32), P(ctypes.c_float)],
         "skv_host_node_for_pci": [ctypes.c_char_p, ctypes.c_char_p, P(i32)],
     }
@@ -118,6 +123,9 @@ skv_set_gather_events = lib.skv_set_gather_events
 skv_set_attend_sms = lib.skv_set_attend_sms
 skv_selftest_mma = lib.skv_selftest_mma
 skv_attend = lib.skv_attend
+skv_attend_q4 = lib.skv_attend_q4
+skv_pack_rows = lib.skv_pack_rows
+skv_unpack_rows = lib.skv_unpack_rows
 skv_selftest_attend_timeout = lib.skv_selftest_attend_timeout
 skv_pool_placement = lib.skv_pool_placement
 skv_host_node_for_pci = lib.skv_host_node_for_pci
@@ -166,6 +174,11 @@ def _ptr(t) -> int:
     if hasattr(t, "data_ptr"):
         return t.data_ptr()
     return t.ctypes.data  # numpy
+
+
+def _need(t, nbytes: int, what: str) -> None:
+    if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{what} must be contiguous and hold {nbytes} bytes")
 
 
 @dataclasses.dataclass
@@ -275,6 +288,36 @@ class Context:
         scale = (1.0 / 576 ** 0.5) if sm_scale is None else sm_scale
         check(skv_attend(self.h, _ptr(req_ids), B, layer, _ptr(q), _ptr(slots), _ptr(out), _ptr(lse), scale,
                          _stream_handle(stream)), "skv_attend")
+
+    def attend_q4(self, req_ids, q, slots, out, lse=None, layer: int = -1, sm_scale: float | None = None,
+                  B: int | None = None, stream=None) -> None:
+        """attend() over a hot buffer of packed rows (row_bytes == SKV_Q4_ROW_BYTES; see skv_attend_q4)."""
+        B = req_ids.numel() if B is None else B
+        scale = (1.0 / 576 ** 0.5) if sm_scale is None else sm_scale
+        check(skv_attend_q4(self.h, _ptr(req_ids), B, layer, _ptr(q), _ptr(slots), _ptr(out), _ptr(lse), scale,
+                            _stream_handle(stream)), "skv_attend_q4")
+
+    def pack_rows(self, rows, packed, values=None, stream=None) -> None:
+        """bf16 rows [n][576] (rows may lie apart: rows.stride(0)) -> packed rows
+        [n][336] bytes and, if given, the bf16 values they stand for [n][576]."""
+        if rows.dim() != 2 or rows.shape[1] != 576 or rows.stride(1) != 1 or rows.element_size() != 2:
+            raise ValueError("pack_rows: rows must be [n][576] bf16 with adjacent values")
+        n = rows.shape[0]
+        stride = 2 * rows.stride(0) if n > 1 else 1152
+        _need(packed, 336 * n, "pack_rows: packed")
+        if values is not None:
+            _need(values, 1152 * n, "pack_rows: values")
+        check(skv_pack_rows(self.h, _ptr(rows), stride, n, _ptr(packed), _ptr(values), _stream_handle(stream)),
+              "skv_pack_rows")
+
+    def unpack_rows(self, packed, values, stream=None) -> None:
+        """Packed rows [n][336] bytes -> the bf16 values they stand for [n][576]."""
+        n, rest = divmod(packed.numel() * packed.element_size(), 336)
+        if rest:
+            raise ValueError("unpack_rows: packed must hold whole rows of 336 bytes")
+        _need(packed, 336 * n, "unpack_rows: packed")
+        _need(values, 1152 * n, "unpack_rows: values")
+        check(skv_unpack_rows(self.h, _ptr(packed), n, _ptr(values), _stream_handle(stream)), "skv_unpack_rows")
 
     def selftest_attend_timeout(self, req_ids, q, slots, out, B: int | None = None, stream=None) -> None:
         """The attention kernel with its key loads withheld: its waits run out
