@@ -390,6 +390,58 @@ SKV_API skv_status skv_attend_q4(skv_ctx *ctx, const int32_t *req_ids_dev, int32
                                  const int32_t *slots_dev, void *out_dev, float *lse_dev, float sm_scale,
                                  skv_stream_t stream);
 
+/* The index a Top-k is selected by: one key for every `block` consecutive
+ * tokens (key j of a request stands for its tokens [j*block, (j+1)*block)), bf16,
+ * in device memory the caller owns and fills.  Key j of request r, layer l lies at
+ *   keys + r*request_stride + l*layer_stride + j*key_stride   (strides in bytes)
+ * with its `dim` values adjacent.  The device may read the whole extent of
+ * R x L x ceil(max_context / block) keys (values behind a request's last key are
+ * not used, whatever they are). */
+typedef struct {
+    const void *keys;        /* 16-byte aligned */
+    int64_t request_stride;  /* multiples of 16, > 0, < 2^40 (free where the axis has one entry); */
+    int64_t layer_stride;    /* the axes may lie in any order */
+    int64_t key_stride;      /* >= 2 * dim */
+    int32_t heads;           /* index query heads, 1 .. 64 */
+    int32_t dim;             /* 64 or 128 */
+    int32_t block;           /* tokens a key stands for; divides topk */
+    int32_t first;           /* blocks at the start of the context that are always taken, */
+    int32_t last;            /* and at its end; first + last <= topk / block */
+    int32_t relu;            /* 0: products are summed as they are */
+} skv_index;
+
+/* Bytes of workspace that an skv_select of this shape needs (it depends on
+ * max_context, not on the requests' lengths).  Host code only. */
+SKV_API skv_status skv_select_workspace(skv_ctx *ctx, const skv_index *index, int32_t B, int32_t layer, int64_t *bytes);
+
+/* Select each unit's Top-k tokens by a cheap score over the index keys (the
+ * "select" of select-then-compute: "SGLang и Tair представили иерархичную Sparse
+ * Attention ...", paragraph 2; the indexer's key cache stays in HBM: [xm] section
+ * "为何稀疏注意力需要快速高容量内存层").  Units as in skv_attend: all layers when layer
+ * == -1 (b*L + l), else only `layer` (b).  With r = req_ids_dev[b], T = len(r) as
+ * the device has it when the call runs, n = ceil(T / block):
+ *   score_j = sum_h w[unit][h] * max(0, q[unit][h] . key_j)    j < n
+ * (without the max if index->relu is 0; products and sums in fp32).  Taken are the
+ * first `first` and last `last` blocks and, of the others, those with the
+ * largest scores, k / block in all; of equal scores the lower j.  A NaN product counts as 0 under
+ * the max; a NaN score is below every other.  topk_dev[unit][0..k) receives the tokens of the taken
+ * blocks in ascending order, -1 behind them (fewer than k tokens, or a last
+ * block that T cuts short): what skv_assemble and skv_prefetch take.
+ * q_dev is [units][heads][dim] bf16, w_dev [units][heads] fp32, topk_dev [units][k]
+ * int32; device memory, q_dev and workspace_dev 16-byte aligned.  Scores are fp32
+ * sums, so two blocks whose scores differ by less than their rounding may come in
+ * either order; a call always gives the same result.  A request may appear more
+ * than once in req_ids_dev (several queries of it).  Device errors:
+ * SKV_DEVERR_BAD_REQUEST for an id that is not an active request; the call then
+ * (and while the error word is set) only fills topk_dev with -1.  Changes no
+ * request.  The workspace is the caller's and holds nothing between calls: two
+ * calls, or two captured graphs, that may run at the same time need one each.
+ * Requires max_context <= 2^30.  B == 0 enqueues nothing.  Captures into a CUDA
+ * graph. */
+SKV_API skv_status skv_select(skv_ctx *ctx, const skv_index *index, const int32_t *req_ids_dev, int32_t B, int32_t layer,
+                              const void *q_dev, const float *w_dev, int32_t *topk_dev, void *workspace_dev,
+                              int64_t workspace_bytes, skv_stream_t stream);
+
 /* Read the sticky device error word into *bits (SKV_DEVERR_* mask, 0 = none)
  * and clear it.  Synchronises `stream`.
  * Source: the pages are silent on invalid input; this library's reading is

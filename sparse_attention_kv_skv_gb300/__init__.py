@@ -7,7 +7,7 @@ The binding is loaded on first use of any exported name, so that
 ``sparse_attention_kv_skv_gb300.build`` can run before the library exists;
 using the API without the library raises ImportError (there is no fallback).
 """
-_EXPORTS = ("Config", "Context", "SkvError", "SKV_DEVERR_BAD_INDEX", "SKV_DEVERR_BAD_REQUEST",
+_EXPORTS = ("Config", "Context", "Index", "SkvError", "SKV_DEVERR_BAD_INDEX", "SKV_DEVERR_BAD_REQUEST",
             "SKV_DEVERR_CONTEXT_FULL", "SKV_DEVERR_DUPLICATE", "SKV_Q4_ROW_BYTES",
             "LIB_PATH", "skv")
 

@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libskv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["skv_runtime.cu", "skv_step_kernels.cu", "skv_lifecycle_kernels.cu", "skv_noalloc.cu",
-           "skv_attention.cu", "skv_q4.cu"]
+           "skv_attention.cu", "skv_q4.cu", "skv_select.cu"]
 
 
 def nvcc() -> str:

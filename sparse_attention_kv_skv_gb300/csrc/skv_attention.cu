@@ -949,27 +949,32 @@ __global__ void __launch_bounds__(kHeads) combine_kernel(KeySplit sp, uint16_t* 
 
 size_t attend_smem_bytes(int) { return attend_layout().bytes; }
 
-// The hot buffer as a 2-D tensor of R*L*S rows by 576 bf16 (row stride 1152
-// bytes) for TMA: box one row by 64 columns, 128-byte swizzle, out-of-range
-// rows read as zeros.  cuTensorMapEncodeTiled is reached through the runtime's
-// driver entry point (no link against the driver library).
-cudaError_t encode_hot_map(const Dev& d, CUtensorMap* map)
+cudaError_t tensor_map_encoder(TensorMapEncoder* encode)
 {
-    const uint64_t rows = (uint64_t)d.R * (uint64_t)d.L * (uint64_t)d.S;
-    if (rows > 0x7FFFFFFFull || d.row_bytes != kRowBytes) return cudaErrorInvalidValue;
-    using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static EncodeTiled encode = nullptr;
-    if (!encode) {
+    static TensorMapEncoder known = nullptr;
+    if (!known) {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
         const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
                                                                &found);
         if (e != cudaSuccess) return e;
         if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-        encode = reinterpret_cast<EncodeTiled>(fn);
+        known = reinterpret_cast<TensorMapEncoder>(fn);
     }
+    *encode = known;
+    return cudaSuccess;
+}
+
+// The hot buffer as a 2-D tensor of R*L*S rows by 576 bf16 (row stride 1152
+// bytes) for TMA: box one row by 64 columns, 128-byte swizzle, out-of-range
+// rows read as zeros.
+cudaError_t encode_hot_map(const Dev& d, CUtensorMap* map)
+{
+    const uint64_t rows = (uint64_t)d.R * (uint64_t)d.L * (uint64_t)d.S;
+    if (rows > 0x7FFFFFFFull || d.row_bytes != kRowBytes) return cudaErrorInvalidValue;
+    TensorMapEncoder encode = nullptr;
+    const cudaError_t e = tensor_map_encoder(&encode);
+    if (e != cudaSuccess) return e;
     const cuuint64_t dims[2] = {(cuuint64_t)kDim, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)kRowBytes};
     const cuuint32_t box[2] = {64, 1}, elem_strides[2] = {1, 1};

@@ -34,6 +34,17 @@ struct skv_ctx {
 namespace skv {
 // Sets the message returned by skv_last_cuda_error on this thread.
 void set_last_error_message(const char* msg);
+// The driver's cuTensorMapEncodeTiled, reached through the runtime's entry
+// point query (no link against the driver library).
+using TensorMapEncoder = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+cudaError_t tensor_map_encoder(TensorMapEncoder* encode);
+// Selection of Top-k tokens by index scores (skv_select.cu).  select_stride: scores a unit has room for.
+int64_t select_stride(int64_t max_context, int block);
+cudaError_t prepare_select();  // once per context, on its device
+cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_ids, int B, const void* q, const float* w,
+                          int32_t* topk, void* workspace, int device_sms, cudaStream_t st);
 // Loads skv_assemble_noalloc's static work list on `device` (current) and
 // caches its address, so that no later call loads or allocates anything.
 cudaError_t noalloc_prepare(int device);

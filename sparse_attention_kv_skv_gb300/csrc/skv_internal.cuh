@@ -94,6 +94,7 @@ cudaError_t launch_attend_q4(const Dev& d, const int32_t* req_ids, int B, const 
 // Once per context, on its device: the kernel's shared-memory attribute; *device_sms = the SM count.
 cudaError_t prepare_attend(int* device_sms);
 
+constexpr int64_t kMaxSelectTokens = (int64_t)1 << 30;  // of a request in skv_select (32-bit token arithmetic)
 // Rows to 4 bits and back (q4.cuh); n >= 1.
 constexpr int64_t kMaxPackRows = (int64_t)1 << 32;    // a pool holds fewer
 constexpr int64_t kMaxPackStride = (int64_t)1 << 24;  // bytes; keeps n * stride far inside 64 bits

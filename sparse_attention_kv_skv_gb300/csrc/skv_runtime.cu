@@ -464,6 +464,7 @@ skv_status skv_create(const skv_config* cfg, skv_ctx** out)
     SKV_TRY(skv::launch_init_lru_all(d, 0));
     SKV_TRY(skv::prepare_step_kernels(c.topk, c.hot_slots, &x->gather_grid));
     SKV_TRY(skv::prepare_attend(&x->device_sms));
+    SKV_TRY(skv::prepare_select());
     SKV_TRY(skv::noalloc_prepare(c.device));
     if (c.row_bytes == skv::q4::kRowBytes)  // skv_attend_q4 may be called on this context
         SKV_ALLOC(cudaMalloc(&x->q4_scratch, skv::attend_q4_scratch_bytes(x->device_sms)));
@@ -689,6 +690,64 @@ skv_status skv_unpack_rows(skv_ctx* ctx, const void* packed, int64_t n, void* va
     DeviceGuard g(ctx->cfg.device);
     if (!g.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
     SKV_CUDA(skv::launch_unpack_rows(packed, n, values, stream));
+    return SKV_OK;
+}
+
+}  // extern "C"
+
+namespace {
+// What skv_select and skv_select_workspace check alike.
+bool select_shape_ok(const skv_ctx* ctx, const skv_index* ix, int32_t B, int32_t layer)
+{
+    return ctx && ix && B >= 0 && B <= ctx->cfg.max_batch && layer >= -1 && layer < ctx->cfg.num_layers &&
+           ix->block >= 1 && ix->block <= ctx->cfg.topk && ctx->cfg.topk % ix->block == 0 &&
+           ctx->cfg.max_context <= skv::kMaxSelectTokens;
+}
+int64_t select_bytes(const skv_ctx* ctx, const skv_index* ix, int32_t B, int32_t layer)
+{
+    return (int64_t)B * (layer < 0 ? ctx->cfg.num_layers : 1) * skv::select_stride(ctx->cfg.max_context, ix->block) * 4;
+}
+// Strides of an axis are used only where it has more than one entry.
+bool select_stride_ok(int64_t stride, int64_t entries)
+{
+    return entries <= 1 || (stride > 0 && stride % 16 == 0 && stride < ((int64_t)1 << 40));
+}
+}  // namespace
+
+extern "C" {
+
+skv_status skv_select_workspace(skv_ctx* ctx, const skv_index* index, int32_t B, int32_t layer, int64_t* bytes)
+{
+    if (!select_shape_ok(ctx, index, B, layer) || !bytes) return SKV_ERR_INVALID_ARG;
+    *bytes = select_bytes(ctx, index, B, layer);
+    return SKV_OK;
+}
+
+skv_status skv_select(skv_ctx* ctx, const skv_index* index, const int32_t* req_ids_dev, int32_t B, int32_t layer,
+                      const void* q_dev, const float* w_dev, int32_t* topk_dev, void* workspace_dev,
+                      int64_t workspace_bytes, skv_stream_t stream)
+{
+    if (!select_shape_ok(ctx, index, B, layer)) return SKV_ERR_INVALID_ARG;
+    const skv_config& c = ctx->cfg;
+    const skv_index& ix = *index;
+    const int64_t keys = (c.max_context + ix.block - 1) / ix.block;
+    if (ix.heads < 1 || ix.heads > 64 || (ix.dim != 64 && ix.dim != 128) || ix.first < 0 || ix.last < 0 ||
+        (int64_t)ix.first + ix.last > c.topk / ix.block)
+        return SKV_ERR_INVALID_ARG;
+    if (B == 0) return SKV_OK;
+    if (!select_stride_ok(ix.key_stride, keys) || (keys > 1 && ix.key_stride < 2 * ix.dim) ||
+        !select_stride_ok(ix.layer_stride, c.num_layers) || !select_stride_ok(ix.request_stride, c.max_requests))
+        return SKV_ERR_INVALID_ARG;
+    if (!ix.keys || !req_ids_dev || !q_dev || !w_dev || !topk_dev || !workspace_dev ||
+        workspace_bytes < select_bytes(ctx, index, B, layer) ||
+        ((reinterpret_cast<uintptr_t>(ix.keys) | reinterpret_cast<uintptr_t>(q_dev) |
+          reinterpret_cast<uintptr_t>(workspace_dev)) & 15u))
+        return SKV_ERR_INVALID_ARG;
+    DeviceGuard g(c.device);
+    if (!g.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+    Dev d = ctx->d;
+    d.layer_sel = layer;
+    SKV_CUDA(skv::launch_select(d, ix, req_ids_dev, B, q_dev, w_dev, topk_dev, workspace_dev, ctx->device_sms, stream));
     return SKV_OK;
 }
 

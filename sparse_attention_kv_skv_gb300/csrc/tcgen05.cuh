@@ -262,6 +262,26 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const void* map, int x
         : "memory");
 }
 
+// One box of a 3-D or 4-D tensor map at the given coordinates (x innermost,
+// x times the element size a multiple of 16 bytes); what lies outside the
+// tensor reads zeros and still counts towards the bytes that complete on `bar`.
+__device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int x, int y, int z, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load4(uint32_t dst, const void* map, int x, int y, int z, int w, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // The same for 4 bytes, and for 16 bytes given as a uint4.
 __device__ __forceinline__ void st_async4(uint32_t remote_addr, float a, uint32_t remote_bar)
 {

@@ -48,6 +48,21 @@ class skv_config(ctypes.Structure):
     ]
 
 
+class skv_index(ctypes.Structure):
+    _fields_ = [
+        ("keys", ctypes.c_void_p),
+        ("request_stride", ctypes.c_int64),
+        ("layer_stride", ctypes.c_int64),
+        ("key_stride", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("block", ctypes.c_int32),
+        ("first", ctypes.c_int32),
+        ("last", ctypes.c_int32),
+        ("relu", ctypes.c_int32),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m sparse_attention_kv_skv_gb300.build` "
@@ -83,6 +98,8 @@ def _load():
         "skv_attend_q4": [vp, vp, i32, i32, vp, vp, vp, vp, ctypes.c_float, vp],
         "skv_pack_rows": [vp, vp, i64, i64, vp, vp, vp],
         "skv_unpack_rows": [vp, vp, i64, vp, vp],
+        "skv_select_workspace": [vp, P(skv_index), i32, i32, P(i64)],
+        "skv_select": [vp, P(skv_index), vp, i32, i32, vp, vp, vp, vp, i64, vp],
         "skv_pool_placement": [vp, P(i32), P(i32), P(ctypes.c_float)],
         "skv_host_node_for_pci": [ctypes.c_char_p, ctypes.c_char_p, P(i32)],
     }
@@ -124,6 +141,8 @@ skv_set_attend_sms = lib.skv_set_attend_sms
 skv_selftest_mma = lib.skv_selftest_mma
 skv_attend = lib.skv_attend
 skv_attend_q4 = lib.skv_attend_q4
+skv_select = lib.skv_select
+skv_select_workspace = lib.skv_select_workspace
 skv_pack_rows = lib.skv_pack_rows
 skv_unpack_rows = lib.skv_unpack_rows
 skv_selftest_attend_timeout = lib.skv_selftest_attend_timeout
@@ -195,6 +214,27 @@ class Config:
     def c(self) -> skv_config:
         return skv_config(self.max_requests, self.num_layers, self.max_context, self.row_bytes, self.topk,
                           self.hot_slots, self.max_batch, self.device)
+
+
+class Index:
+    """The index keys a Top-k is selected by: keys [R][L][n][dim] bf16 on the
+    device (any strides with adjacent dims; n >= ceil(max_context / block)), one
+    key for `block` tokens (see skv_index)."""
+
+    def __init__(self, keys, block: int = 1, first: int = 0, last: int = 0, relu: bool = True):
+        if keys.dim() != 4 or keys.stride(3) != 1 or keys.element_size() != 2 or not keys.is_floating_point():
+            raise ValueError("Index: keys must be [requests][layers][keys][dim] bf16 with adjacent values")
+        self.keys, self.block = keys, block
+        self._c = skv_index(keys.data_ptr(), 2 * keys.stride(0), 2 * keys.stride(1), 2 * keys.stride(2), 1, keys.shape[3],
+                            block, first, last, int(bool(relu)))
+
+    def c(self, heads: int = 1):
+        self._c.heads = heads
+        return ctypes.byref(self._c)
+
+    def fits(self, cfg: Config) -> bool:
+        n = self.keys.shape
+        return n[0] >= cfg.max_requests and n[1] >= cfg.num_layers and n[2] * self.block >= cfg.max_context
 
 
 class Context:
@@ -296,6 +336,30 @@ class Context:
         scale = (1.0 / 576 ** 0.5) if sm_scale is None else sm_scale
         check(skv_attend_q4(self.h, _ptr(req_ids), B, layer, _ptr(q), _ptr(slots), _ptr(out), _ptr(lse), scale,
                             _stream_handle(stream)), "skv_attend_q4")
+
+    def select_workspace(self, index: Index, B: int, layer: int = -1) -> int:
+        """Bytes of workspace a select() of B entries needs."""
+        n = ctypes.c_int64()
+        check(skv_select_workspace(self.h, index.c(), B, layer, ctypes.byref(n)), "skv_select_workspace")
+        return n.value
+
+    def select(self, index: Index, req_ids, q, w, topk, workspace, layer: int = -1, B: int | None = None,
+               stream=None) -> None:
+        """Select each unit's Top-k tokens by index scores (see skv_select):
+        q [units][heads][dim] bf16, w [units][heads] fp32 -> topk [units][k]
+        int32, ascending, -1 behind the last.  workspace: select_workspace() bytes."""
+        B = req_ids.numel() if B is None else B
+        heads, dim = q.shape[-2:]
+        units = B if layer >= 0 else B * self.cfg.num_layers
+        if not index.fits(self.cfg):
+            raise ValueError("select: the index has fewer requests, layers or keys than the context")
+        if dim != index.keys.shape[3]:
+            raise ValueError("select: q and the index keys differ in width")
+        _need(q, 2 * units * heads * dim, "select: q")
+        _need(w, 4 * units * heads, "select: w")
+        _need(topk, 4 * units * self.cfg.topk, "select: topk")
+        check(skv_select(self.h, index.c(heads), _ptr(req_ids), B, layer, _ptr(q), _ptr(w), _ptr(topk), _ptr(workspace),
+                         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "skv_select")
 
     def pack_rows(self, rows, packed, values=None, stream=None) -> None:
         """bf16 rows [n][576] (rows may lie apart: rows.stride(0)) -> packed rows
