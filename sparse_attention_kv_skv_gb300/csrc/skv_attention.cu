@@ -158,6 +158,7 @@ constexpr int kQKHalf = kDim / 2;                        // score dims per CTA (
 constexpr int kBlk = 64;         // keys per block (the N of S = Q K^T)
 constexpr int kHalfBlk = kBlk / 2;                       // keys of a block whose softmax this CTA finishes
 constexpr int kWinBoxes = 5;     // 64-dim column boxes of the key-row window a CTA loads (320 dims)
+constexpr int kRawStages = 2;    // raw stages of packed rows in flight
 constexpr int kMaxStages = 4;    // key stages in flight (3 when a long slot list needs the room)
 constexpr int kSoftmaxThreads = 128;                     // warpgroup 0: one head a thread
 constexpr int kXchgWarp0 = 4;                            // warpgroup 1: sends the peer its partial scores
@@ -186,12 +187,13 @@ struct alignas(16) AttnCtl;
 struct AttnLayout {
     int stages;
     uint32_t off_x, off_p, off_ctl, bytes;
+    uint32_t off_raw;  // packed rows: the raw stages
 };
 __host__ __device__ constexpr uint32_t attend_ctl_bytes();
-__host__ __device__ inline AttnLayout attend_layout()
+__host__ __device__ inline AttnLayout attend_layout(uint32_t raw_bytes = 0)
 {
     for (int st = kMaxStages;; --st) {
-        AttnLayout a{st, (uint32_t)st * kStageBytes, 0, 0, 0};
+        AttnLayout a{st, (uint32_t)st * kStageBytes + raw_bytes, 0, 0, 0, (uint32_t)st * kStageBytes};
         a.off_p = a.off_x + 2 * kXBytes;
         a.off_ctl = a.off_p + 2 * kPBytes;
         a.bytes = a.off_ctl + attend_ctl_bytes();
@@ -230,6 +232,8 @@ struct alignas(16) AttnCtl {
     uint64_t l_full;             // the peer's share of the softmax denominators has arrived (512 bytes; a phase a unit)
     uint64_t q_ready;            // a unit's Q is in tensor memory (a phase a unit)
     uint64_t o_free;             // the softmax has read a unit's accumulator out of tensor memory (a phase a unit)
+    uint64_t raw_full[kRawStages];   // packed rows: a raw stage has landed
+    uint64_t raw_empty[kRawStages];  // packed rows: a raw stage has been turned into a key stage
     uint64_t fin;                // every MMA this CTA issued has completed
     float mx[2][kHeads];         // [block parity][head] the peer's row maxima of the raw scores
     float lx[kHeads];            // [head] the peer's share of the denominator
@@ -307,100 +311,104 @@ struct KeySplit {
     float* lse;  // [units * n][128], log2 domain
 };
 
-constexpr int kPairChunks = 2;                              // 16-byte chunks of codes (32 dims each) a task takes of a row
-constexpr int kTaskRows = 32 / kPairChunks;                 // key rows a warp task covers
-constexpr int kTasks = kWinBoxes * (kBlk / kTaskRows);      // warp tasks a block (20): a 64-dim box of 16 rows each
-constexpr int kWarpTasks = (kTasks + kLoadWarps - 1) / kLoadWarps;
+// The loaders of packed rows.  One warp (the last of the seven) gathers a block's
+// rows as they are, 336 bytes each, into a ring of raw stages with TMA
+// (tile::gather4, lane j the rows 4j..4j+3; a masked slot is an out-of-range row,
+// which reads as zeros, and so are its values); the other six turn a raw stage
+// into a key stage.  A block is 20 tasks of 16 rows by one 64-dim box of this
+// CTA's window: lane 2j + c takes 32 dims (16 bytes of codes, two scales) of
+// row j and writes them where the swizzle puts them -- a quarter warp writes
+// four rows by both halves of a 128-byte line, which the swizzle spreads over
+// all banks.  (Plain loads instead of the raw ring: 1.79 ms at 192 x 8 units of
+// 2048 keys against the ring's; the scattered 16-byte loads of a block need more lines in
+// flight than the L1 that 227 KB of shared memory leaves, and more blocks in
+// flight make it worse.)
+constexpr int kConvWarps = kLoadWarps - 1;
+constexpr uint32_t kRawGroup = 4 * q4::kRowBytes;                      // bytes of one gather
+constexpr uint32_t kRawGroupStride = (kRawGroup + 127u) / 128u * 128u; // a TMA destination is 128-byte aligned
+constexpr uint32_t kRawBytes = kBlk / 4 * kRawGroupStride;             // a raw stage: 22528
+constexpr int kTaskRows = 16;
+constexpr int kTasks = kWinBoxes * (kBlk / kTaskRows);                 // warp tasks a block (20)
 
-// The loaders of packed rows: per key block, 20 tasks of 16 rows by one 64-dim
-// box of this CTA's window, spread over the seven warps.  Lane 2j + c reads 16
-// bytes of codes (32 dims) of row j, its two scales and the row's exponent,
-// and writes the 32 bf16 values where the swizzle puts them: a quarter warp
-// writes four rows by both halves of a 128-byte line, which the swizzle spreads
-// over all banks.  The slots of a block are fetched two blocks ahead and its
-// rows one block ahead (they are in flight while the previous block waits for
-// its stage and is written).  next_req(u) is the request of unit u or -1.
+// Both roles; returns false if a wait gave up.  req_of(u, b, l): the request of unit u or -1.
 template <typename ReqOf>
-__device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const Dev& d, const int32_t* __restrict__ slots,
-                                                 const KeySplit& sp, uint8_t* sK, int nst, int gtot, int cl, int ncl,
-                                                 int h, int lw, int lane, const volatile uint32_t* abort, ReqOf req_of)
+__device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* hot_map, const Dev& d,
+                                                 const int32_t* __restrict__ slots, const KeySplit& sp, uint8_t* sK,
+                                                 uint8_t* sRaw, int nst, int gtot, int units, int cl, int ncl, int h,
+                                                 int lw, int lane, const volatile uint32_t* abort, ReqOf req_of)
 {
-    struct Slots {
-        int32_t a, b;  // slots of keys `lane` and 32 + `lane` of the block, -1 masked
-        int64_t row0;  // the unit's first hot row
-    };
-    struct Rows {
-        uint4 codes[kWarpTasks];
-        uint32_t meta[kWarpTasks];  // two scales, then the exponent byte
-    };
-    int u = cl - ncl, i = sp.blocks - 1;  // the block before the first
-    int key0 = 0;
-    int64_t row0 = 0;
-    const int32_t* sl = slots;
-    auto fetch = [&]() -> Slots {  // the next block's slots; called gtot times at most
-        if (++i == sp.blocks) {
+    if (lw == kConvWarps) {
+        int g = 0;
+        bool ok = true;
+        for (int u = cl; ok && u < units; u += ncl) {
             int b, l;
-            int32_t r;
-            do {
-                u += ncl;
-                r = req_of(u, b, l);
-            } while (r < 0);
-            i = 0;
-            row0 = ((int64_t)r * d.L + l) * d.S;
-            sl = slots + (size_t)(u / sp.n) * d.k;
-            key0 = (u % sp.n) * sp.blocks * kBlk;
-        }
-        const int key = key0 + i * kBlk + lane;
-        const int32_t a = key < d.k ? sl[key] : -1, b = key + 32 < d.k ? sl[key + 32] : -1;
-        return Slots{a >= 0 && a < d.S ? a : -1, b >= 0 && b < d.S ? b : -1, row0};
-    };
-    auto request = [&](const Slots& s, Rows& w) {
+            const int32_t r = req_of(u, b, l);
+            if (r < 0) continue;
+            const int64_t row0 = ((int64_t)r * d.L + l) * d.S;  // the unit's first hot row
+            const int32_t* sl = slots + (size_t)(u / sp.n) * d.k;
+            const int key0 = (u % sp.n) * sp.blocks * kBlk;
+            auto fetch = [&](int i, int half) -> int32_t {
+                const int key = key0 + i * kBlk + 32 * half + lane;
+                const int32_t slot = key < d.k ? sl[key] : -1;
+                return slot >= 0 && slot < d.S ? slot : -1;
+            };
+            int32_t v0 = fetch(0, 0), v1 = fetch(0, 1);
+            for (int i = 0; i < sp.blocks; ++i, ++g) {
+                const int st = g % kRawStages;
+                const int32_t n0 = i + 1 < sp.blocks ? fetch(i + 1, 0) : -1, n1 = i + 1 < sp.blocks ? fetch(i + 1, 1) : -1;
+                if (g >= kRawStages &&
+                    !(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.raw_empty[st], ((g / kRawStages) - 1) & 1, abort))))
+                    break;
+                if (lane == 0) tc::mbar_arrive_expect_tx(&c.raw_full[st], kBlk / 4 * kRawGroup);
+                __syncwarp();
+                int rr[4];
 #pragma unroll
-        for (int x = 0; x < kWarpTasks; ++x) {
-            const int task = lw + kLoadWarps * x;
-            if (task < kTasks) {
-                const int rg = task & 3, chunk = 8 * h + kPairChunks * (task >> 2) + (lane & 1);
-                const int32_t slot = __shfl_sync(0xFFFFFFFFu, rg < 2 ? s.a : s.b, (kTaskRows * rg + (lane >> 1)) & 31);
-                w.codes[x] = make_uint4(0, 0, 0, 0);
-                w.meta[x] = 0u;  // a masked key reads as zeros
-                if (slot >= 0) {
-                    const uint8_t* p = d.hot + (size_t)(s.row0 + slot) * q4::kRowBytes;
-                    w.codes[x] = __ldg(reinterpret_cast<const uint4*>(p) + chunk);
-                    w.meta[x] = __ldg(reinterpret_cast<const uint16_t*>(p + q4::kScalesAt) + chunk) |
-                                (uint32_t)__ldg(p + q4::kExpAt) << 16;
+                for (int x = 0; x < 4; ++x) {
+                    const int j = (4 * lane + x) & (kBlk - 1);  // lanes 16..31 gather nothing
+                    const int32_t a = __shfl_sync(0xFFFFFFFFu, v0, j & 31), b2 = __shfl_sync(0xFFFFFFFFu, v1, j & 31);
+                    const int32_t slot = j < 32 ? a : b2;
+                    rr[x] = slot >= 0 ? (int)(row0 + slot) : -1;
                 }
+                if (lane < kBlk / 4)
+                    tc::tma_gather4(tc::smem_u32(sRaw + st * kRawBytes) + lane * kRawGroupStride, hot_map, 0, rr[0], rr[1],
+                                    rr[2], rr[3], &c.raw_full[st]);
+                v0 = n0;
+                v1 = n1;
             }
         }
-    };
-    Rows cur, nxt;
-    Slots s{-1, -1, 0};
-    if (gtot > 0) request(fetch(), cur);
-    if (gtot > 1) s = fetch();
+        if (!ok && lane == 0)  // no copy may still be landing when the CTA leaves
+            for (int i = max(0, g - kRawStages); i < g; ++i)
+                tc::mbar_wait(&c.raw_full[i % kRawStages], (uint32_t)(i / kRawStages) & 1u, kMaxPolls);
+        __syncwarp();
+        return ok;
+    }
     for (int g = 0; g < gtot; ++g) {
-        if (g + 1 < gtot) request(s, nxt);
-        if (g + 2 < gtot) s = fetch();
-        const int st = g % nst;
+        const int st = g % nst, rs = g % kRawStages;
         if (g >= nst && !__all_sync(0xFFFFFFFFu, wait_phase(&c.empty[st], ((g / nst) - 1) & 1, abort))) return false;
+        if (!__all_sync(0xFFFFFFFFu, wait_phase(&c.raw_full[rs], (g / kRawStages) & 1, abort))) return false;
         uint8_t* stage = sK + st * kStageBytes;
+        const uint8_t* raw = sRaw + rs * kRawBytes;
+        for (int task = lw; task < kTasks; task += kConvWarps) {
+            const int row = kTaskRows * (task & 3) + (lane >> 1), box = task >> 2;
+            const int chunk = 8 * h + 2 * box + (lane & 1);  // of 32 dims, in the row
+            const uint8_t* p = raw + (row >> 2) * kRawGroupStride + (row & 3) * q4::kRowBytes;
+            const uint4 codes = *reinterpret_cast<const uint4*>(p + 16 * chunk);
+            const uint32_t scales = *reinterpret_cast<const uint16_t*>(p + q4::kScalesAt + 2 * chunk);
+            const uint32_t eb = p[q4::kExpAt];
+            const uint32_t f0 = q4::group_factor(scales & 0xFFu, eb), f1 = q4::group_factor(scales >> 8, eb);
+            const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+            uint8_t* line = stage + box * kBoxBytes + row * 128;
 #pragma unroll
-        for (int x = 0; x < kWarpTasks; ++x) {
-            const int task = lw + kLoadWarps * x;
-            if (task < kTasks) {
-                const int row = kTaskRows * (task & 3) + (lane >> 1);
-                uint8_t* line = stage + (task >> 2) * kBoxBytes + row * 128;
-                const uint32_t f0 = q4::group_factor(cur.meta[x] & 0xFFu, cur.meta[x] >> 16);
-                const uint32_t f1 = q4::group_factor((cur.meta[x] >> 8) & 0xFFu, cur.meta[x] >> 16);
-                const uint32_t w[4] = {cur.codes[x].x, cur.codes[x].y, cur.codes[x].z, cur.codes[x].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4*>(line + (((4 * (lane & 1) + j) ^ (row & 7)) << 4)) =
-                        q4::decode8(w[j], j < 2 ? f0 : f1);
-            }
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(line + (((4 * (lane & 1) + j) ^ (row & 7)) << 4)) =
+                    q4::decode8(w[j], j < 2 ? f0 : f1);
         }
         tc::fence_smem_async();  // the tensor core reads the stage
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&c.full[st]);
-        cur = nxt;
+        if (lane == 0) {
+            tc::mbar_arrive(&c.full[st]);
+            tc::mbar_arrive(&c.raw_empty[rs]);
+        }
     }
     return true;
 }
@@ -447,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 
     if (tid == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
-            tc::mbar_init(&c.full[s], kLoadWarps);
+            tc::mbar_init(&c.full[s], kQ4 ? kConvWarps : kLoadWarps);
             tc::mbar_init(&c.empty[s], 1);
         }
         tc::mbar_init(&c.s_full, 1);
@@ -458,6 +466,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             tc::mbar_init(&c.m_full[i], 1);
             tc::mbar_init(&c.p_full[i], kSoftmaxThreads);  // my half (one of them with expect_tx) + the peer's bytes
             tc::mbar_init(&c.pv_done[i], 1);
+        }
+        if constexpr (kQ4) {
+            for (int i = 0; i < kRawStages; ++i) {
+                tc::mbar_init(&c.raw_full[i], 1);
+                tc::mbar_init(&c.raw_empty[i], kConvWarps);
+            }
         }
         tc::mbar_init(&c.l_full, 1);
         tc::mbar_init(&c.q_ready, kSoftmaxThreads);  // the exchange warpgroup writes Q
@@ -477,8 +491,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         tc::regs_shrink<kServiceRegs>();
         if (kQ4 && warp >= kLoadWarp0) {
             if constexpr (kQ4) {
-                const bool ok = load_packed_keys(c, d, slots, ks, sK, nst, gtot, cl, ncl, (int)h, warp - kLoadWarp0, lane,
-                                                 abort, req_of);
+                const bool ok = load_packed_keys(c, &hot_map, d, slots, ks, sK, smem + lay.off_raw, nst, gtot, units, cl, ncl,
+                                                 (int)h, warp - kLoadWarp0, lane, abort, req_of);
                 if (!ok && lane == 0) give_up(c, &d.ctl[CTL_ERR]);
                 __syncwarp();
             }
@@ -965,21 +979,24 @@ cudaError_t tensor_map_encoder(TensorMapEncoder* encode)
     return cudaSuccess;
 }
 
-// The hot buffer as a 2-D tensor of R*L*S rows by 576 bf16 (row stride 1152
-// bytes) for TMA: box one row by 64 columns, 128-byte swizzle, out-of-range
-// rows read as zeros.
+// The hot buffer as a 2-D tensor of R*L*S rows for TMA, out-of-range rows read
+// as zeros: rows of 576 bf16, box one row by 64 columns, 128-byte swizzle; or
+// packed rows of 336 bytes (as 168 16-bit words), box one whole row.
 cudaError_t encode_hot_map(const Dev& d, CUtensorMap* map)
 {
     const uint64_t rows = (uint64_t)d.R * (uint64_t)d.L * (uint64_t)d.S;
-    if (rows > 0x7FFFFFFFull || d.row_bytes != kRowBytes) return cudaErrorInvalidValue;
+    const bool packed = d.row_bytes == q4::kRowBytes;
+    if (rows > 0x7FFFFFFFull || (d.row_bytes != kRowBytes && !packed)) return cudaErrorInvalidValue;
     TensorMapEncoder encode = nullptr;
     const cudaError_t e = tensor_map_encoder(&encode);
     if (e != cudaSuccess) return e;
-    const cuuint64_t dims[2] = {(cuuint64_t)kDim, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)kRowBytes};
-    const cuuint32_t box[2] = {64, 1}, elem_strides[2] = {1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d.hot, dims, strides, box, elem_strides,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t dims[2] = {(cuuint64_t)(d.row_bytes / 2), (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)d.row_bytes};
+    const cuuint32_t box[2] = {packed ? (cuuint32_t)q4::kRowBytes / 2 : 64u, 1}, elem_strides[2] = {1, 1};
+    const CUresult r = encode(map, packed ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d.hot, dims, strides, box, elem_strides,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              packed ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -1017,10 +1034,10 @@ size_t attend_q4_scratch_bytes(int device_sms)
     return (size_t)std::max(1, device_sms / 2) * (512 + 1) * kHeads * sizeof(float);
 }
 
-cudaError_t launch_attend_q4(const Dev& d, const int32_t* req_ids, int B, const void* q, const int32_t* slots, void* out,
+cudaError_t launch_attend_q4(const void* hot_map, const Dev& d, const int32_t* req_ids, int B, const void* q, const int32_t* slots, void* out,
                              float* lse, float sm_scale, float* scratch, int max_sms, int device_sms, cudaStream_t st)
 {
-    const AttnLayout lay = attend_layout();
+    const AttnLayout lay = attend_layout(kRawStages * kRawBytes);
     if (d.k > (int)kMaxTopk || lay.bytes > kSmemLimit || device_sms < 2) return cudaErrorInvalidValue;
     const int units = call_units(d, B);
     const int use_sms = max_sms > 0 ? std::min(max_sms, device_sms) : device_sms;
@@ -1038,7 +1055,7 @@ cudaError_t launch_attend_q4(const Dev& d, const int32_t* req_ids, int B, const 
     }
     const int clusters = std::min(units * sp.n, pairs);
     attend_kernel<true><<<clusters * 2, kAttnThreads, lay.bytes, st>>>(
-        CUtensorMap{}, d, req_ids, static_cast<const uint16_t*>(q), slots, static_cast<uint16_t*>(out), lse,
+        *static_cast<const CUtensorMap*>(hot_map), d, req_ids, static_cast<const uint16_t*>(q), slots, static_cast<uint16_t*>(out), lse,
         sm_scale * 1.4426950408889634f, lay, units * sp.n, 0, sp);
     if (sp.n > 1) combine_kernel<<<dim3(512 / kJoinCols, units), kHeads, 0, st>>>(sp, static_cast<uint16_t*>(out), lse);
     return cudaGetLastError();
@@ -1063,14 +1080,14 @@ skv_status attend_impl(skv_ctx* ctx, const int32_t* req_ids_dev, int32_t B, int3
     if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
     if (prev != ctx->cfg.device && cudaSetDevice(ctx->cfg.device) != cudaSuccess) return SKV_ERR_CUDA;
     cudaError_t e = cudaSuccess;
-    if (!q4 && !ctx->hot_map_ready) {  // host-side encoding only: safe while a stream is being captured
+    if (!ctx->hot_map_ready) {  // host-side encoding only: safe while a stream is being captured
         e = skv::encode_hot_map(ctx->d, &ctx->hot_map);
         ctx->hot_map_ready = e == cudaSuccess;
     }
     skv::Dev d = ctx->d;
     d.layer_sel = layer;
-    if (q4)
-        e = skv::launch_attend_q4(d, req_ids_dev, B, q_dev, slots_dev, out_dev, lse_dev, sm_scale, ctx->q4_scratch,
+    if (e == cudaSuccess && q4)
+        e = skv::launch_attend_q4(&ctx->hot_map, d, req_ids_dev, B, q_dev, slots_dev, out_dev, lse_dev, sm_scale, ctx->q4_scratch,
                                   ctx->attend_sms, ctx->device_sms, stream);
     else if (e == cudaSuccess)
         e = skv::launch_attend(&ctx->hot_map, d, req_ids_dev, B, q_dev, slots_dev, out_dev, lse_dev, sm_scale,
