@@ -178,6 +178,11 @@ constexpr uint32_t kSmemLimit = 227 * 1024;              // dynamic shared memor
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;  // O 256, S 64, Q 144 columns
 constexpr float kRescaleLog2 = 8.0f;                     // lazy rescale threshold (factor 256)
+// The same for packed rows.  P is bf16 and the sums are fp32, so a stale reference costs range, not
+// precision: with 2^24, sums of up to 4096 keys stay finite for values below 2^91.  A rescale moves the
+// whole accumulator through registers; at 192 x 8 units of 2048 keys with scores of 6 standard deviations in
+// log2, the threshold 8 costs 1.37 ms, 24 1.22 ms.
+constexpr float kRescaleLog2Q4 = 24.0f;
 static_assert(kColQ + kQKHalf / 2 <= kTmemCols && kColS + kBlk <= kColQ, "tensor-memory columns");
 
 struct alignas(16) AttnCtl;
@@ -484,6 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     tc::cluster_sync();  // barriers of both CTAs exist before either sends to the other
     tc::fence_after_sync();
     const uint32_t tbase = c.tmem_base;
+    if constexpr (kQ4) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // combine_kernel, if any
     // Register split (warpgroup-wide): softmax 192 a thread, exchange 72, MMA and loaders 88; the
     // shares fit the launch's 512 x 128 in total and on every SM sub-partition (one warp of each
     // warpgroup per sub-partition).
@@ -792,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 const float mb = fmaxf(mloc, c.mx[bb][hd]) * scale_log2;  // the same in both CTAs
                 tc::mbar_arrive(&c.adv[bb]);  // the exchange warpgroup may now send block g + 2
                 float factor = 1.0f;
-                if (mb > m_ref + kRescaleLog2) {
+                if (mb > m_ref + (kQ4 ? kRescaleLog2Q4 : kRescaleLog2)) {
                     factor = m_ref == -INFINITY ? 0.0f : ex2(m_ref - mb);
                     m_ref = mb;
                     l_run *= factor;
@@ -930,31 +936,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 }
 
 // The results of a unit's splits joined: with lse_i the splits' log2 sums and
-// M their maximum, out = sum 2^(lse_i - M) o_i / sum 2^(lse_i - M).  One CTA per
-// unit and 8 value columns, one thread per head; a split without a single key
-// (lse -inf) is skipped.
-constexpr int kJoinCols = 8;
-__global__ void __launch_bounds__(kHeads) combine_kernel(KeySplit sp, uint16_t* __restrict__ out, float* __restrict__ lse)
+// M their maximum, out = sum 2^(lse_i - M) o_i / sum 2^(lse_i - M); a split without
+// a single key (lse -inf) is skipped.  One CTA per unit and kCols value columns;
+// thread (t, g) <-> head t and every kShares-th split, the shares summed through
+// shared memory in a fixed order.  Bound by latency: the loads of all of a
+// thread's splits are in flight at once.
+template <int kShares, int kCols>
+__global__ void __launch_bounds__(kHeads * kShares) combine_kernel(KeySplit sp, uint16_t* __restrict__ out,
+                                                                   float* __restrict__ lse)
 {
-    const int u = blockIdx.y, c0 = blockIdx.x * kJoinCols, hd = threadIdx.x;
+    __shared__ float peak[kShares][kHeads], sum[kShares][kCols + 1][kHeads];
+    const int u = blockIdx.y, c0 = blockIdx.x * kCols, hd = threadIdx.x % kHeads, g = threadIdx.x / kHeads;
     const float* ls = sp.lse + (size_t)u * sp.n * kHeads + hd;
     const float* po = sp.o + ((size_t)u * sp.n * 512 + c0) * kHeads + hd;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the splits' kernel has finished
     float m = -INFINITY;
-    for (int i = 0; i < sp.n; ++i) m = fmaxf(m, ls[(size_t)i * kHeads]);
-    float acc[kJoinCols] = {}, total = 0.0f;
-#pragma unroll 2
-    for (int i = 0; i < sp.n; ++i) {
+#pragma unroll 4
+    for (int i = g; i < sp.n; i += kShares) m = fmaxf(m, ls[(size_t)i * kHeads]);
+    if constexpr (kShares > 1) {
+        peak[g][hd] = m;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kShares; ++x) m = fmaxf(m, peak[x][hd]);
+    }
+    float acc[kCols] = {}, total = 0.0f;
+#pragma unroll 4
+    for (int i = g; i < sp.n; i += kShares) {
         const float li = ls[(size_t)i * kHeads];
-        if (li == -INFINITY) continue;
-        const float w = ex2(li - m);
+        float o[kCols];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) o[j] = po[((size_t)i * 512 + j) * kHeads];
+        const bool none = li == -INFINITY;  // its o was never written
+        const float w = none ? 0.0f : ex2(li - m);
         total += w;
 #pragma unroll
-        for (int j = 0; j < kJoinCols; ++j) acc[j] = fmaf(w, po[((size_t)i * 512 + j) * kHeads], acc[j]);
+        for (int j = 0; j < kCols; ++j) acc[j] = fmaf(w, none ? 0.0f : o[j], acc[j]);
+    }
+    if constexpr (kShares > 1) {
+        sum[g][kCols][hd] = total;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) sum[g][j][hd] = acc[j];
+        __syncthreads();
+        if (g != 0) return;
+#pragma unroll
+        for (int x = 1; x < kShares; ++x) {
+            total += sum[x][kCols][hd];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) acc[j] += sum[x][j][hd];
+        }
     }
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    *reinterpret_cast<uint4*>(out + ((size_t)u * kHeads + hd) * 512 + c0) =
-        make_uint4(bf2(acc[0] * inv, acc[1] * inv), bf2(acc[2] * inv, acc[3] * inv), bf2(acc[4] * inv, acc[5] * inv),
-                   bf2(acc[6] * inv, acc[7] * inv));
+    uint16_t* o = out + ((size_t)u * kHeads + hd) * 512 + c0;
+#pragma unroll
+    for (int j = 0; j < kCols; j += 4)
+        *reinterpret_cast<uint2*>(o + j) = make_uint2(bf2(acc[j] * inv, acc[j + 1] * inv), bf2(acc[j + 2] * inv, acc[j + 3] * inv));
     if (blockIdx.x == 0 && lse)
         lse[(size_t)u * kHeads + hd] = total == 0.0f ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
 }
@@ -1057,8 +1092,21 @@ cudaError_t launch_attend_q4(const void* hot_map, const Dev& d, const int32_t* r
     attend_kernel<true><<<clusters * 2, kAttnThreads, lay.bytes, st>>>(
         *static_cast<const CUtensorMap*>(hot_map), d, req_ids, static_cast<const uint16_t*>(q), slots, static_cast<uint16_t*>(out), lse,
         sm_scale * 1.4426950408889634f, lay, units * sp.n, 0, sp);
-    if (sp.n > 1) combine_kernel<<<dim3(512 / kJoinCols, units), kHeads, 0, st>>>(sp, static_cast<uint16_t*>(out), lse);
-    return cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || sp.n == 1) return e;
+    // launched while the splits' kernel runs (every CTA of it lets it, once it is set up) and waits for its end
+    cudaLaunchConfig_t cfg{};
+    // many splits: a thread for every fourth of them and 4 columns; few: all of them and 8 columns a thread
+    const bool many = sp.n > 8;
+    cfg.gridDim = dim3(many ? 512 / 4 : 512 / 8, (unsigned)units);
+    cfg.blockDim = dim3(many ? kHeads * 4 : kHeads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, many ? combine_kernel<4, 4> : combine_kernel<1, 8>, sp, static_cast<uint16_t*>(out), lse);
 }
 
 }  // namespace skv

@@ -300,13 +300,16 @@ def test_masked_rows_and_rows_behind_the_selection_are_not_read():
     c.ctx.close()
 
 
-def test_attention_equals_skv_attend_over_the_unpacked_rows():
-    """The same values as bf16 rows in another context: skv_attend and skv_attend_q4 agree bit for bit when no unit is
-    split (the same products in the same order)."""
-    c = Cache(80, 1, 300, 256, seed=17)
+@pytest.mark.parametrize("k", [64, 256])
+def test_attention_equals_skv_attend_over_the_unpacked_rows(k):
+    """The same values as bf16 rows in another context.  One block of keys: the same products against the same reference
+    maximum, so skv_attend and skv_attend_q4 agree bit for bit.  More blocks: the two raise their reference at different
+    thresholds, so P is rounded on another scale; each is within the derived bounds of the same value, so they differ by
+    at most twice those."""
+    c = Cache(80, 1, 300, k, seed=17)
     rows = torch.empty((80 * 300, 576), dtype=torch.bfloat16, device="cuda")
     c.ctx.unpack_rows(torch.from_numpy(c.packed.reshape(-1, ROW)).cuda(), rows)
-    with _ctx(80, 1, 300, 256, 256, 80, row_bytes=1152) as wide:
+    with _ctx(80, 1, 300, k, k, 80, row_bytes=1152) as wide:
         for r in range(80):
             wide.publish(300, rows=rows[300 * r:300 * (r + 1)])
         slots = torch.empty_like(c.slots)
@@ -317,7 +320,11 @@ def test_attention_equals_skv_attend_over_the_unpacked_rows():
         b, lb = _outputs(80)
         wide.attend(c.req_dev, c.q_dev, slots, a, la, sm_scale=0.2)
         c.ctx.attend_q4(c.req_dev, c.q_dev, c.slots, b, lb, sm_scale=0.2)
-        assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(la, lb)
+        if k == 64:
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(la, lb)
+        else:
+            c.check(a, la, 0.2)
+            c.check(b, lb, 0.2)
     c.ctx.close()
 
 
