@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const uint32_t q_box = sh.npad * 128u, q_bytes = kBoxes * q_box;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // pick_kernel, which waits for this kernel's end
     // the call's entries: every id an active request; how many tiles each has
     const int per = (sh.B + kScoreThreads - 1) / kScoreThreads;
     const int b0 = min(sh.B, tid * per), b1 = min(sh.B, b0 + per);
@@ -363,12 +364,22 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 // ---------------------------------------------------------------------------
 constexpr int kPickThreads = 1024;
 constexpr int kBins = 2048;            // two a thread
-constexpr int kStagedKeys = 24576;     // scores a CTA keeps in shared memory (96 KB: two CTAs a SM)
+constexpr int kStagedKeys = 20480;     // scores a CTA keeps in shared memory (80 KB: two CTAs a SM)
+constexpr int kWindowKeys = 262144;    // scores whose bits fit the same room when the scores stay in L2
+constexpr int kFew = 1024;             // scores that are ranked directly
+// Dynamic shared memory: the scores and two bits each, or the bits of a window alone.
+constexpr size_t kPickSmem = (size_t)kStagedKeys * 4 + kStagedKeys / 4;
+static_assert(kWindowKeys / 4 <= (int)kPickSmem, "a window's bits fit");
+constexpr int kSample = 8;             // scores a thread samples of a long context
 
 struct PickCtl {
     uint32_t hist[kBins];
+    uint32_t few[kFew];                // the scores of the threshold's bin: this CTA's,
+    uint32_t pool[kFew];               // and the team's
+    uint32_t few_n;
     uint32_t lo, hi;                   // this CTA's range of scores
     uint32_t bin, need, count;         // the threshold's bin, what is still to take from it, what it holds
+    uint32_t edge[2];                  // a bracket of the threshold, from a sample
     uint32_t above, ties;              // this CTA's scores above the threshold, and at it
     uint32_t warp_a[32], warp_b[32];
 };
@@ -396,7 +407,7 @@ __device__ __forceinline__ uint32_t team_load(const uint32_t* p, uint32_t rank)
         return *p;
 }
 
-// f(index, score) for this CTA's scores, four a thread at a time.
+// f(score) for the m scores at s, four a thread at a time.
 template <typename F>
 __device__ __forceinline__ void each_score(const uint32_t* s, int m, F f)
 {
@@ -404,23 +415,44 @@ __device__ __forceinline__ void each_score(const uint32_t* s, int m, F f)
 #pragma unroll 4
     for (int i = threadIdx.x; i < m4; i += kPickThreads) {
         const uint4 v = reinterpret_cast<const uint4*>(s)[i];
-        f(4 * i, v.x);
-        f(4 * i + 1, v.y);
-        f(4 * i + 2, v.z);
-        f(4 * i + 3, v.w);
+        f(v.x);
+        f(v.y);
+        f(v.z);
+        f(v.w);
     }
     const int i = 4 * m4 + threadIdx.x;
-    if (i < m) f(i, s[i]);
+    if (i < m) f(s[i]);
+}
+
+// Inclusive sum over the CTA's threads, in thread order; `all` receives the total.
+__device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* warp_sum, uint32_t* all)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += x;
+    }
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    const uint32_t w = warp_sum[lane];
+    if (all) *all = __reduce_add_sync(0xFFFFFFFFu, w);
+    return v + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u);
 }
 
 // One team (a CTA, or a cluster of kC that share the scores of a long context)
 // a unit.  The threshold -- the score of the last block taken -- is found by
 // narrowing its range: histogram 2048 equal parts of the range, find the part in
-// which the count from above passes k / block, go on inside it; at most three
-// times for 32 bits, mostly twice (the parts divide the range the scores really
-// span, so they spread over the bins and few atomics meet).  Then each warp
-// counts what it takes of its stretch of keys, and after a scan of the counts
-// the stretches are written side by side: ascending, with no sort.
+// which the count from above passes k / block, and go on inside it until it holds so few
+// scores that they are ranked directly.  The first range is that of the scores
+// themselves, so they spread over the bins and few atomics meet, and the first
+// histogram is mostly the only one.  A context too long for shared memory is
+// read from L2 in each pass; there the first range is a bracket of the threshold
+// taken from a sample, so no pass is spent on the extremes and only the
+// scores inside the bracket are counted (a bracket that misses is noticed by its
+// counts and replaced by the whole range).  With the threshold known, one bit a
+// score says what is taken, a scan of the words' counts gives each word its place,
+// and the tokens come out ascending without a sort.
 template <int kC>
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t* __restrict__ req_ids, SelectShape sh,
                                                             const uint32_t* __restrict__ scores, int staged,
@@ -428,14 +460,15 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
 {
     extern __shared__ __align__(16) uint32_t kept[];
     __shared__ PickCtl c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int u = blockIdx.x / kC, rank = blockIdx.x % kC;
     int32_t* out = topk + (size_t)u * d.k;
+    const int32_t r = req_ids[u / sh.layers];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores (and the error word) are complete
     if (d.ctl[CTL_ERR] != 0u) {  // the same for every CTA: nothing writes the word during this kernel
         for (int i = rank * kPickThreads + tid; i < d.k; i += kC * kPickThreads) out[i] = -1;
         return;
     }
-    const int32_t r = req_ids[u / sh.layers];
     const int len = (int)d.len[r], n = keys_of(d, r, sh.block), nb = d.k / sh.block;
     if (n <= nb) {  // everything there is
         for (int i = rank * kPickThreads + tid; i < d.k; i += kC * kPickThreads) out[i] = i < len ? i : -1;
@@ -449,9 +482,16 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
         c.hi = 0u;
         c.above = c.ties = 0u;
     }
+    for (int i = tid; i < kBins; i += kPickThreads) c.hist[i] = 0u;
     __syncthreads();
-    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-    if (chunk <= staged) {
+
+    // the first range
+    uint32_t lo = 0xFFFFFFFFu, hi = 0u, seen[kSample];
+    const bool on_chip = chunk <= staged;
+    // a bit a score: above the threshold; at it (where not all of those are taken)
+    uint32_t* taken = on_chip ? kept + chunk : kept;
+    uint32_t* equal = taken + (on_chip ? chunk : kWindowKeys) / 32;
+    if (on_chip) {
         const int m4 = m >> 2;
 #pragma unroll 4
         for (int i = tid; i < m4; i += kPickThreads) {
@@ -468,11 +508,14 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
             hi = max(hi, v);
         }
         s = kept;
-    } else {
-        each_score(s, m, [&](int, uint32_t v) {
-            lo = min(lo, v);
-            hi = max(hi, v);
-        });
+    } else {  // evenly spaced scores of different keys (each CTA of the team has more than kSample * kPickThreads)
+        const int step = m / (kSample * kPickThreads);
+#pragma unroll
+        for (int j = 0; j < kSample; ++j) {
+            seen[j] = s[(size_t)(j * kPickThreads + tid) * step];
+            lo = min(lo, seen[j]);
+            hi = max(hi, seen[j]);
+        }
     }
     lo = __reduce_min_sync(0xFFFFFFFFu, lo);
     hi = __reduce_max_sync(0xFFFFFFFFu, hi);
@@ -487,37 +530,75 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
         lo = min(lo, team_load<kC>(&c.lo, p));
         hi = max(hi, team_load<kC>(&c.hi, p));
     }
-
-    uint32_t need = (uint32_t)nb;  // blocks still to take from [lo, hi]; every score above hi is taken
-    bool all = false;              // the whole range is taken
-    for (;;) {
-        const int bits = 32 - __clz(hi - lo);  // 0 for a single value
-        if (bits == 0) break;
-        const int shift = bits > 11 ? bits - 11 : 0;
-        for (int i = tid; i < kBins; i += kPickThreads) c.hist[i] = 0u;
-        __syncthreads();
-        each_score(s, m, [&](int, uint32_t v) {
-            if (v >= lo && v <= hi) atomicAdd(&c.hist[(v - lo) >> shift], 1u);
-        });
+    // thread t looks after the bins 2047 - 2t and 2046 - 2t: counts of the team, and a running count from the top
+    uint32_t h1, h0, before, total;
+    const int top = kBins - 1 - 2 * tid;
+    auto count_bins = [&]() {
         team_sync<kC>();
-        // thread t holds the bins 2047 - 2t and 2046 - 2t: a running count from the top
-        const int top = kBins - 1 - 2 * tid;
-        uint32_t h1 = 0, h0 = 0;
+        h1 = h0 = 0;
         for (int p = 0; p < kC; ++p) {
             h1 += team_load<kC>(&c.hist[top], p);
             h0 += team_load<kC>(&c.hist[top - 1], p);
         }
-        uint32_t run = h1 + h0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, run, o);
-            if (lane >= o) run += v;
-        }
-        if (lane == 31) c.warp_a[warp] = run;
+        before = cta_scan(h1 + h0, c.warp_a, &total) - h1 - h0;
+    };
+    auto clear_bins = [&]() {
+        team_sync<kC>();  // the peers have read this histogram, too
+        c.hist[top] = c.hist[top - 1] = 0u;
         __syncthreads();
-        uint32_t base = lane < warp ? c.warp_a[lane] : 0u;
-        base = __reduce_add_sync(0xFFFFFFFFu, base);
-        const uint32_t before = base + run - h1 - h0;
+    };
+    auto shift_of = [](uint32_t span) {
+        const int bits = 32 - __clz(span);
+        return bits > 11 ? bits - 11 : 0;
+    };
+    uint32_t need = (uint32_t)nb;  // blocks still to take from [lo, hi]; every score above hi is taken
+    bool bracket = false;
+    if (!on_chip) {
+        // ranks of the threshold in the sample, six standard deviations either way
+        const int shift = shift_of(hi - lo);
+#pragma unroll
+        for (int j = 0; j < kSample; ++j) atomicAdd(&c.hist[(seen[j] - lo) >> shift], 1u);
+        count_bins();
+        const float share = (float)nb / (float)n * (float)total, dev = 6.0f * sqrtf(share) + 6.0f;
+        const uint32_t upper = share > dev ? (uint32_t)(share - dev) : 0u, lower = (uint32_t)(share + dev);
+        if (tid == 0) {
+            c.edge[0] = 0u;            // no bin that low: open
+            c.edge[1] = 0xFFFFFFFFu;
+        }
+        __syncthreads();
+        if (before <= lower && lower < before + h1 + h0) c.edge[0] = lo + ((uint32_t)(top - 1) << shift);
+        if (upper > 0u && before <= upper && upper < before + h1 + h0)
+            c.edge[1] = min(hi - lo, ((uint32_t)(top + 1) << shift) - 1u) + lo;
+        clear_bins();
+        lo = c.edge[0];
+        hi = max(c.edge[1], lo);
+        bracket = true;
+    }
+    uint32_t above = 0;  // this thread's scores above the bracket
+    bool all = false, exact = false;  // the whole range is taken; lo == hi is the threshold
+    while (lo != hi || bracket) {
+        const int shift = shift_of(hi - lo);
+        each_score(s, m, [&](uint32_t v) {
+            if (v >= lo && v <= hi) atomicAdd(&c.hist[(v - lo) >> shift], 1u);
+            if (bracket) above += v > hi;
+        });
+        if (bracket) {
+            above = __reduce_add_sync(0xFFFFFFFFu, above);
+            if (lane == 0 && above) atomicAdd(&c.above, above);
+        }
+        count_bins();
+        if (bracket) {
+            uint32_t over = 0;
+            for (int p = 0; p < kC; ++p) over += team_load<kC>(&c.above, p);
+            bracket = false;
+            if (over >= need || over + total < need) {  // the threshold is not in it
+                clear_bins();
+                lo = 0u;
+                hi = 0xFFFFFFFFu;
+                continue;
+            }
+            need -= over;
+        }
         if (before < need && need <= before + h1) {
             c.bin = top;
             c.need = need - before;
@@ -527,84 +608,148 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
             c.need = need - before - h1;
             c.count = h0;
         }
-        team_sync<kC>();  // the peers have read this histogram, too
+        clear_bins();
         lo += c.bin << shift;
         hi = min(hi - lo, (1u << shift) - 1u) + lo;  // (lo + 2^shift may pass 32 bits)
         need = c.need;
-        all = need == c.count;
-        if (all || shift == 0) break;
+        const uint32_t in = c.count;
+        all = need == in;
+        if (all || lo == hi) break;
+        if (in <= kFew) {
+            // rank them: the threshold is the score with less than `need` above it and no less up to it
+            if (tid == 0) c.few_n = 0u;
+            __syncthreads();
+            each_score(s, m, [&](uint32_t v) {
+                if (v >= lo && v <= hi) c.few[atomicAdd(&c.few_n, 1u)] = v;
+            });
+            team_sync<kC>();
+            uint32_t at = 0;
+            for (int p = 0; p < kC; ++p) {
+                const uint32_t np = team_load<kC>(&c.few_n, p);
+                if (tid < np) c.pool[at + tid] = team_load<kC>(&c.few[tid], p);
+                at += np;
+            }
+            __syncthreads();
+            if (tid < in) {
+                const uint32_t mine = c.pool[tid];
+                uint32_t more = 0, same = 0;
+                for (uint32_t i = 0; i < in; ++i) {
+                    more += c.pool[i] > mine;
+                    same += c.pool[i] == mine;
+                }
+                if (more < need && need <= more + same) {  // every thread with this score writes the same
+                    c.lo = mine;
+                    c.need = need - more;
+                    c.count = same;
+                }
+            }
+            __syncthreads();
+            lo = hi = c.lo;
+            need = c.need;
+            all = need == c.count;
+            break;
+        }
         __syncthreads();  // c.bin, c.need and c.count have been read
     }
-    // taken: a score above hi, or in [lo, hi] if all of them are, or (lo == hi) the first `need` equal to it
-    const uint32_t above_from = all ? lo : hi + 1u;  // hi + 1 == 0 only if nothing lies above hi
-    const bool none_above = !all && hi == 0xFFFFFFFFu;
+    exact = !all;  // then lo == hi, and of the scores equal to it the first `need` are taken
+    // taken: above hi, or not below lo if the whole range is
+    auto is_taken = [&](uint32_t v) { return v > hi || (all && v >= lo); };
 
-    const int seg = ((m + 31) / 32 + 127) & ~127;  // a warp's stretch of keys, 128 at a time
-    const int s0 = min(m, warp * seg), s1 = min(m, s0 + seg);
+    // one window of this CTA's scores: bits, the words' counts, places
+    const int windows = (m + kWindowKeys - 1) / kWindowKeys;
+    auto mark = [&](int w0, int wm) {
+        const uint32_t* sw = s + w0;
+        for (int i = 4 * tid; i < ((wm + 127) & ~127); i += 4 * kPickThreads) {
+            uint32_t v[4];
+            if (i + 4 <= wm) {
+                const uint4 x = *reinterpret_cast<const uint4*>(sw + i);
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = i + j < wm ? sw[i + j] : 0u;
+            }
+            uint32_t a = 0, e = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = i + j < wm, t = in && is_taken(v[j]);
+                a |= (uint32_t)t << j;
+                e |= (uint32_t)(exact && in && !t && v[j] == lo) << j;
+            }
+            // eight lanes make a word of 32 keys
+            uint32_t both = a | e << 4;
+            a = both & 15u, e = both >> 4;
+            a <<= 4 * (lane & 7);
+            e <<= 4 * (lane & 7);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                a |= __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                e |= __shfl_xor_sync(0xFFFFFFFFu, e, o);
+            }
+            if ((lane & 7) == 0) {
+                taken[i >> 5] = a;
+                equal[i >> 5] = e;
+            }
+        }
+    };
+    if (tid == 0) c.above = 0u;
+    team_sync<kC>();  // the peers have read c.above and the lists
     uint32_t na = 0, nt = 0;
-    for (int i = s0 + 4 * lane; i < s1; i += 128) {
-        uint32_t v[4];
-        if (i + 4 <= s1) {
-            const uint4 x = *reinterpret_cast<const uint4*>(s + i);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-            for (int j = 0; j < 4; ++j) v[j] = i + j < s1 ? s[i + j] : 0u;
+    if (windows == 1) {
+        mark(0, m);
+        __syncthreads();
+        for (int i = tid; i < (m + 31) / 32; i += kPickThreads) {
+            na += __popc(taken[i]);
+            nt += __popc(equal[i]);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool in = i + j < s1, a = in && v[j] >= above_from && !none_above;
-            na += a;
-            nt += in && !a && !all && v[j] == lo;
+    } else {
+        each_score(s, m, [&](uint32_t v) {
+            const bool t = is_taken(v);
+            na += t;
+            nt += exact && !t && v == lo;
+        });
+    }
+    uint32_t pa = 0, pt = 0;  // taken and equal in the CTAs before this one
+    if constexpr (kC > 1) {
+        na = __reduce_add_sync(0xFFFFFFFFu, na);
+        nt = __reduce_add_sync(0xFFFFFFFFu, nt);
+        if (lane == 0 && na) atomicAdd(&c.above, na);
+        if (lane == 0 && nt) atomicAdd(&c.ties, nt);
+        team_sync<kC>();
+        for (int p = 0; p < rank; ++p) {
+            pa += team_load<kC>(&c.above, p);
+            pt += team_load<kC>(&c.ties, p);
         }
     }
-    na = __reduce_add_sync(0xFFFFFFFFu, na);
-    nt = __reduce_add_sync(0xFFFFFFFFu, nt);
-    if (lane == 0) {
-        c.warp_a[warp] = na;
-        c.warp_b[warp] = nt;
-        if (na) atomicAdd(&c.above, na);
-        if (nt) atomicAdd(&c.ties, nt);
-    }
-    team_sync<kC>();
-    uint32_t pa = lane < warp ? c.warp_a[lane] : 0u, pt = lane < warp ? c.warp_b[lane] : 0u;
-    pa = __reduce_add_sync(0xFFFFFFFFu, pa);
-    pt = __reduce_add_sync(0xFFFFFFFFu, pt);
-    for (int p = 0; p < rank; ++p) {
-        pa += team_load<kC>(&c.above, p);
-        pt += team_load<kC>(&c.ties, p);
-    }
-    for (int i0 = s0; i0 < s1; i0 += 128) {
-        const int i = i0 + 4 * lane;
-        uint32_t v[4] = {0u, 0u, 0u, 0u};
-        if (i + 4 <= s1) {
-            const uint4 x = *reinterpret_cast<const uint4*>(s + i);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-            for (int j = 0; j < 4; ++j)
-                if (i + j < s1) v[j] = s[i + j];
+    for (int w = 0; w < windows; ++w) {
+        const int w0 = w * kWindowKeys, wm = min(m - w0, kWindowKeys);
+        if (windows > 1) {
+            __syncthreads();  // the window before has been written out
+            mark(w0, wm);
+            __syncthreads();
         }
-        bool a[4], e[4];
-        uint32_t ca = 0, ct = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool in = i + j < s1;
-            a[j] = in && v[j] >= above_from && !none_above;
-            e[j] = in && !a[j] && !all && v[j] == lo;
-            ca += a[j];
-            ct += e[j];
-        }
-        uint32_t both = ca | ct << 16, run = both;  // at most 128 each
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, run, o);
-            if (lane >= o) run += x;
-        }
-        uint32_t qa = pa + ((run - both) & 0xFFFFu), qt = pt + ((run - both) >> 16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (a[j] || (e[j] && qt < need)) {
-                const uint32_t at = qa + min(qt, need);
-                const int key = c0 + i + j;
+        const int words = (wm + 31) / 32;
+        for (int i0 = 0; i0 < words; i0 += kPickThreads) {
+            const int i = i0 + tid;
+            uint32_t a = i < words ? taken[i] : 0u, e = i < words ? equal[i] : 0u;
+            const uint32_t ca = __popc(a), ce = __popc(e);
+            uint32_t sum, sum_e;
+            const uint32_t qa = pa + cta_scan(ca, c.warp_a, &sum) - ca;
+            const uint32_t qe = exact ? pt + cta_scan(ce, c.warp_b, &sum_e) - ce : 0u;
+            if (exact) {  // the first need - qe of the word's equal scores
+                uint32_t left = need > qe ? need - qe : 0u;
+                uint32_t kept_e = 0;
+                while (e != 0u && left > 0u) {
+                    kept_e |= e & (0u - e);
+                    e &= e - 1u;
+                    --left;
+                }
+                a |= kept_e;
+                pt += sum_e;
+            }
+            uint32_t at = qa + min(qe, need);
+            while (a != 0u) {
+                const int key = c0 + w0 + 32 * i + __ffs(a) - 1;
+                a &= a - 1u;
                 if (sh.block == 1) {
                     out[at] = key;
                 } else {
@@ -613,13 +758,11 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
                         out[(size_t)at * sh.block + x] = token < len ? token : -1;
                     }
                 }
+                ++at;
             }
-            qa += a[j];
-            qt += e[j];
+            pa += sum;
+            __syncthreads();  // the sums have been read
         }
-        const uint32_t sum = __shfl_sync(0xFFFFFFFFu, run, 31);
-        pa += sum & 0xFFFFu;
-        pt += sum >> 16;
     }
     if constexpr (kC > 1) tc::cluster_sync();  // the peers may still be reading this CTA's counts
 }
@@ -638,10 +781,10 @@ cudaError_t prepare_select()
     set(score_kernel<64, true>, kScoreSmem);
     set(score_kernel<128, false>, kScoreSmem);
     set(score_kernel<128, true>, kScoreSmem);
-    set(pick_kernel<1>, kStagedKeys * 4);
-    set(pick_kernel<2>, kStagedKeys * 4);
-    set(pick_kernel<4>, kStagedKeys * 4);
-    set(pick_kernel<8>, kStagedKeys * 4);
+    set(pick_kernel<1>, (int)kPickSmem);
+    set(pick_kernel<2>, (int)kPickSmem);
+    set(pick_kernel<4>, (int)kPickSmem);
+    set(pick_kernel<8>, (int)kPickSmem);
     return e;
 }
 
@@ -701,18 +844,20 @@ cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_
     int team = 1;
     while (team < 8 && max_keys / (2 * team) >= 2048 && (max_keys / team > kStagedKeys || units * team * 2 <= device_sms)) team *= 2;
     const int64_t chunk = ((max_keys + team - 1) / team + 127) & ~(int64_t)127;
-    const int staged = chunk <= kStagedKeys ? (int)chunk : 0;
+    const int staged = (int)std::min<int64_t>(chunk, kStagedKeys);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * team));
     cfg.blockDim = dim3(kPickThreads);
-    cfg.dynamicSmemBytes = (size_t)staged * 4;
+    cfg.dynamicSmemBytes = chunk <= staged ? (size_t)staged * 4 + staged / 4 : kPickSmem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = team;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // takes the SMs that score_kernel leaves, and waits
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     auto pick = team == 1 ? pick_kernel<1> : team == 2 ? pick_kernel<2> : team == 4 ? pick_kernel<4> : pick_kernel<8>;
     return cudaLaunchKernelEx(&cfg, pick, d, req_ids, sh, static_cast<const uint32_t*>(scores), staged, topk);
 }
