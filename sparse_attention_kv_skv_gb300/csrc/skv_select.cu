@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     if (warp == kLoadWarp) {
         if (lane == 0) {
             Walk k(d, sh, req_ids, c.start);
+            const uint64_t stream_once = tc::evict_first_policy();  // keys pass L2 by; the scores stay for pick_kernel
             bool ok = true;
             int units = 0, it = 0;
             for (; it < count; ++it) {
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 #pragma unroll
                 for (int x = 0; x < kBoxes; ++x)
                     tc::tma_load4(tc::smem_u32(smem) + s * kStageBytes + x * kBoxBytes, &key_map, 64 * x, k.tile * kTileKeys,
-                                  d.layer_sel >= 0 ? d.layer_sel : k.l, k.r, &c.full[s]);
+                                  d.layer_sel >= 0 ? d.layer_sel : k.l, k.r, &c.full[s], stream_once);
                 if (it + 1 < count) k.next();
             }
             if (!ok) {
@@ -362,26 +363,30 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-constexpr int kPickThreads = 1024;
-constexpr int kBins = 2048;            // two a thread
-constexpr int kStagedKeys = 20480;     // scores a CTA keeps in shared memory (80 KB: two CTAs a SM)
-constexpr int kWindowKeys = 262144;    // scores whose bits fit the same room when the scores stay in L2
-constexpr int kFew = 1024;             // scores that are ranked directly
-// Dynamic shared memory: the scores and two bits each, or the bits of a window alone.
-constexpr size_t kPickSmem = (size_t)kStagedKeys * 4 + kStagedKeys / 4;
-static_assert(kWindowKeys / 4 <= (int)kPickSmem, "a window's bits fit");
-constexpr int kSample = 8;             // scores a thread samples of a long context
+constexpr int kPickThreads = 512;
+constexpr int kBinBits = 10;
+constexpr int kBins = 1 << kBinBits;   // two a thread
+constexpr int kStagedKeys = 20480;     // scores a CTA keeps in shared memory (80 KB: two CTAs a SM; three up to 64 KB)
+constexpr int kWindowKeys = 524288;    // scores whose bits fit the same room when the scores stay in L2
+constexpr int kFew = 512;              // scores that are ranked directly
+constexpr int kSample = 4;             // scores a thread samples of a long context
+// Dynamic shared memory: the scores and a bit each, or the bits of a window alone.
+constexpr size_t kPickSmem = (size_t)kStagedKeys * 4 + kStagedKeys / 8;
+static_assert(kWindowKeys / 8 + kMaxTopk / 2 * 4 <= (int)kPickSmem, "a window's bits fit, and the blocks behind them");
 
+template <int kC>
 struct PickCtl {
     uint32_t hist[kBins];
-    uint32_t few[kFew];                // the scores of the threshold's bin: this CTA's,
-    uint32_t pool[kFew];               // and the team's
+    uint2 few[kFew];                   // (score, key) in the threshold's bin: this CTA's,
+    uint2 pool[kC > 1 ? kFew : 1];     // and the team's
     uint32_t few_n;
     uint32_t lo, hi;                   // this CTA's range of scores
     uint32_t bin, need, count;         // the threshold's bin, what is still to take from it, what it holds
     uint32_t edge[2];                  // a bracket of the threshold, from a sample
-    uint32_t above, ties;              // this CTA's scores above the threshold, and at it
-    uint32_t warp_a[32], warp_b[32];
+    uint32_t over;                     // this CTA's scores above the bracket
+    uint32_t taken;                    // what this CTA takes
+    uint2 last;                        // (score, key) of the last block taken
+    uint32_t warp_sum[32];
 };
 
 __device__ __forceinline__ uint32_t peer_load(const uint32_t* p, uint32_t rank)
@@ -407,24 +412,49 @@ __device__ __forceinline__ uint32_t team_load(const uint32_t* p, uint32_t rank)
         return *p;
 }
 
-// f(score) for the m scores at s, four a thread at a time.
-template <typename F>
-__device__ __forceinline__ void each_score(const uint32_t* s, int m, F f)
+// 16-byte reads a thread has in flight (longer contexts are read from L2 in every pass)
+template <int kC>
+constexpr int kAtOnce = kC > 1 ? 8 : 4;
+
+__device__ __forceinline__ uint32_t largest(uint4 v) { return max(max(v.x, v.y), max(v.z, v.w)); }
+
+// f(score, index) for those of the m scores at s that are at least `least`, and perhaps for others.  Four a thread at a
+// time; mostly all four are below.
+template <int kReads, typename F>
+__device__ __forceinline__ void each_score(const uint32_t* s, int m, uint32_t least, F f)
 {
     const int m4 = m >> 2;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < m4; i += kPickThreads) {
-        const uint4 v = reinterpret_cast<const uint4*>(s)[i];
-        f(v.x);
-        f(v.y);
-        f(v.z);
-        f(v.w);
+    const uint4* s4 = reinterpret_cast<const uint4*>(s);
+    int i = threadIdx.x;
+    for (; i + (kReads - 1) * kPickThreads < m4; i += kReads * kPickThreads) {
+        uint4 v[kReads];  // read before f may write shared memory, so that the reads are in flight together
+#pragma unroll
+        for (int x = 0; x < kReads; ++x) v[x] = s4[i + x * kPickThreads];
+#pragma unroll
+        for (int x = 0; x < kReads; ++x) {
+            const int at = 4 * (i + x * kPickThreads);
+            if (largest(v[x]) >= least) {
+                f(v[x].x, at);
+                f(v[x].y, at + 1);
+                f(v[x].z, at + 2);
+                f(v[x].w, at + 3);
+            }
+        }
     }
-    const int i = 4 * m4 + threadIdx.x;
-    if (i < m) f(s[i]);
+    for (; i < m4; i += kPickThreads) {
+        const uint4 v = s4[i];
+        if (largest(v) >= least) {
+            f(v.x, 4 * i);
+            f(v.y, 4 * i + 1);
+            f(v.z, 4 * i + 2);
+            f(v.w, 4 * i + 3);
+        }
+    }
+    i = 4 * m4 + threadIdx.x;
+    if (i < m) f(s[i], i);
 }
 
-// Inclusive sum over the CTA's threads, in thread order; `all` receives the total.
+// Inclusive sum over the CTA's threads, in thread order; *all receives the total.
 __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* warp_sum, uint32_t* all)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -435,65 +465,64 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* warp_sum, uin
     }
     if (lane == 31) warp_sum[warp] = v;
     __syncthreads();
-    const uint32_t w = warp_sum[lane];
-    if (all) *all = __reduce_add_sync(0xFFFFFFFFu, w);
+    const uint32_t w = lane < kPickThreads / 32 ? warp_sum[lane] : 0u;
+    *all = __reduce_add_sync(0xFFFFFFFFu, w);
     return v + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u);
 }
 
 // One team (a CTA, or a cluster of kC that share the scores of a long context)
-// a unit.  The threshold -- the score of the last block taken -- is found by
-// narrowing its range: histogram 2048 equal parts of the range, find the part in
-// which the count from above passes k / block, and go on inside it until it holds so few
-// scores that they are ranked directly.  The first range is that of the scores
-// themselves, so they spread over the bins and few atomics meet, and the first
-// histogram is mostly the only one.  A context too long for shared memory is
-// read from L2 in each pass; there the first range is a bracket of the threshold
-// taken from a sample, so no pass is spent on the extremes and only the
-// scores inside the bracket are counted (a bracket that misses is noticed by its
-// counts and replaced by the whole range).  With the threshold known, one bit a
-// score says what is taken, a scan of the words' counts gives each word its place,
-// and the tokens come out ascending without a sort.
+// a unit.  Taken are the k / block first in the order (score descending, key
+// ascending); the last of them is the threshold, and a key is taken if it is not
+// behind it.  The threshold is found by narrowing its range: histogram 1024 equal
+// parts of the range, find the part in which the count from above passes k / block, and
+// go on inside it until it holds so few scores that they are ranked directly.
+// The first range is that of the scores themselves, so they spread over the bins
+// and few atomics meet, and the first histogram is mostly the only one.  (More
+// scores equal to the threshold than can be ranked: their keys are narrowed down in the
+// same way.)  A context too long for shared memory is read from L2 in each
+// pass; there the first range is a bracket of the threshold taken from a sample,
+// so no pass is spent on the extremes and only the scores inside the bracket are
+// counted (a bracket that misses shows in its counts and is replaced by the
+// whole range).  With the threshold known, one bit a score says what is taken, a
+// scan of the words' counts gives each word its place, and the tokens come out
+// ascending without a sort.
 template <int kC>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t* __restrict__ req_ids, SelectShape sh,
+__global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 1) pick_kernel(Dev d, const int32_t* __restrict__ req_ids, SelectShape sh,
                                                             const uint32_t* __restrict__ scores, int staged,
                                                             int32_t* __restrict__ topk)
 {
     extern __shared__ __align__(16) uint32_t kept[];
-    __shared__ PickCtl c;
+    __shared__ PickCtl<kC> c;
+    constexpr int kReads = kAtOnce<kC>;
     const int tid = threadIdx.x, lane = tid & 31;
     const int u = blockIdx.x / kC, rank = blockIdx.x % kC;
     int32_t* out = topk + (size_t)u * d.k;
+    if (tid == 0) {
+        c.lo = 0xFFFFFFFFu;
+        c.hi = 0u;
+        c.over = c.taken = 0u;
+    }
+    for (int i = tid; i < kBins; i += kPickThreads) c.hist[i] = 0u;
     const int32_t r = req_ids[u / sh.layers];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores (and the error word) are complete
-    if (d.ctl[CTL_ERR] != 0u) {  // the same for every CTA: nothing writes the word during this kernel
-        for (int i = rank * kPickThreads + tid; i < d.k; i += kC * kPickThreads) out[i] = -1;
-        return;
-    }
-    const int len = (int)d.len[r], n = keys_of(d, r, sh.block), nb = d.k / sh.block;
-    if (n <= nb) {  // everything there is
-        for (int i = rank * kPickThreads + tid; i < d.k; i += kC * kPickThreads) out[i] = i < len ? i : -1;
+    const uint32_t err = d.ctl[CTL_ERR];  // the same for every CTA: nothing writes the word during this kernel
+    const int len = r >= 0 && r < d.R ? (int)d.len[r] : 0, n = (len + sh.block - 1) / sh.block, nb = d.k / sh.block;
+    if (err != 0u || n <= nb) {  // nothing, or everything there is
+        for (int i = rank * kPickThreads + tid; i < d.k; i += kC * kPickThreads) out[i] = err == 0u && i < len ? i : -1;
         return;
     }
     const int chunk = ((n + kC - 1) / kC + 127) & ~127;
     const int c0 = min(n, rank * chunk), m = min(n, c0 + chunk) - c0;
     const uint32_t* s = scores + (size_t)u * sh.stride + c0;
-    if (tid == 0) {
-        c.lo = 0xFFFFFFFFu;
-        c.hi = 0u;
-        c.above = c.ties = 0u;
-    }
-    for (int i = tid; i < kBins; i += kPickThreads) c.hist[i] = 0u;
+    const bool on_chip = chunk <= staged;
+    uint32_t* bits = on_chip ? kept + chunk : kept;
     __syncthreads();
 
     // the first range
     uint32_t lo = 0xFFFFFFFFu, hi = 0u, seen[kSample];
-    const bool on_chip = chunk <= staged;
-    // a bit a score: above the threshold; at it (where not all of those are taken)
-    uint32_t* taken = on_chip ? kept + chunk : kept;
-    uint32_t* equal = taken + (on_chip ? chunk : kWindowKeys) / 32;
     if (on_chip) {
         const int m4 = m >> 2;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = tid; i < m4; i += kPickThreads) {
             const uint4 v = __ldcg(reinterpret_cast<const uint4*>(s) + i);
             reinterpret_cast<uint4*>(kept)[i] = v;
@@ -524,13 +553,17 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
         atomicMax(&c.hi, hi);
     }
     team_sync<kC>();
-    lo = 0xFFFFFFFFu;
-    hi = 0u;
-    for (int p = 0; p < kC; ++p) {
-        lo = min(lo, team_load<kC>(&c.lo, p));
-        hi = max(hi, team_load<kC>(&c.hi, p));
+    lo = c.lo;
+    hi = c.hi;
+    if constexpr (kC > 1) {
+        for (int p = 0; p < kC; ++p) {
+            lo = min(lo, team_load<kC>(&c.lo, p));
+            hi = max(hi, team_load<kC>(&c.hi, p));
+        }
     }
-    // thread t looks after the bins 2047 - 2t and 2046 - 2t: counts of the team, and a running count from the top
+    // thread t looks after the bins kBins - 1 - 2t and kBins - 2 - 2t: counts of the team, and a running
+    // count from the top
+    static_assert(kBins == 2 * kPickThreads, "two bins a thread");
     uint32_t h1, h0, before, total;
     const int top = kBins - 1 - 2 * tid;
     auto count_bins = [&]() {
@@ -540,19 +573,19 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
             h1 += team_load<kC>(&c.hist[top], p);
             h0 += team_load<kC>(&c.hist[top - 1], p);
         }
-        before = cta_scan(h1 + h0, c.warp_a, &total) - h1 - h0;
+        before = cta_scan(h1 + h0, c.warp_sum, &total) - h1 - h0;
     };
     auto clear_bins = [&]() {
-        team_sync<kC>();  // the peers have read this histogram, too
+        team_sync<kC>();  // every thread of the team has read what it needs
         c.hist[top] = c.hist[top - 1] = 0u;
         __syncthreads();
     };
     auto shift_of = [](uint32_t span) {
         const int bits = 32 - __clz(span);
-        return bits > 11 ? bits - 11 : 0;
+        return bits > kBinBits ? bits - kBinBits : 0;
     };
     uint32_t need = (uint32_t)nb;  // blocks still to take from [lo, hi]; every score above hi is taken
-    bool bracket = false;
+    bool bracket = false, open = false;
     if (!on_chip) {
         // ranks of the threshold in the sample, six standard deviations either way
         const int shift = shift_of(hi - lo);
@@ -561,9 +594,10 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
         count_bins();
         const float share = (float)nb / (float)n * (float)total, dev = 6.0f * sqrtf(share) + 6.0f;
         const uint32_t upper = share > dev ? (uint32_t)(share - dev) : 0u, lower = (uint32_t)(share + dev);
+        open = upper == 0u;  // then the last bin takes whatever lies above the sample, too
         if (tid == 0) {
-            c.edge[0] = 0u;            // no bin that low: open
-            c.edge[1] = 0xFFFFFFFFu;
+            c.edge[0] = 0u;  // no bin that low
+            c.edge[1] = hi;
         }
         __syncthreads();
         if (before <= lower && lower < before + h1 + h0) c.edge[0] = lo + ((uint32_t)(top - 1) << shift);
@@ -574,22 +608,93 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
         hi = max(c.edge[1], lo);
         bracket = true;
     }
-    uint32_t above = 0;  // this thread's scores above the bracket
-    bool all = false, exact = false;  // the whole range is taken; lo == hi is the threshold
-    while (lo != hi || bracket) {
+
+    // Narrow the scores, then, if need be, the keys of the scores equal to the threshold (as ~key: the lower key is
+    // the larger).  [lo, hi] is the range of either.
+    bool keys = false, marked = false;
+    uint32_t tv = 0, ti = 0;  // the threshold: score and key
+    auto is_taken = [&](uint32_t v, uint32_t key) { return v > tv || (v == tv && key <= ti); };
+    // One window of this CTA's scores: a bit each for f(score, key), which is false below `least`.  A lane has four
+    // consecutive keys, eight lanes make a word.
+    const int windows = (m + kWindowKeys - 1) / kWindowKeys;
+    auto mark = [&](int w0, int wm, uint32_t least, auto f) {
+        const uint32_t* sw = s + w0;
+        const int end = (wm + 127) & ~127;  // whole warps
+        for (int i0 = 4 * tid; i0 < end; i0 += 4 * kPickThreads * kReads) {
+            uint4 v[kReads];
+#pragma unroll
+            for (int x = 0; x < kReads; ++x) {
+                const int i = i0 + 4 * kPickThreads * x;
+                v[x] = make_uint4(0, 0, 0, 0);
+                if (i + 4 <= wm) {
+                    v[x] = *reinterpret_cast<const uint4*>(sw + i);
+                } else if (i < wm) {
+                    v[x].x = sw[i];
+                    if (i + 1 < wm) v[x].y = sw[i + 1];
+                    if (i + 2 < wm) v[x].z = sw[i + 2];
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kReads; ++x) {
+                const int i = i0 + 4 * kPickThreads * x;
+                if (i < end) {  // the same for a warp
+                    uint32_t a = 0u;
+                    if (__any_sync(0xFFFFFFFFu, largest(v[x]) >= least)) {
+                        const uint32_t key = (uint32_t)(c0 + w0 + i);
+                        if (i + 4 <= wm)
+                            a = (f(v[x].x, key) ? 1u : 0u) | (f(v[x].y, key + 1) ? 2u : 0u) |
+                                (f(v[x].z, key + 2) ? 4u : 0u) | (f(v[x].w, key + 3) ? 8u : 0u);
+                        else if (i < wm)
+                            a = (f(v[x].x, key) ? 1u : 0u) | (i + 1 < wm && f(v[x].y, key + 1) ? 2u : 0u) |
+                                (i + 2 < wm && f(v[x].z, key + 2) ? 4u : 0u);
+                        a <<= 4 * (lane & 7);
+                        a |= __shfl_xor_sync(0xFFFFFFFFu, a, 1);
+                        a |= __shfl_xor_sync(0xFFFFFFFFu, a, 2);
+                        a |= __shfl_xor_sync(0xFFFFFFFFu, a, 4);
+                    }
+                    if ((lane & 7) == 0) bits[i >> 5] = a;
+                }
+            }
+        }
+    };
+    for (;;) {
+        if (lo == hi && !bracket) {
+            if (keys) {  // a single key
+                ti = ~lo;
+                break;
+            }
+            tv = lo;  // equal scores, more of them than needed
+            keys = true;
+            lo = ~(uint32_t)(n - 1);
+            hi = 0xFFFFFFFFu;
+        }
         const int shift = shift_of(hi - lo);
-        each_score(s, m, [&](uint32_t v) {
-            if (v >= lo && v <= hi) atomicAdd(&c.hist[(v - lo) >> shift], 1u);
-            if (bracket) above += v > hi;
-        });
+        uint32_t over = 0;
+        const uint32_t span = hi - lo;
+        if (keys)
+            each_score<kReads>(s, m, tv, [&](uint32_t v, int i) {
+                const uint32_t x = ~(uint32_t)(c0 + i) - lo;
+                if (v == tv && x <= span) atomicAdd(&c.hist[x >> shift], 1u);
+            });
+        else if (bracket)
+            each_score<kReads>(s, m, lo, [&](uint32_t v, int) {
+                if (v > hi && !open)
+                    ++over;
+                else if (v >= lo)
+                    atomicAdd(&c.hist[min((v - lo) >> shift, (uint32_t)kBins - 1u)], 1u);
+            });
+        else
+            each_score<kReads>(s, m, lo, [&](uint32_t v, int) {
+                if (v - lo <= span) atomicAdd(&c.hist[(v - lo) >> shift], 1u);
+            });
         if (bracket) {
-            above = __reduce_add_sync(0xFFFFFFFFu, above);
-            if (lane == 0 && above) atomicAdd(&c.above, above);
+            over = __reduce_add_sync(0xFFFFFFFFu, over);
+            if (lane == 0 && over) atomicAdd(&c.over, over);
         }
         count_bins();
         if (bracket) {
-            uint32_t over = 0;
-            for (int p = 0; p < kC; ++p) over += team_load<kC>(&c.above, p);
+            over = 0;
+            for (int p = 0; p < kC; ++p) over += team_load<kC>(&c.over, p);
             bracket = false;
             if (over >= need || over + total < need) {  // the threshold is not in it
                 clear_bins();
@@ -598,6 +703,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
                 continue;
             }
             need -= over;
+            if (open) hi = 0xFFFFFFFFu;
         }
         if (before < need && need <= before + h1) {
             c.bin = top;
@@ -608,160 +714,116 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Dev d, const int32_t
             c.need = need - before - h1;
             c.count = h0;
         }
-        clear_bins();
+        __syncthreads();
         lo += c.bin << shift;
-        hi = min(hi - lo, (1u << shift) - 1u) + lo;  // (lo + 2^shift may pass 32 bits)
+        if (!open || c.bin != kBins - 1) hi = min(hi - lo, (1u << shift) - 1u) + lo;  // (lo + 2^shift may pass 32 bits)
+        open = false;
         need = c.need;
         const uint32_t in = c.count;
-        all = need == in;
-        if (all || lo == hi) break;
-        if (in <= kFew) {
-            // rank them: the threshold is the score with less than `need` above it and no less up to it
-            if (tid == 0) c.few_n = 0u;
-            __syncthreads();
-            each_score(s, m, [&](uint32_t v) {
-                if (v >= lo && v <= hi) c.few[atomicAdd(&c.few_n, 1u)] = v;
-            });
-            team_sync<kC>();
-            uint32_t at = 0;
-            for (int p = 0; p < kC; ++p) {
-                const uint32_t np = team_load<kC>(&c.few_n, p);
-                if (tid < np) c.pool[at + tid] = team_load<kC>(&c.few[tid], p);
-                at += np;
+        if (need == in) {  // all of the range
+            if (!keys) {
+                tv = lo - 1u;  // every score from lo on (lo > 0: fewer than n scores are taken)
+                ti = 0u;
+                if (lo == 0u) ti = 0xFFFFFFFFu, tv = 0u;
+            } else {
+                ti = ~lo;
             }
-            __syncthreads();
-            if (tid < in) {
-                const uint32_t mine = c.pool[tid];
-                uint32_t more = 0, same = 0;
-                for (uint32_t i = 0; i < in; ++i) {
-                    more += c.pool[i] > mine;
-                    same += c.pool[i] == mine;
-                }
-                if (more < need && need <= more + same) {  // every thread with this score writes the same
-                    c.lo = mine;
-                    c.need = need - more;
-                    c.count = same;
-                }
-            }
-            __syncthreads();
-            lo = hi = c.lo;
-            need = c.need;
-            all = need == c.count;
             break;
         }
-        __syncthreads();  // c.bin, c.need and c.count have been read
-    }
-    exact = !all;  // then lo == hi, and of the scores equal to it the first `need` are taken
-    // taken: above hi, or not below lo if the whole range is
-    auto is_taken = [&](uint32_t v) { return v > hi || (all && v >= lo); };
-
-    // one window of this CTA's scores: bits, the words' counts, places
-    const int windows = (m + kWindowKeys - 1) / kWindowKeys;
-    auto mark = [&](int w0, int wm) {
-        const uint32_t* sw = s + w0;
-        for (int i = 4 * tid; i < ((wm + 127) & ~127); i += 4 * kPickThreads) {
-            uint32_t v[4];
-            if (i + 4 <= wm) {
-                const uint4 x = *reinterpret_cast<const uint4*>(sw + i);
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = i + j < wm ? sw[i + j] : 0u;
+        if (in <= kFew) {
+            // rank them in the order of taking: the threshold is the one with need - 1 before it
+            if (tid == 0) c.few_n = 0u;
+            __syncthreads();
+            const uint32_t span = hi - lo;
+            marked = windows == 1 && !keys;
+            if (marked)  // the bits of what is above the range in the same pass
+                mark(0, m, lo, [&](uint32_t v, uint32_t key) {
+                    if (v - lo <= span) c.few[atomicAdd(&c.few_n, 1u)] = make_uint2(v, key);
+                    return v > hi;
+                });
+            else
+                each_score<kReads>(s, m, keys ? tv : lo, [&](uint32_t v, int i) {
+                    const uint32_t key = (uint32_t)(c0 + i);
+                    if ((keys ? ~key : v) - lo <= span && (!keys || v == tv)) c.few[atomicAdd(&c.few_n, 1u)] = make_uint2(v, key);
+                });
+            team_sync<kC>();
+            const uint2* list = c.few;
+            if constexpr (kC > 1) {
+                uint32_t at = 0;
+                for (int p = 0; p < kC; ++p) {
+                    const uint32_t np = team_load<kC>(&c.few_n, p);
+                    if (tid < np) c.pool[at + tid] = make_uint2(team_load<kC>(&c.few[tid].x, p), team_load<kC>(&c.few[tid].y, p));
+                    at += np;
+                }
+                __syncthreads();
+                list = c.pool;
             }
-            uint32_t a = 0, e = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = i + j < wm, t = in && is_taken(v[j]);
-                a |= (uint32_t)t << j;
-                e |= (uint32_t)(exact && in && !t && v[j] == lo) << j;
+            if (tid < in) {
+                const uint2 mine = list[tid];
+                uint32_t first = 0;
+                for (uint32_t i = 0; i < in; ++i) {
+                    const uint2 o = list[i];
+                    first += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+                }
+                if (first + 1 == need) c.last = mine;
             }
-            // eight lanes make a word of 32 keys
-            uint32_t both = a | e << 4;
-            a = both & 15u, e = both >> 4;
-            a <<= 4 * (lane & 7);
-            e <<= 4 * (lane & 7);
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                a |= __shfl_xor_sync(0xFFFFFFFFu, a, o);
-                e |= __shfl_xor_sync(0xFFFFFFFFu, e, o);
-            }
-            if ((lane & 7) == 0) {
-                taken[i >> 5] = a;
-                equal[i >> 5] = e;
-            }
+            __syncthreads();
+            tv = c.last.x;
+            ti = c.last.y;
+            if (marked && tid < c.few_n && is_taken(c.few[tid].x, c.few[tid].y))
+                atomicOr(&bits[(c.few[tid].y - c0) >> 5], 1u << ((c.few[tid].y - c0) & 31u));
+            break;
         }
-    };
-    if (tid == 0) c.above = 0u;
-    team_sync<kC>();  // the peers have read c.above and the lists
-    uint32_t na = 0, nt = 0;
-    if (windows == 1) {
-        mark(0, m);
-        __syncthreads();
-        for (int i = tid; i < (m + 31) / 32; i += kPickThreads) {
-            na += __popc(taken[i]);
-            nt += __popc(equal[i]);
-        }
-    } else {
-        each_score(s, m, [&](uint32_t v) {
-            const bool t = is_taken(v);
-            na += t;
-            nt += exact && !t && v == lo;
-        });
+        clear_bins();
     }
-    uint32_t pa = 0, pt = 0;  // taken and equal in the CTAs before this one
+    if (!marked && windows == 1) mark(0, m, tv, is_taken);
+    uint32_t base = 0;  // taken in the CTAs before this one
     if constexpr (kC > 1) {
-        na = __reduce_add_sync(0xFFFFFFFFu, na);
-        nt = __reduce_add_sync(0xFFFFFFFFu, nt);
-        if (lane == 0 && na) atomicAdd(&c.above, na);
-        if (lane == 0 && nt) atomicAdd(&c.ties, nt);
-        team_sync<kC>();
-        for (int p = 0; p < rank; ++p) {
-            pa += team_load<kC>(&c.above, p);
-            pt += team_load<kC>(&c.ties, p);
+        uint32_t mine = 0;
+        if (windows == 1) {
+            __syncthreads();
+            for (int i = tid; i < (m + 31) / 32; i += kPickThreads) mine += __popc(bits[i]);
+        } else {
+            each_score<kReads>(s, m, tv, [&](uint32_t v, int i) { mine += is_taken(v, (uint32_t)(c0 + i)); });
         }
+        mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+        if (lane == 0 && mine) atomicAdd(&c.taken, mine);
+        team_sync<kC>();
+        for (int p = 0; p < rank; ++p) base += team_load<kC>(&c.taken, p);
     }
+    const uint32_t base0 = base;
+    // the blocks taken, by place: where the scores were (more of them than blocks), or behind the window's bits
+    uint32_t* blocks = (on_chip ? kept : kept + kWindowKeys / 32) - base0;
     for (int w = 0; w < windows; ++w) {
         const int w0 = w * kWindowKeys, wm = min(m - w0, kWindowKeys);
+        __syncthreads();  // the bits are written, or the window before has been written out
         if (windows > 1) {
-            __syncthreads();  // the window before has been written out
-            mark(w0, wm);
+            mark(w0, wm, tv, is_taken);
             __syncthreads();
         }
         const int words = (wm + 31) / 32;
         for (int i0 = 0; i0 < words; i0 += kPickThreads) {
             const int i = i0 + tid;
-            uint32_t a = i < words ? taken[i] : 0u, e = i < words ? equal[i] : 0u;
-            const uint32_t ca = __popc(a), ce = __popc(e);
-            uint32_t sum, sum_e;
-            const uint32_t qa = pa + cta_scan(ca, c.warp_a, &sum) - ca;
-            const uint32_t qe = exact ? pt + cta_scan(ce, c.warp_b, &sum_e) - ce : 0u;
-            if (exact) {  // the first need - qe of the word's equal scores
-                uint32_t left = need > qe ? need - qe : 0u;
-                uint32_t kept_e = 0;
-                while (e != 0u && left > 0u) {
-                    kept_e |= e & (0u - e);
-                    e &= e - 1u;
-                    --left;
-                }
-                a |= kept_e;
-                pt += sum_e;
-            }
-            uint32_t at = qa + min(qe, need);
+            uint32_t a = i < words ? bits[i] : 0u, sum;
+            uint32_t at = base + cta_scan(__popc(a), c.warp_sum, &sum) - __popc(a);
             while (a != 0u) {
                 const int key = c0 + w0 + 32 * i + __ffs(a) - 1;
                 a &= a - 1u;
-                if (sh.block == 1) {
+                if (sh.block == 1)
                     out[at] = key;
-                } else {
-                    for (int x = 0; x < sh.block; ++x) {
-                        const int token = key * sh.block + x;
-                        out[(size_t)at * sh.block + x] = token < len ? token : -1;
-                    }
-                }
+                else
+                    blocks[at] = (uint32_t)key;
                 ++at;
             }
-            pa += sum;
-            __syncthreads();  // the sums have been read
+            base += sum;
+            if (i0 + kPickThreads < words) __syncthreads();  // the sums have been read
+        }
+    }
+    if (sh.block > 1) {  // the blocks' tokens, by all threads
+        __syncthreads();
+        for (int i = (int)base0 * sh.block + tid; i < (int)base * sh.block; i += kPickThreads) {
+            const int at = i / sh.block, token = (int)blocks[at] * sh.block + (i - at * sh.block);
+            out[i] = token < len ? token : -1;
         }
     }
     if constexpr (kC > 1) tc::cluster_sync();  // the peers may still be reading this CTA's counts
@@ -840,15 +902,15 @@ cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_
     if (e != cudaSuccess) return e;
 
     // A unit's scores go to one CTA while they fit its shared memory and units fill the SMs; else a
-    // cluster shares them (never fewer than 2048 scores a CTA).
+    // cluster shares them (never fewer than 8192 scores a CTA: the cluster's barriers cost more than they save).
     int team = 1;
-    while (team < 8 && max_keys / (2 * team) >= 2048 && (max_keys / team > kStagedKeys || units * team * 2 <= device_sms)) team *= 2;
+    while (team < 8 && max_keys / (2 * team) >= 8192 && (max_keys / team > kStagedKeys || units * team * 2 <= device_sms)) team *= 2;
     const int64_t chunk = ((max_keys + team - 1) / team + 127) & ~(int64_t)127;
     const int staged = (int)std::min<int64_t>(chunk, kStagedKeys);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * team));
     cfg.blockDim = dim3(kPickThreads);
-    cfg.dynamicSmemBytes = chunk <= staged ? (size_t)staged * 4 + staged / 4 : kPickSmem;
+    cfg.dynamicSmemBytes = chunk <= staged ? (size_t)staged * 4 + staged / 8 : kPickSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

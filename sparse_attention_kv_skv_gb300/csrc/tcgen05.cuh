@@ -273,13 +273,21 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int x, 
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void tma_load4(uint32_t dst, const void* map, int x, int y, int z, int w, uint64_t* bar)
+__device__ __forceinline__ void tma_load4(uint32_t dst, const void* map, int x, int y, int z, int w, uint64_t* bar,
+                                          uint64_t policy)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
+}
+// An L2 policy for data that is read once: first to be evicted.
+__device__ __forceinline__ uint64_t evict_first_policy()
+{
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
 }
 
 // The same for 4 bytes, and for 16 bytes given as a uint4.

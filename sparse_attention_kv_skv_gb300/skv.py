@@ -174,12 +174,14 @@ def check(status: int, what: str) -> None:
         raise SkvError(status, what)
 
 
-def _stream_handle(stream) -> int:
-    """A stream argument: None -> torch's current stream; an int -> as is;
-    a torch.cuda.Stream -> its handle."""
+def _stream_handle(stream, device: int | None = None) -> int:
+    """A stream argument: None -> torch's current stream (of `device`, if given);
+    an int -> as is; a torch.cuda.Stream -> its handle."""
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if device is None:
+            return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device)  # current_stream(device).cuda_stream, in 0.1 instead of 4 us
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -335,7 +337,7 @@ class Context:
         B = req_ids.numel() if B is None else B
         scale = (1.0 / 576 ** 0.5) if sm_scale is None else sm_scale
         check(skv_attend_q4(self.h, _ptr(req_ids), B, layer, _ptr(q), _ptr(slots), _ptr(out), _ptr(lse), scale,
-                            _stream_handle(stream)), "skv_attend_q4")
+                            _stream_handle(stream, self.cfg.device)), "skv_attend_q4")
 
     def select_workspace(self, index: Index, B: int, layer: int = -1) -> int:
         """Bytes of workspace a select() of B entries needs."""
@@ -359,7 +361,7 @@ class Context:
         _need(w, 4 * units * heads, "select: w")
         _need(topk, 4 * units * self.cfg.topk, "select: topk")
         check(skv_select(self.h, index.c(heads), _ptr(req_ids), B, layer, _ptr(q), _ptr(w), _ptr(topk), _ptr(workspace),
-                         workspace.numel() * workspace.element_size(), _stream_handle(stream)), "skv_select")
+                         workspace.numel() * workspace.element_size(), _stream_handle(stream, self.cfg.device)), "skv_select")
 
     def pack_rows(self, rows, packed, values=None, stream=None) -> None:
         """bf16 rows [n][576] (rows may lie apart: rows.stride(0)) -> packed rows
@@ -371,7 +373,7 @@ class Context:
         _need(packed, 336 * n, "pack_rows: packed")
         if values is not None:
             _need(values, 1152 * n, "pack_rows: values")
-        check(skv_pack_rows(self.h, _ptr(rows), stride, n, _ptr(packed), _ptr(values), _stream_handle(stream)),
+        check(skv_pack_rows(self.h, _ptr(rows), stride, n, _ptr(packed), _ptr(values), _stream_handle(stream, self.cfg.device)),
               "skv_pack_rows")
 
     def unpack_rows(self, packed, values, stream=None) -> None:
@@ -381,7 +383,7 @@ class Context:
             raise ValueError("unpack_rows: packed must hold whole rows of 336 bytes")
         _need(packed, 336 * n, "unpack_rows: packed")
         _need(values, 1152 * n, "unpack_rows: values")
-        check(skv_unpack_rows(self.h, _ptr(packed), n, _ptr(values), _stream_handle(stream)), "skv_unpack_rows")
+        check(skv_unpack_rows(self.h, _ptr(packed), n, _ptr(values), _stream_handle(stream, self.cfg.device)), "skv_unpack_rows")
 
     def selftest_attend_timeout(self, req_ids, q, slots, out, B: int | None = None, stream=None) -> None:
         """The attention kernel with its key loads withheld: its waits run out
