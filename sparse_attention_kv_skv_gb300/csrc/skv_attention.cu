@@ -449,10 +449,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         return;  // both CTAs of the cluster see the same layout and leave together
     }
     int gtot = 0;  // blocks of this cluster's real units
-    for (int u = cl; u < units; u += ncl) {
-        int b, l;
-        if (req_of(u, b, l) >= 0) gtot += nblk;
-    }
+    auto count_blocks = [&]() {
+        for (int u = cl; u < units; u += ncl) {
+            int b, l;
+            if (req_of(u, b, l) >= 0) gtot += nblk;
+        }
+    };
+    if constexpr (!kQ4) count_blocks();
     uint8_t* sK = smem;  // key stages
     uint8_t* sX = smem + lay.off_x;
     uint8_t* sP = smem + lay.off_p;
@@ -489,7 +492,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     tc::cluster_sync();  // barriers of both CTAs exist before either sends to the other
     tc::fence_after_sync();
     const uint32_t tbase = c.tmem_base;
-    if constexpr (kQ4) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // combine_kernel, if any
+    if constexpr (kQ4) {
+        chain_next();
+        chain_wait();
+        count_blocks();
+    }
     // Register split (warpgroup-wide): softmax 192 a thread, exchange 72, MMA and loaders 88; the
     // shares fit the launch's 512 x 128 in total and on every SM sub-partition (one warp of each
     // warpgroup per sub-partition).
@@ -949,7 +956,8 @@ __global__ void __launch_bounds__(kHeads * kShares) combine_kernel(KeySplit sp, 
     const int u = blockIdx.y, c0 = blockIdx.x * kCols, hd = threadIdx.x % kHeads, g = threadIdx.x / kHeads;
     const float* ls = sp.lse + (size_t)u * sp.n * kHeads + hd;
     const float* po = sp.o + ((size_t)u * sp.n * 512 + c0) * kHeads + hd;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the splits' kernel has finished
+    chain_next();
+    chain_wait();  // the splits' kernel has finished
     float m = -INFINITY;
 #pragma unroll 4
     for (int i = g; i < sp.n; i += kShares) m = fmaxf(m, ls[(size_t)i * kHeads]);
@@ -1089,24 +1097,17 @@ cudaError_t launch_attend_q4(const void* hot_map, const Dev& d, const int32_t* r
         sp.lse = scratch + (size_t)units * sp.n * 512 * kHeads;
     }
     const int clusters = std::min(units * sp.n, pairs);
-    attend_kernel<true><<<clusters * 2, kAttnThreads, lay.bytes, st>>>(
-        *static_cast<const CUtensorMap*>(hot_map), d, req_ids, static_cast<const uint16_t*>(q), slots, static_cast<uint16_t*>(out), lse,
-        sm_scale * 1.4426950408889634f, lay, units * sp.n, 0, sp);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_chained(attend_kernel<true>, dim3((unsigned)clusters * 2), kAttnThreads, lay.bytes, st,
+                                   *static_cast<const CUtensorMap*>(hot_map), d, req_ids, static_cast<const uint16_t*>(q),
+                                   slots, static_cast<uint16_t*>(out), lse, sm_scale * 1.4426950408889634f, lay,
+                                   units * sp.n, 0, sp);
     if (e != cudaSuccess || sp.n == 1) return e;
-    // launched while the splits' kernel runs (every CTA of it lets it, once it is set up) and waits for its end
-    cudaLaunchConfig_t cfg{};
     // many splits: a thread for every fourth of them and 4 columns; few: all of them and 8 columns a thread
-    const bool many = sp.n > 8;
-    cfg.gridDim = dim3(many ? 512 / 4 : 512 / 8, (unsigned)units);
-    cfg.blockDim = dim3(many ? kHeads * 4 : kHeads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, many ? combine_kernel<4, 4> : combine_kernel<1, 8>, sp, static_cast<uint16_t*>(out), lse);
+    if (sp.n > 8)
+        return launch_chained(combine_kernel<4, 4>, dim3(512 / 4, (unsigned)units), kHeads * 4, 0, st, sp,
+                              static_cast<uint16_t*>(out), lse);
+    return launch_chained(combine_kernel<1, 8>, dim3(512 / 8, (unsigned)units), kHeads, 0, st, sp,
+                          static_cast<uint16_t*>(out), lse);
 }
 
 }  // namespace skv

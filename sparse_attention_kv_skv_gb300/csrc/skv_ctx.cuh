@@ -34,6 +34,26 @@ struct skv_ctx {
 namespace skv {
 // Sets the message returned by skv_last_cuda_error on this thread.
 void set_last_error_message(const char* msg);
+// Launches a kernel that may start while the kernel before it on the stream
+// still runs (programmatic dependent launch): it executes griddepcontrol.wait
+// in every CTA before it reads or writes global memory, and lets the next such
+// kernel start early in turn.  Hides the launch and the kernel's set-up where
+// calls follow one another; no kernel waits for one that has not started.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
 // The driver's cuTensorMapEncodeTiled, reached through the runtime's entry
 // point query (no link against the driver library).
 using TensorMapEncoder = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

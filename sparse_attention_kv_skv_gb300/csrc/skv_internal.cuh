@@ -25,6 +25,10 @@ enum : int {
 };
 enum : int { STAT_CALLS = 0, STAT_HITS = 1, STAT_MISSES = 2, STAT_WORDS = 3 };
 
+// The two halves of a chained launch (launch_chained), executed by every CTA.
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 enum : uint32_t {
     DEVERR_BAD_REQUEST = 1,
     DEVERR_BAD_INDEX = 2,

@@ -61,6 +61,8 @@ __device__ __forceinline__ uint32_t code_pair(float lo, float hi)
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint8_t* __restrict__ rows, int64_t stride, int64_t n,
                                                             uint8_t* __restrict__ packed, uint8_t* __restrict__ values)
 {
+    chain_next();
+    chain_wait();
     const int64_t row = (int64_t)blockIdx.x * kPackRows + threadIdx.x / kLanesPerRow;
     const int t = threadIdx.x % kLanesPerRow;
     const bool real = row < n;
@@ -142,6 +144,8 @@ constexpr int kRowChunks = q4::kDim / 8;           // chunks of 8 values in a ro
 __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const uint8_t* __restrict__ packed, int64_t n,
                                                                 uint4* __restrict__ values)
 {
+    chain_next();
+    chain_wait();
     const int64_t first = (int64_t)blockIdx.x * (kUnpackThreads * kUnpackEach) + threadIdx.x;
     const int64_t chunks = n * kRowChunks;
     uint32_t code[kUnpackEach], scale[kUnpackEach], eb[kUnpackEach];
@@ -168,17 +172,16 @@ __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const uint8_t* _
 
 cudaError_t launch_pack_rows(const void* rows, int64_t stride, int64_t n, void* packed, void* values, cudaStream_t st)
 {
-    pack_kernel<<<(unsigned)((n + kPackRows - 1) / kPackRows), kPackThreads, 0, st>>>(
-        static_cast<const uint8_t*>(rows), stride, n, static_cast<uint8_t*>(packed), static_cast<uint8_t*>(values));
-    return cudaGetLastError();
+    return launch_chained(pack_kernel, dim3((unsigned)((n + kPackRows - 1) / kPackRows)), kPackThreads, 0, st,
+                          static_cast<const uint8_t*>(rows), stride, n, static_cast<uint8_t*>(packed),
+                          static_cast<uint8_t*>(values));
 }
 
 cudaError_t launch_unpack_rows(const void* packed, int64_t n, void* values, cudaStream_t st)
 {
     constexpr int64_t per = kUnpackThreads * kUnpackEach;
-    unpack_kernel<<<(unsigned)((n * kRowChunks + per - 1) / per), kUnpackThreads, 0, st>>>(
-        static_cast<const uint8_t*>(packed), n, static_cast<uint4*>(values));
-    return cudaGetLastError();
+    return launch_chained(unpack_kernel, dim3((unsigned)((n * kRowChunks + per - 1) / per)), kUnpackThreads, 0, st,
+                          static_cast<const uint8_t*>(packed), n, static_cast<uint4*>(values));
 }
 
 }  // namespace skv

@@ -162,7 +162,29 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const uint32_t q_box = sh.npad * 128u, q_bytes = kBoxes * q_box;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // pick_kernel, which waits for this kernel's end
+    if (tid == 0) {
+        for (int s = 0; s < 8; ++s) {
+            tc::mbar_init(&c.full[s], 1);
+            tc::mbar_init(&c.empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&c.q_full[i], 1);
+            tc::mbar_init(&c.q_empty[i], 1);
+        }
+        for (int i = 0; i < kDepth; ++i) {
+            tc::mbar_init(&c.d_full[i], 1);
+            tc::mbar_init(&c.d_empty[i], 128);
+        }
+        c.abort = 0u;
+    }
+    // query rows behind the last head are zeros for good (a copy writes `heads` rows)
+    for (uint32_t i = tid; i < 2 * q_bytes / 16; i += kScoreThreads)
+        reinterpret_cast<uint4*>(smem + lay.off_q)[i] = make_uint4(0, 0, 0, 0);
+    tc::fence_smem_async();
+    if (warp == kMmaWarp) tc::tmem_alloc(&c.tmem_base, kTmemCols);
+    chain_next();
+    chain_wait();
+
     // the call's entries: every id an active request; how many tiles each has
     const int per = (sh.B + kScoreThreads - 1) / kScoreThreads;
     const int b0 = min(sh.B, tid * per), b1 = min(sh.B, b0 + per);
@@ -184,16 +206,15 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     if (lane == 31) c.sums[warp] = upto;
     bad = __syncthreads_or(bad);
     if (bad && blockIdx.x == 0 && tid == 0) atomicOr(&d.ctl[CTL_ERR], DEVERR_BAD_REQUEST);
-    if (__syncthreads_or(stop || bad)) return;  // pick_kernel sees the error word
+    stop = __syncthreads_or(stop || bad);  // pick_kernel sees the error word
     long long before = upto - mine, total = 0;
     for (int i = 0; i < kScoreThreads / 32; ++i) {
         if (i < warp) before += c.sums[i];
         total += c.sums[i];
     }
     const long long begin = total * sh.layers * blockIdx.x / gridDim.x;
-    const int count = (int)(total * sh.layers * (blockIdx.x + 1) / gridDim.x - begin);
-    if (count == 0) return;
-    if (begin >= before * sh.layers && begin < (before + mine) * sh.layers) {  // this thread's entries hold it
+    const int count = stop ? 0 : (int)(total * sh.layers * (blockIdx.x + 1) / gridDim.x - begin);
+    if (count > 0 && begin >= before * sh.layers && begin < (before + mine) * sh.layers) {  // this thread's entries hold it
         long long at = before * sh.layers;
         for (int b = b0; b < b1; ++b) {
             const long long t = (keys_of(d, req_ids[b], sh.block) + kTileKeys - 1) / kTileKeys;
@@ -206,26 +227,6 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
             at += t * sh.layers;
         }
     }
-    if (tid == 0) {
-        for (int s = 0; s < 8; ++s) {
-            tc::mbar_init(&c.full[s], 1);
-            tc::mbar_init(&c.empty[s], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&c.q_full[i], 1);
-            tc::mbar_init(&c.q_empty[i], 1);
-        }
-        for (int i = 0; i < kDepth; ++i) {
-            tc::mbar_init(&c.d_full[i], 1);
-            tc::mbar_init(&c.d_empty[i], 128);
-        }
-        c.abort = 0u;
-    }
-    // query rows behind the last head are zeros for good (a copy writes `heads` rows)
-    for (uint32_t i = tid; i < 2 * q_bytes / 16; i += kScoreThreads)
-        reinterpret_cast<uint4*>(smem + lay.off_q)[i] = make_uint4(0, 0, 0, 0);
-    if (warp == kMmaWarp) tc::tmem_alloc(&c.tmem_base, kTmemCols);
-    tc::fence_smem_async();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -233,7 +234,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const volatile uint32_t* abort = &c.abort;
     const int nst = lay.stages;
 
-    if (warp == kLoadWarp) {
+    if (count == 0) {
+        // no tile for this CTA
+    } else if (warp == kLoadWarp) {
         if (lane == 0) {
             Walk k(d, sh, req_ids, c.start);
             const uint64_t stream_once = tc::evict_first_policy();  // keys pass L2 by; the scores stay for pick_kernel
@@ -497,14 +500,15 @@ __global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 1) pick_kernel(Dev
     const int tid = threadIdx.x, lane = tid & 31;
     const int u = blockIdx.x / kC, rank = blockIdx.x % kC;
     int32_t* out = topk + (size_t)u * d.k;
+    chain_next();
     if (tid == 0) {
         c.lo = 0xFFFFFFFFu;
         c.hi = 0u;
         c.over = c.taken = 0u;
     }
     for (int i = tid; i < kBins; i += kPickThreads) c.hist[i] = 0u;
+    chain_wait();  // the scores (and the error word) are complete
     const int32_t r = req_ids[u / sh.layers];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores (and the error word) are complete
     const uint32_t err = d.ctl[CTL_ERR];  // the same for every CTA: nothing writes the word during this kernel
     const int len = r >= 0 && r < d.R ? (int)d.len[r] : 0, n = (len + sh.block - 1) / sh.block, nb = d.k / sh.block;
     if (err != 0u || n <= nb) {  // nothing, or everything there is
@@ -897,8 +901,7 @@ cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_
     const unsigned grid = (unsigned)std::min<int64_t>(device_sms, tiles);
     auto score = ix.dim == 64 ? (ix.relu ? score_kernel<64, true> : score_kernel<64, false>)
                               : (ix.relu ? score_kernel<128, true> : score_kernel<128, false>);
-    score<<<grid, kScoreThreads, lay.bytes, st>>>(key_map, q_map, d, req_ids, w, sh, lay, scores);
-    e = cudaGetLastError();
+    e = launch_chained(score, dim3(grid), kScoreThreads, lay.bytes, st, key_map, q_map, d, req_ids, w, sh, lay, scores);
     if (e != cudaSuccess) return e;
 
     // A unit's scores go to one CTA while they fit its shared memory and units fill the SMs; else a
