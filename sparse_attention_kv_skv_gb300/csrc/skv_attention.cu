@@ -312,8 +312,10 @@ __device__ __forceinline__ void give_up(AttnCtl& c, uint32_t* err)
 struct KeySplit {
     int n;       // splits a unit (1: the kernel writes the results itself)
     int blocks;  // key blocks a split
-    float* o;    // [units * n][512][128 heads]
+    float* o;    // [units * n][512 / 4][128 heads][4]
     float* lse;  // [units * n][128], log2 domain
+    __device__ __forceinline__ int unit(int u) const { return u / n; }               // of split u
+    __device__ __forceinline__ int block0(int u) const { return (u % n) * blocks; }  // its first key block
 };
 
 // The loaders of packed rows.  One warp (the last of the seven) gathers a block's
@@ -335,12 +337,22 @@ constexpr uint32_t kRawBytes = kBlk / 4 * kRawGroupStride;             // a raw 
 constexpr int kTaskRows = 16;
 constexpr int kTasks = kWinBoxes * (kBlk / kTaskRows);                 // warp tasks a block (20)
 
+// The slot of key `key` of block i of split u, -1 masked.
+__device__ __forceinline__ int32_t split_slot(const Dev& d, const int32_t* __restrict__ slots, const KeySplit& sp, int u,
+                                              int i, int key)
+{
+    key += (sp.block0(u) + i) * kBlk;
+    const int32_t slot = key < d.k ? slots[(size_t)sp.unit(u) * d.k + key] : -1;
+    return slot >= 0 && slot < d.S ? slot : -1;
+}
+
 // Both roles; returns false if a wait gave up.  req_of(u, b, l): the request of unit u or -1.
 template <typename ReqOf>
 __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* hot_map, const Dev& d,
                                                  const int32_t* __restrict__ slots, const KeySplit& sp, uint8_t* sK,
                                                  uint8_t* sRaw, int nst, int gtot, int units, int cl, int ncl, int h,
-                                                 int lw, int lane, const volatile uint32_t* abort, ReqOf req_of)
+                                                 int lw, int lane, const int32_t (&first_slots)[2],
+                                                 const volatile uint32_t* abort, ReqOf req_of)
 {
     if (lw == kConvWarps) {
         int g = 0;
@@ -350,14 +362,8 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
             const int32_t r = req_of(u, b, l);
             if (r < 0) continue;
             const int64_t row0 = ((int64_t)r * d.L + l) * d.S;  // the unit's first hot row
-            const int32_t* sl = slots + (size_t)(u / sp.n) * d.k;
-            const int key0 = (u % sp.n) * sp.blocks * kBlk;
-            auto fetch = [&](int i, int half) -> int32_t {
-                const int key = key0 + i * kBlk + 32 * half + lane;
-                const int32_t slot = key < d.k ? sl[key] : -1;
-                return slot >= 0 && slot < d.S ? slot : -1;
-            };
-            int32_t v0 = fetch(0, 0), v1 = fetch(0, 1);
+            auto fetch = [&](int i, int half) -> int32_t { return split_slot(d, slots, sp, u, i, 32 * half + lane); };
+            int32_t v0 = g == 0 ? first_slots[0] : fetch(0, 0), v1 = g == 0 ? first_slots[1] : fetch(0, 1);
             for (int i = 0; i < sp.blocks; ++i, ++g) {
                 const int st = g % kRawStages;
                 const int32_t n0 = i + 1 < sp.blocks ? fetch(i + 1, 0) : -1, n1 = i + 1 < sp.blocks ? fetch(i + 1, 1) : -1;
@@ -435,15 +441,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     const int k = d.k, S = d.S;
     const int nblk = kQ4 ? ks.blocks : (k + kBlk - 1) / kBlk;
     const int nsp = kQ4 ? ks.n : 1;  // `units` counts every split of a unit
+    auto unit_of = [&](int u) -> int { return kQ4 ? ks.unit(u) : u; };
     // The cluster serves units cl, cl + ncl, ... in order; blocks are numbered across them (g), so the
     // key pipeline, the exchanges and all phase arithmetic run on without a break between units.
     auto req_of = [&](int u, int& b, int& l) -> int32_t {
-        if constexpr (kQ4) u /= nsp;
+        if constexpr (kQ4) u = ks.unit(u);
         b = d.layer_sel >= 0 ? u : u / d.L;
         l = d.layer_sel >= 0 ? d.layer_sel : u % d.L;
         const int32_t r = req_ids[b];
         return r >= 0 && r < d.R ? r : -1;  // not a request: zero output (assemble would have rejected it)
     };
+    if constexpr (kQ4) chain_wait();
     if (tc::smem_u32(smem) & 1023u) {  // the swizzled key stages need 1024-byte-aligned rows of atoms
         if (tid == 0) atomicOr(&d.ctl[CTL_ERR], DEVERR_TIMEOUT);
         return;  // both CTAs of the cluster see the same layout and leave together
@@ -455,7 +463,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             if (req_of(u, b, l) >= 0) gtot += nblk;
         }
     };
-    if constexpr (!kQ4) count_blocks();
+    count_blocks();
+    int32_t first_slots[2] = {-1, -1};
+    if constexpr (kQ4) {
+        if (warp == kLoadWarp0 + kConvWarps && gtot > 0) {  // the gathering warp's first slots, while the others set up
+            int u = cl, b, l;
+            while (req_of(u, b, l) < 0) u += ncl;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) first_slots[half] = split_slot(d, slots, ks, u, 0, 32 * half + lane);
+        }
+    }
     uint8_t* sK = smem;  // key stages
     uint8_t* sX = smem + lay.off_x;
     uint8_t* sP = smem + lay.off_p;
@@ -492,11 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     tc::cluster_sync();  // barriers of both CTAs exist before either sends to the other
     tc::fence_after_sync();
     const uint32_t tbase = c.tmem_base;
-    if constexpr (kQ4) {
-        chain_next();
-        chain_wait();
-        count_blocks();
-    }
+    if constexpr (kQ4) chain_next();
     // Register split (warpgroup-wide): softmax 192 a thread, exchange 72, MMA and loaders 88; the
     // shares fit the launch's 512 x 128 in total and on every SM sub-partition (one warp of each
     // warpgroup per sub-partition).
@@ -505,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         if (kQ4 && warp >= kLoadWarp0) {
             if constexpr (kQ4) {
                 const bool ok = load_packed_keys(c, &hot_map, d, slots, ks, sK, smem + lay.off_raw, nst, gtot, units, cl, ncl,
-                                                 (int)h, warp - kLoadWarp0, lane, abort, req_of);
+                                                 (int)h, warp - kLoadWarp0, lane, first_slots, abort, req_of);
                 if (!ok && lane == 0) give_up(c, &d.ctl[CTL_ERR]);
                 __syncwarp();
             }
@@ -666,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             int b, l;
             if (req_of(u, b, l) < 0) continue;
             {   // Q of the unit: this head's 288 score dims into columns [kColQ, kColQ + 144)
-                const uint4* qr = reinterpret_cast<const uint4*>(q + ((size_t)(u / nsp) * kHeads + hd) * kDim + h * kQKHalf);
+                const uint4* qr = reinterpret_cast<const uint4*>(q + ((size_t)unit_of(u) * kHeads + hd) * kDim + h * kQKHalf);
 #pragma unroll 3
                 for (int gq = 0; gq < kQKHalf / 32; ++gq) {  // 9 groups of 16 columns
                     uint4 a = qr[4 * gq], bq = qr[4 * gq + 1], cq4 = qr[4 * gq + 2], dq = qr[4 * gq + 3];
@@ -684,7 +697,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 // warm L2 with the next unit's Q row a few blocks before it is loaded (earlier, the key rows
                 // streaming through L2 in the meantime would evict it)
                 if (i == (nblk > 3 ? nblk - 3 : 0) && u + ncl < units) {
-                    const uint8_t* nq = reinterpret_cast<const uint8_t*>(q + ((size_t)((u + ncl) / nsp) * kHeads + hd) * kDim + h * kQKHalf);
+                    const uint8_t* nq = reinterpret_cast<const uint8_t*>(q + ((size_t)unit_of(u + ncl) * kHeads + hd) * kDim + h * kQKHalf);
 #pragma unroll
                     for (int x = 0; x < 5; ++x) tc::prefetch_l2(nq + 128 * x);
                 }
@@ -751,8 +764,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 continue;
             }
             if (!ok) continue;
-            const int32_t* sl = slots + (size_t)(u / nsp) * k;
-            const int blk0 = kQ4 ? (u % nsp) * nblk : 0;  // the split's first block
+            const int32_t* sl = slots + (size_t)unit_of(u) * k;
+            const int blk0 = kQ4 ? ks.block0(u) : 0;  // the split's first block
             auto slot_of = [&](int i) -> int32_t {  // the slot of my key `lane` of block i
                 const int key = (blk0 + i) * kBlk + kHalfBlk * (int)h + lane;
                 return key < k ? sl[key] : -1;
@@ -882,13 +895,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 // has sent it the next block's maxima.  16-byte chunk c of staged row r sits at chunk
                 // position c ^ (r % 16), which keeps both passes free of bank conflicts.
                 if (nsp > 1) {
-                    // a split's result: fp32, columns outermost, so that a warp's stores are whole lines
-                    float* po = ks.o + ((size_t)u * 512 + h * kVHalf) * kHeads + hd;
+                    // a split's result: fp32, four columns of a head together, then the heads, so that a warp's
+                    // 16-byte stores are whole lines
+                    float4* po = reinterpret_cast<float4*>(ks.o) + ((size_t)u * 512 + h * kVHalf) / 4 * kHeads + hd;
                     for (int c0 = 0; c0 < kVHalf; c0 += 32) {
                         float ov[32];
                         tc::tmem_ld32(tl + kColO + (uint32_t)c0, ov);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) po[(size_t)(c0 + j) * kHeads] = ov[j] * inv;
+                        for (int j = 0; j < 32; j += 4)
+                            po[(size_t)(c0 + j) / 4 * kHeads] =
+                                make_float4(ov[j] * inv, ov[j + 1] * inv, ov[j + 2] * inv, ov[j + 3] * inv);
                     }
                     if (h == 0) ks.lse[(size_t)u * kHeads + hd] = l_all == 0.0f ? -INFINITY : m_ref + log2f(l_all);
                 }
@@ -944,61 +960,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 
 // The results of a unit's splits joined: with lse_i the splits' log2 sums and
 // M their maximum, out = sum 2^(lse_i - M) o_i / sum 2^(lse_i - M); a split without
-// a single key (lse -inf) is skipped.  One CTA per unit and kCols value columns;
-// thread (t, g) <-> head t and every kShares-th split, the shares summed through
-// shared memory in a fixed order.  Bound by latency: the loads of all of a
+// a single key (lse -inf) is skipped.  Thread (t, g) of a CTA <-> head t and, of
+// the kShares groups of threads, every kShares-th split of four value columns
+// (blockIdx.x), or, with one share, all splits of columns 4 (kGroups blockIdx.x + g).
+// Shares are summed through shared memory in a fixed order.  Bound by latency: the loads of all of a
 // thread's splits are in flight at once.
-template <int kShares, int kCols>
-__global__ void __launch_bounds__(kHeads * kShares) combine_kernel(KeySplit sp, uint16_t* __restrict__ out,
-                                                                   float* __restrict__ lse)
+template <int kShares>
+__global__ void __launch_bounds__(512) combine_kernel(KeySplit sp, uint16_t* __restrict__ out, float* __restrict__ lse)
 {
-    __shared__ float peak[kShares][kHeads], sum[kShares][kCols + 1][kHeads];
-    const int u = blockIdx.y, c0 = blockIdx.x * kCols, hd = threadIdx.x % kHeads, g = threadIdx.x / kHeads;
-    const float* ls = sp.lse + (size_t)u * sp.n * kHeads + hd;
-    const float* po = sp.o + ((size_t)u * sp.n * 512 + c0) * kHeads + hd;
+    constexpr int kGroups = 512 / kHeads;
+    static_assert(kShares == 1 || kShares == kGroups, "the groups of threads share splits or columns");
+    __shared__ float peak[kGroups][kHeads], sum[kShares > 1 ? kGroups : 1][5][kHeads];
     chain_next();
+    const int u = blockIdx.y, hd = threadIdx.x % kHeads, g = threadIdx.x / kHeads;
+    const int col4 = kShares > 1 ? blockIdx.x : kGroups * blockIdx.x + g, first = kShares > 1 ? g : 0;
+    const float* ls = sp.lse + (size_t)u * sp.n * kHeads + hd;
+    const float4* po = reinterpret_cast<const float4*>(sp.o) + ((size_t)u * sp.n * 128 + col4) * kHeads + hd;
     chain_wait();  // the splits' kernel has finished
     float m = -INFINITY;
-#pragma unroll 4
-    for (int i = g; i < sp.n; i += kShares) m = fmaxf(m, ls[(size_t)i * kHeads]);
+#pragma unroll 8
+    for (int i = first; i < sp.n; i += kShares) m = fmaxf(m, ls[(size_t)i * kHeads]);
     if constexpr (kShares > 1) {
         peak[g][hd] = m;
         __syncthreads();
 #pragma unroll
-        for (int x = 0; x < kShares; ++x) m = fmaxf(m, peak[x][hd]);
+        for (int x = 0; x < kGroups; ++x) m = fmaxf(m, peak[x][hd]);
     }
-    float acc[kCols] = {}, total = 0.0f;
-#pragma unroll 4
-    for (int i = g; i < sp.n; i += kShares) {
+    float acc[4] = {}, total = 0.0f;
+#pragma unroll 8
+    for (int i = first; i < sp.n; i += kShares) {
         const float li = ls[(size_t)i * kHeads];
-        float o[kCols];
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) o[j] = po[((size_t)i * 512 + j) * kHeads];
+        const float4 o = po[(size_t)i * 128 * kHeads];
         const bool none = li == -INFINITY;  // its o was never written
         const float w = none ? 0.0f : ex2(li - m);
         total += w;
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) acc[j] = fmaf(w, none ? 0.0f : o[j], acc[j]);
+        acc[0] = fmaf(w, none ? 0.0f : o.x, acc[0]);
+        acc[1] = fmaf(w, none ? 0.0f : o.y, acc[1]);
+        acc[2] = fmaf(w, none ? 0.0f : o.z, acc[2]);
+        acc[3] = fmaf(w, none ? 0.0f : o.w, acc[3]);
     }
     if constexpr (kShares > 1) {
-        sum[g][kCols][hd] = total;
+        sum[g][4][hd] = total;
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) sum[g][j][hd] = acc[j];
+        for (int j = 0; j < 4; ++j) sum[g][j][hd] = acc[j];
         __syncthreads();
         if (g != 0) return;
 #pragma unroll
-        for (int x = 1; x < kShares; ++x) {
-            total += sum[x][kCols][hd];
+        for (int x = 1; x < kGroups; ++x) {
+            total += sum[x][4][hd];
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) acc[j] += sum[x][j][hd];
+            for (int j = 0; j < 4; ++j) acc[j] += sum[x][j][hd];
         }
     }
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    uint16_t* o = out + ((size_t)u * kHeads + hd) * 512 + c0;
-#pragma unroll
-    for (int j = 0; j < kCols; j += 4)
-        *reinterpret_cast<uint2*>(o + j) = make_uint2(bf2(acc[j] * inv, acc[j + 1] * inv), bf2(acc[j + 2] * inv, acc[j + 3] * inv));
-    if (blockIdx.x == 0 && lse)
+    *reinterpret_cast<uint2*>(out + ((size_t)u * kHeads + hd) * 512 + 4 * col4) =
+        make_uint2(bf2(acc[0] * inv, acc[1] * inv), bf2(acc[2] * inv, acc[3] * inv));
+    if (col4 == 0 && lse)
         lse[(size_t)u * kHeads + hd] = total == 0.0f ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
 }
 
@@ -1102,12 +1119,9 @@ cudaError_t launch_attend_q4(const void* hot_map, const Dev& d, const int32_t* r
                                    slots, static_cast<uint16_t*>(out), lse, sm_scale * 1.4426950408889634f, lay,
                                    units * sp.n, 0, sp);
     if (e != cudaSuccess || sp.n == 1) return e;
-    // many splits: a thread for every fourth of them and 4 columns; few: all of them and 8 columns a thread
     if (sp.n > 8)
-        return launch_chained(combine_kernel<4, 4>, dim3(512 / 4, (unsigned)units), kHeads * 4, 0, st, sp,
-                              static_cast<uint16_t*>(out), lse);
-    return launch_chained(combine_kernel<1, 8>, dim3(512 / 8, (unsigned)units), kHeads, 0, st, sp,
-                          static_cast<uint16_t*>(out), lse);
+        return launch_chained(combine_kernel<4>, dim3(128, (unsigned)units), 512, 0, st, sp, static_cast<uint16_t*>(out), lse);
+    return launch_chained(combine_kernel<1>, dim3(32, (unsigned)units), 512, 0, st, sp, static_cast<uint16_t*>(out), lse);
 }
 
 }  // namespace skv
