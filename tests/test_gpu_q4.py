@@ -81,6 +81,28 @@ def test_unpack_reads_what_a_packed_row_stands_for(n):
         assert bool((values[n] == 7.0).all())
 
 
+@pytest.mark.parametrize("rows_at,values_at,stride", [(0, 0, 576), (8, 0, 576), (0, 8, 576), (8, 8, 584), (0, 0, 584), (0, 0, 592)])
+def test_pack_and_unpack_at_16_and_32_byte_alignment(rows_at, values_at, stride):
+    n = 77
+    bits = _bits(n, seed=7)
+    want = q4.pack(_f64(bits))
+    buf = torch.zeros(n * stride + 64, dtype=torch.bfloat16, device="cuda")
+    rows = buf[rows_at:rows_at + n * stride].view(n, stride)[:, :576]
+    rows.copy_(_bf16(bits))
+    packed = torch.zeros(n * ROW + 64, dtype=torch.uint8, device="cuda")[16:16 + n * ROW].view(n, ROW)
+    out = torch.zeros(n * 576 + 64, dtype=torch.bfloat16, device="cuda")
+    values = out[values_at:values_at + n * 576].view(n, 576)
+    with _ctx() as ctx:
+        ctx.pack_rows(rows, packed, values)
+        assert np.array_equal(packed.cpu().numpy(), want)
+        _same_values(values.view(torch.int16).cpu().numpy().view(np.uint16), q4.values(want))
+        assert not out[:values_at].any() and not out[values_at + n * 576:].any()
+        out.zero_()
+        ctx.unpack_rows(packed, values)
+        _same_values(values.view(torch.int16).cpu().numpy().view(np.uint16), q4.values(want))
+        assert not out[:values_at].any() and not out[values_at + n * 576:].any()
+
+
 def test_every_code_and_scale_unpacks_exactly():
     """All 16 codes under all e4m3 scales, at the ends of the exponent's range."""
     for e in (27, 127, 243):
