@@ -53,7 +53,8 @@ struct alignas(16) ScoreCtl {
     uint64_t full[8], empty[8];            // key stages
     uint64_t q_full[2], q_empty[2];        // query buffers
     uint64_t d_full[kDepth], d_empty[kDepth];  // products
-    float w[kGroups][kMaxHeads];           // a warpgroup's copy of its unit's weights
+    uint64_t fin;                          // every MMA this CTA issued has completed
+    alignas(16) float w[kGroups][kMaxHeads];  // a warpgroup's copy of its unit's weights, read as float4
     long long sums[kScoreThreads / 32];
     int start[3];                          // first batch entry, layer and tile of this CTA
     uint32_t tmem_base, abort;
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
             tc::mbar_init(&c.d_full[i], 1);
             tc::mbar_init(&c.d_empty[i], 128);
         }
+        tc::mbar_init(&c.fin, 1);
         c.abort = 0u;
     }
     // query rows behind the last head are zeros for good (a copy writes `heads` rows)
@@ -297,6 +299,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                 if (it + 1 < count) k.next();
             }
             if (!ok) give_up(c, &d.ctl[CTL_ERR]);
+            tc::mma_commit(&c.fin);  // no product, and no arrival of one, is left when the CTA leaves
+            if (!tc::mbar_wait(&c.fin, 0, 1u << 22)) give_up(c, &d.ctl[CTL_ERR]);
         }
     } else {
         const int grp = warp >> 2, t = tid & 127;
