@@ -380,8 +380,10 @@ SKV_API skv_status skv_unpack_rows(skv_ctx *ctx, const void *packed, int64_t n, 
 /* skv_attend over a hot buffer of packed rows: the same arguments, layouts,
  * masking, errors and ordering, with keys_j the values that the packed hot row
  * at slots[unit][j] stands for.  Requires row_bytes == SKV_Q4_ROW_BYTES.  The
- * rows are turned into bf16 on their way into shared memory (exactly), so the
- * products are skv_attend's.  When a call has fewer units than the device has
+ * rows are turned into bf16 on their way into shared memory (exactly), and P
+ * enters the value product rounded to bf16, as in skv_attend; the rest is fp32.
+ * A row whose score is a NaN (one that holds a NaN group, or a NaN in q) makes
+ * the head's out and lse NaN.  When a call has fewer units than the device has
  * SM pairs (or than skv_set_attend_sms leaves it), each unit's keys are split
  * over several pairs and the partial results, in scratch the context owns, are
  * joined by a second kernel; the sums are then taken in another order, so

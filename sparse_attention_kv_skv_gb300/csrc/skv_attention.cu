@@ -169,11 +169,15 @@ static_assert(128 * (kSoftmaxRegs + kXchgRegs + 2 * kServiceRegs) <= 65536 &&
                   32 * (kSoftmaxRegs + kXchgRegs + 2 * kServiceRegs) <= 16384,
               "the register split must fit the launch's registers, also per SM sub-partition");
 constexpr int kGathers = kBlk / 4 * kWinBoxes;           // four-row TMA copies per block (80)
-constexpr uint32_t kXBytes = kHeads * kHalfBlk * 3;      // the peer's partial scores of my keys (24-bit): 12288
-constexpr int kXChunks = kHalfBlk * 3 / 16;              // 16-byte chunks a head's partial scores take (6)
+template <bool kQ4>
+constexpr int kXChunks = kHalfBlk * (kQ4 ? 32 : 24) / 128;  // 16-byte chunks a head's partial scores of my keys take (8, 6)
+template <bool kQ4>
+constexpr uint32_t kXBytes = kHeads * kXChunks<kQ4> * 16;   // the peer's partial scores of my keys: 16384, 12288
 constexpr uint32_t kPBytes = kHeads * kBlk * 2;          // a P tile, both CTAs' halves (bf16): 16384
 constexpr uint32_t kBoxBytes = kBlk * 128;               // one column box of a key stage: 64 rows x 128 B
-constexpr uint32_t kStageBytes = kWinBoxes * kBoxBytes;  // 40960
+constexpr int kValueBoxes = kVHalf / 64;                 // column boxes of this CTA's value dims (4)
+template <bool kQ4>                                      // a key stage: 32768 (value dims), 40960
+constexpr uint32_t kStageBytes = (kQ4 ? kValueBoxes : kWinBoxes) * kBoxBytes;
 constexpr uint32_t kSmemLimit = 227 * 1024;              // dynamic shared memory a CTA may have (no static part)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;  // O 256, S 64, Q 144 columns
@@ -181,25 +185,31 @@ constexpr float kRescaleLog2 = 8.0f;                     // lazy rescale thresho
 // The same for packed rows.  P is bf16 and the sums are fp32, so a stale reference costs range, not
 // precision: with 2^24, sums of up to 4096 keys stay finite for values below 2^91.  A rescale moves the
 // whole accumulator through registers; at 192 x 8 units of 2048 keys with scores of 6 standard deviations in
-// log2, the threshold 8 costs 1.37 ms, 24 1.22 ms.
+// log2, the threshold 8 cost 1.37 ms, 24 1.22 ms.
 constexpr float kRescaleLog2Q4 = 24.0f;
 static_assert(kColQ + kQKHalf / 2 <= kTmemCols && kColS + kBlk <= kColQ, "tensor-memory columns");
 
 struct alignas(16) AttnCtl;
 // Shared-memory layout: the key stages first (1024-byte aligned for the
 // swizzle), then the two exchange tiles, the two P tiles and the control
-// block.
+// block.  Over packed rows the stages hold the value dims, and two stages share
+// a box with the 32 other dims of each; raw stages follow.
 struct AttnLayout {
     int stages;
+    uint32_t off_rest, off_raw;
     uint32_t off_x, off_p, off_ctl, bytes;
-    uint32_t off_raw;  // packed rows: the raw stages
 };
 __host__ __device__ constexpr uint32_t attend_ctl_bytes();
+template <bool kQ4>
 __host__ __device__ inline AttnLayout attend_layout(uint32_t raw_bytes = 0)
 {
     for (int st = kMaxStages;; --st) {
-        AttnLayout a{st, (uint32_t)st * kStageBytes + raw_bytes, 0, 0, 0, (uint32_t)st * kStageBytes};
-        a.off_p = a.off_x + 2 * kXBytes;
+        AttnLayout a{};
+        a.stages = st;
+        a.off_rest = (uint32_t)st * kStageBytes<kQ4>;
+        a.off_raw = a.off_rest + (kQ4 ? (st + 1) / 2 * kBoxBytes : 0);
+        a.off_x = a.off_raw + raw_bytes;
+        a.off_p = a.off_x + 2 * kXBytes<kQ4>;
         a.off_ctl = a.off_p + 2 * kPBytes;
         a.bytes = a.off_ctl + attend_ctl_bytes();
         if (a.bytes <= kSmemLimit || st == 2) return a;
@@ -230,7 +240,7 @@ struct alignas(16) AttnCtl {
     uint64_t adv[2];             // the softmax warpgroup has taken block g's row maxima (adv[g % 2]: a phase
                                  // every second block, so a waiter that falls behind by a block still sees
                                  // its phase -- a parity wait tells only the current and the previous one)
-    uint64_t x_full[2];          // the peer's partial scores of my keys of a block have arrived (12288 bytes)
+    uint64_t x_full[2];          // the peer's partial scores of my keys of a block have arrived (kXBytes)
     uint64_t m_full[2];          // the peer's row maxima of a block have arrived (512 bytes)
     uint64_t p_full[2];          // a P tile is complete: my half written, the peer's half arrived (8192 bytes)
     uint64_t pv_done[2];         // O += P V of a block has completed
@@ -266,6 +276,17 @@ __device__ __forceinline__ void issue_scores(uint32_t tbase, uint64_t dk, uint32
         tc::mma_bf16_ta(tbase + kColS, tbase + kColQ + 8u * st, dk + (((e >> 6) * kBoxBytes + (e & 63u) * 2u) >> 4),
                         idesc, st > 0 ? 1u : 0u);
     }
+}
+
+// Over packed rows this CTA's score dims are its 256 value dims, the four boxes of the stage, and 32 of
+// the last 64: half a box at `dr`, 64 bytes of every 128.
+__device__ __forceinline__ void issue_scores_q4(uint32_t tbase, uint64_t dk, uint64_t dr, uint32_t idesc)
+{
+#pragma unroll
+    for (int st = 0; st < kQKHalf / 16; ++st)
+        tc::mma_bf16_ta(tbase + kColS, tbase + kColQ + 8u * st,
+                        st < kVHalf / 16 ? dk + (((st >> 2) * kBoxBytes + (st & 3) * 32u) >> 4) : dr + (st & 3) * 2u, idesc,
+                        st > 0 ? 1u : 0u);
 }
 
 // A partial score crosses the CTA pair as the upper 24 bits of its fp32
@@ -322,21 +343,21 @@ struct KeySplit {
 // rows as they are, 336 bytes each, into a ring of raw stages with TMA
 // (tile::gather4, lane j the rows 4j..4j+3; a masked slot is an out-of-range row,
 // which reads as zeros, and so are its values); the other six turn a raw stage
-// into a key stage.  A block is 20 tasks of 16 rows by one 64-dim box of this
-// CTA's window: lane 2j + c takes 32 dims (16 bytes of codes, two scales) of
-// row j and writes them where the swizzle puts them -- a quarter warp writes
-// four rows by both halves of a 128-byte line, which the swizzle spreads over
-// all banks.  (Plain loads instead of the raw ring: 1.79 ms at 192 x 8 units of
-// 2048 keys against the ring's; the scattered 16-byte loads of a block need more lines in
+// into a key stage, in 18 tasks of 32 times 32 dims (16 bytes of codes, two
+// scales; one a lane): 16 tasks of 16 rows by one 64-dim box of this CTA's value
+// dims, and two of 32 rows by its 32 other dims, in this stage's half of a box that
+// two stages share.  The lanes write where the swizzle puts the values -- a
+// quarter warp writes four rows by both halves of a 128-byte line, or eight rows by one
+// 16-byte piece, which the swizzle spreads over all banks.  (Plain loads instead of the raw ring: 1.79 ms at 192 x 8 units of
+// 2048 keys against 1.37 in the same version; the scattered 16-byte loads of a block need more lines in
 // flight than the L1 that 227 KB of shared memory leaves, and more blocks in
 // flight make it worse.)
 constexpr int kConvWarps = kLoadWarps - 1;
 constexpr uint32_t kRawGroup = 4 * q4::kRowBytes;                      // bytes of one gather
 constexpr uint32_t kRawGroupStride = (kRawGroup + 127u) / 128u * 128u; // a TMA destination is 128-byte aligned
 constexpr uint32_t kRawBytes = kBlk / 4 * kRawGroupStride;             // a raw stage: 22528
-constexpr int kTaskRows = 16;
-constexpr int kTasks = kWinBoxes * (kBlk / kTaskRows);                 // warp tasks a block (20)
-
+constexpr int kValueTasks = kValueBoxes * (kBlk / 16), kTasks = kValueTasks + kBlk / 32;  // warp tasks a block: 16 + 2
+static_assert(kTasks % kConvWarps == 0, "every converting warp has the same number of tasks");
 // The slot of key `key` of block i of split u, -1 masked.
 __device__ __forceinline__ int32_t split_slot(const Dev& d, const int32_t* __restrict__ slots, const KeySplit& sp, int u,
                                               int i, int key)
@@ -350,7 +371,7 @@ __device__ __forceinline__ int32_t split_slot(const Dev& d, const int32_t* __res
 template <typename ReqOf>
 __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* hot_map, const Dev& d,
                                                  const int32_t* __restrict__ slots, const KeySplit& sp, uint8_t* sK,
-                                                 uint8_t* sRaw, int nst, int gtot, int units, int cl, int ncl, int h,
+                                                 uint8_t* sRest, uint8_t* sRaw, int nst, int gtot, int units, int cl, int ncl, int h,
                                                  int lw, int lane, const int32_t (&first_slots)[2],
                                                  const volatile uint32_t* abort, ReqOf req_of)
 {
@@ -397,22 +418,26 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
         const int st = g % nst, rs = g % kRawStages;
         if (g >= nst && !__all_sync(0xFFFFFFFFu, wait_phase(&c.empty[st], ((g / nst) - 1) & 1, abort))) return false;
         if (!__all_sync(0xFFFFFFFFu, wait_phase(&c.raw_full[rs], (g / kRawStages) & 1, abort))) return false;
-        uint8_t* stage = sK + st * kStageBytes;
+        uint8_t* stage = sK + st * kStageBytes<true>;
+        uint8_t* rest = sRest + (st >> 1) * kBoxBytes;
         const uint8_t* raw = sRaw + rs * kRawBytes;
-        for (int task = lw; task < kTasks; task += kConvWarps) {
-            const int row = kTaskRows * (task & 3) + (lane >> 1), box = task >> 2;
-            const int chunk = 8 * h + 2 * box + (lane & 1);  // of 32 dims, in the row
+#pragma unroll 1  // (unrolled, the tasks' reads and writes come in bursts that the products and the exchange wait for: 0.3 %)
+        for (int t = 0; t < kTasks / kConvWarps; ++t) {
+            const int task = lw + kConvWarps * t;
+            const bool value = task < kValueTasks;
+            const int row = value ? 16 * (task & 3) + (lane >> 1) : 32 * (task & 1) + lane;
+            const int half = value ? lane & 1 : st & 1;                                // of the box's 128-byte lines
+            const int chunk = value ? 8 * h + 2 * (task >> 2) + (lane & 1) : 16 + h;  // of 32 dims, in the row
             const uint8_t* p = raw + (row >> 2) * kRawGroupStride + (row & 3) * q4::kRowBytes;
             const uint4 codes = *reinterpret_cast<const uint4*>(p + 16 * chunk);
             const uint32_t scales = *reinterpret_cast<const uint16_t*>(p + q4::kScalesAt + 2 * chunk);
             const uint32_t eb = p[q4::kExpAt];
             const uint32_t f0 = q4::group_factor(scales & 0xFFu, eb), f1 = q4::group_factor(scales >> 8, eb);
             const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-            uint8_t* line = stage + box * kBoxBytes + row * 128;
+            uint8_t* line = (value ? stage + (task >> 2) * kBoxBytes : rest) + row * 128;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(line + (((4 * (lane & 1) + j) ^ (row & 7)) << 4)) =
-                    q4::decode8(w[j], j < 2 ? f0 : f1);
+                *reinterpret_cast<uint4*>(line + (((4 * half + j) ^ (row & 7)) << 4)) = q4::decode8(w[j], j < 2 ? f0 : f1);
         }
         tc::fence_smem_async();  // the tensor core reads the stage
         __syncwarp();
@@ -425,7 +450,17 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
 }
 
 // kQ4: the hot buffer holds packed rows (q4.cuh) instead of bf16 rows; the key
-// stages hold the same bf16 values either way.
+// stages hold the same bf16 values either way.  What differs besides the loaders:
+// - CTA h's score dims are its value dims [256h, 256h + 256) and [512 + 32h, 544 + 32h), so a stage holds 288 dims
+//   instead of 320: a tenth less to convert, and room for
+// - the partial scores to cross the pair as fp32.  (As 24 bits they cost lse a relative error of 2.8e-6 instead of
+//   6e-8; they would save 3.6 % of the time at 192 x 8 units of 2048 keys, where the pairs' exchange is busiest.)
+// - A NaN key makes its unit's results NaN.
+// - A call of few units splits their keys (KeySplit).
+// Measured: 1.27 ms at 192 x 8 units of 2048 keys, 691 TFLOP/s, 37 % of the tensor rate; 32 us at 21 units of 1337
+// keys, 16.7 us at one unit of 2048.  What bounds it: a block of 64 keys is a chain of dependent steps between the
+// two CTAs (scores, their exchange, maxima, P, its exchange, the value product) of 3.9K cycles, of which the products
+// fill 1.1K; there is no room in shared memory for more blocks in flight.
 template <bool kQ4>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap hot_map, Dev d, const int32_t* __restrict__ req_ids,
@@ -517,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         tc::regs_shrink<kServiceRegs>();
         if (kQ4 && warp >= kLoadWarp0) {
             if constexpr (kQ4) {
-                const bool ok = load_packed_keys(c, &hot_map, d, slots, ks, sK, smem + lay.off_raw, nst, gtot, units, cl, ncl,
+                const bool ok = load_packed_keys(c, &hot_map, d, slots, ks, sK, smem + lay.off_rest, smem + lay.off_raw, nst, gtot, units, cl, ncl,
                                                  (int)h, warp - kLoadWarp0, lane, first_slots, abort, req_of);
                 if (!ok && lane == 0) give_up(c, &d.ctl[CTL_ERR]);
                 __syncwarp();
@@ -569,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                             rr[x] = slot >= 0 ? (int)(row0 + slot) : -1;
                         }
                         if ((uint32_t)lane < mine)
-                            tc::tma_gather4(tc::smem_u32(sK + s * kStageBytes) + cb * kBoxBytes + gr * 512u, &hot_map,
+                            tc::tma_gather4(tc::smem_u32(sK + s * kStageBytes<false>) + cb * kBoxBytes + gr * 512u, &hot_map,
                                             256 * (int)h + 64 * cb, rr[0], rr[1], rr[2], rr[3], &c.full[s]);
                     }
                     if (lw == 0 && i + nst < nblk) {
@@ -616,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                         const int bb = ipv & 1, s = ipv % nst;
                         tc::fence_smem_async();  // the peer's half arrived through the generic proxy
                         tc::fence_after_sync();
-                        const uint32_t vst = aK + s * kStageBytes;  // value dims are the window's first four boxes
+                        const uint32_t vst = aK + s * kStageBytes<kQ4>;  // value dims are the window's first four boxes
 #pragma unroll
                         for (int st = 0; st < kBlk / 16; ++st)
                             tc::mma_bf16(tbase + kColO, tc::kmajor_desc(aP + bb * kPBytes + 256u * st, kBlk),
@@ -634,11 +669,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                         (js == 0 || tc::mbar_ready(tc::smem_u32(&c.s_empty), (uint32_t)(js - 1) & 1u))) {
                         const int s = js % nst;
                         tc::fence_after_sync();
-                        const uint32_t kst = aK + s * kStageBytes;
+                        const uint32_t kst = aK + s * kStageBytes<kQ4>;
                         // fully unrolled per CTA rank, so every step's descriptor is the stage's plus a
                         // constant (the MMA issue rate, not the tensor pipe, bounded this loop)
                         const uint64_t dk = tc::sw128_kmajor_desc(kst);
-                        if (h == 0)
+                        if constexpr (kQ4)
+                            issue_scores_q4(tbase, dk,
+                                            tc::sw128_kmajor_desc(tc::smem_u32(smem) + lay.off_rest + (s >> 1) * kBoxBytes + (s & 1) * 64u),
+                                            idesc_s);
+                        else if (h == 0)
                             issue_scores<0>(tbase, dk, idesc_s);
                         else
                             issue_scores<1>(tbase, dk, idesc_s);
@@ -673,16 +712,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         const uint32_t x_peer = tc::map_to_rank(tc::smem_u32(sX), peer) + (uint32_t)hd * 16u;
         const uint32_t xf0 = tc::map_to_rank(tc::smem_u32(&c.x_full[0]), peer);
         const uint32_t xf1 = tc::map_to_rank(tc::smem_u32(&c.x_full[1]), peer);
+        // the first of the score dims [32 i, 32 i + 32) of this CTA
+        auto score_dim = [&](int i) -> int {
+            if constexpr (kQ4) return i < kVHalf / 32 ? kVHalf * (int)h + 32 * i : 2 * kVHalf + 32 * (int)h;
+            return kQKHalf * (int)h + 32 * i;
+        };
         bool ok = true;
         int g0 = 0;
         for (int u = cl; ok && u < units; u += ncl) {
             int b, l;
             if (req_of(u, b, l) < 0) continue;
             {   // Q of the unit: this head's 288 score dims into columns [kColQ, kColQ + 144)
-                const uint4* qr = reinterpret_cast<const uint4*>(q + ((size_t)unit_of(u) * kHeads + hd) * kDim + h * kQKHalf);
+                const uint16_t* qrow = q + ((size_t)unit_of(u) * kHeads + hd) * kDim;
 #pragma unroll 3
                 for (int gq = 0; gq < kQKHalf / 32; ++gq) {  // 9 groups of 16 columns
-                    uint4 a = qr[4 * gq], bq = qr[4 * gq + 1], cq4 = qr[4 * gq + 2], dq = qr[4 * gq + 3];
+                    const uint4* qr = reinterpret_cast<const uint4*>(qrow + score_dim(gq));
+                    uint4 a = qr[0], bq = qr[1], cq4 = qr[2], dq = qr[3];
                     const uint32_t w0[8] = {a.x, a.y, a.z, a.w, bq.x, bq.y, bq.z, bq.w};
                     const uint32_t w1[8] = {cq4.x, cq4.y, cq4.z, cq4.w, dq.x, dq.y, dq.z, dq.w};
                     tc::tmem_st8_async(tl + kColQ + 16u * gq, w0);
@@ -697,9 +742,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 // warm L2 with the next unit's Q row a few blocks before it is loaded (earlier, the key rows
                 // streaming through L2 in the meantime would evict it)
                 if (i == (nblk > 3 ? nblk - 3 : 0) && u + ncl < units) {
-                    const uint8_t* nq = reinterpret_cast<const uint8_t*>(q + ((size_t)unit_of(u + ncl) * kHeads + hd) * kDim + h * kQKHalf);
+                    const uint16_t* nq = q + ((size_t)unit_of(u + ncl) * kHeads + hd) * kDim;
 #pragma unroll
-                    for (int x = 0; x < 5; ++x) tc::prefetch_l2(nq + 128 * x);
+                    for (int x = 0; x < 5; ++x) tc::prefetch_l2(nq + score_dim(2 * x));
                 }
                 if (g >= 2 && !(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.adv[g & 1], (uint32_t)((g - 2) >> 1) & 1u, abort))))
                     break;
@@ -709,13 +754,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 tc::tmem_ld32(tl + kColS + (uint32_t)(kHalfBlk * peer), v);
                 tc::fence_before_sync();
                 tc::mbar_arrive(&c.s_empty);
-                const uint32_t xb = x_peer + (uint32_t)(g & 1) * kXBytes;
+                const uint32_t xb = x_peer + (uint32_t)(g & 1) * kXBytes<kQ4>;
                 const uint32_t rb = (g & 1) ? xf1 : xf0;
-                uint32_t w[kXChunks * 4];
+                uint32_t w[kXChunks<kQ4> * 4];
+                if constexpr (kQ4) {
 #pragma unroll
-                for (int j = 0; j < kHalfBlk / 4; ++j) pack24(v + 4 * j, w + 3 * j);
+                    for (int j = 0; j < kHalfBlk; ++j) w[j] = __float_as_uint(v[j]);
+                } else {
 #pragma unroll
-                for (int m = 0; m < kXChunks; ++m)
+                    for (int j = 0; j < kHalfBlk / 4; ++j) pack24(v + 4 * j, w + 3 * j);
+                }
+#pragma unroll
+                for (int m = 0; m < kXChunks<kQ4>; ++m)
                     tc::st_async16u(xb + 2048u * m, make_uint4(w[4 * m], w[4 * m + 1], w[4 * m + 2], w[4 * m + 3]), rb);
             }
             g0 += nblk;
@@ -747,7 +797,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         float cur[kHalfBlk];  // my partial S of the block being processed, my keys
         bool ok = true;
         if (gtot > 0) {
-            if (tid == 0) tc::mbar_arrive_expect_tx(&c.x_full[0], kXBytes);
+            if (tid == 0) tc::mbar_arrive_expect_tx(&c.x_full[0], kXBytes<kQ4>);
             ok = own(0, cur);
         }
         int g0 = 0, n = 0;  // first block of the unit; units done
@@ -778,10 +828,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 const uint32_t ph = (uint32_t)(g >> 1) & 1u;
                 if (!(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.x_full[bb], ph, abort)))) break;
                 float sv[kHalfBlk];  // mine + the peer's partial: the full scores of my keys
-                const uint8_t* xrow = sX + bb * kXBytes + hd * 16;
-                uint32_t xw[kXChunks * 4];
+                const uint8_t* xrow = sX + bb * kXBytes<kQ4> + hd * 16;
+                uint32_t xw[kXChunks<kQ4> * 4];
 #pragma unroll
-                for (int m = 0; m < kXChunks; ++m) {
+                for (int m = 0; m < kXChunks<kQ4>; ++m) {
                     const uint4 pr = *reinterpret_cast<const uint4*>(xrow + 2048 * m);
                     xw[4 * m] = pr.x;
                     xw[4 * m + 1] = pr.y;
@@ -791,12 +841,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kHalfBlk / 4; ++j) {
                     float px[4];
-                    unpack24(xw + 3 * j, px);
+                    if constexpr (kQ4) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) px[e] = __uint_as_float(xw[4 * j + e]);
+                    } else {
+                        unpack24(xw + 3 * j, px);
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sv[4 * j + e] = cur[4 * j + e] + px[e];
                 }
                 const int32_t sp_next = i + 1 < nblk ? slot_of(i + 1) : -1;  // in flight while this block runs
-                if (g + 1 < gtot && tid == 0) tc::mbar_arrive_expect_tx(&c.x_full[bb ^ 1], kXBytes);
+                if (g + 1 < gtot && tid == 0) tc::mbar_arrive_expect_tx(&c.x_full[bb ^ 1], kXBytes<kQ4>);
                 const uint32_t vm = __ballot_sync(0xFFFFFFFFu, sp >= 0 && sp < S);
                 if (vm != 0xFFFFFFFFu) {
 #pragma unroll
@@ -849,6 +904,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                         ps[(j >> 1) & 3] += p0 + p1;
                         pk[j / 2] = bf2(p0, p1);
                     }
+                } else if constexpr (kQ4) {  // or only keys whose scores are NaN: the maxima leave those out
+#pragma unroll
+                    for (int j = 0; j < kHalfBlk; j += 2) {
+                        const float p0 = sv[j] != sv[j] ? sv[j] : 0.0f, p1 = sv[j + 1] != sv[j + 1] ? sv[j + 1] : 0.0f;
+                        ps[(j >> 1) & 3] += p0 + p1;
+                        pk[j / 2] = bf2(p0, p1);
+                    }
                 } else {
 #pragma unroll
                     for (int j = 0; j < kHalfBlk / 2; ++j) pk[j] = 0u;
@@ -885,7 +947,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             if (ok) {
                 const float l_all = h == 0 ? l_run + c.lx[hd] : c.lx[hd] + l_run;
                 tc::fence_after_sync();
-                const float inv = l_all > 0.0f ? 1.0f / l_all : 0.0f;
+                const bool none = kQ4 ? l_all == 0.0f : !(l_all > 0.0f);  // over packed rows a NaN stays one
+                const float inv = none ? 0.0f : 1.0f / l_all;
                 // O goes out through shared memory so that every store instruction writes whole rows:
                 // thread hd puts its row (this CTA's 256 value dims as bf16) into a staging area, 128
                 // columns at a time; then the warp stores its 32 rows two at a time, 16 lanes a row.
@@ -933,7 +996,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                     __syncwarp();
                 }
                 if (h == 0 && lse && nsp == 1)
-                    lse[(size_t)u * kHeads + hd] = l_all > 0.0f ? (m_ref + log2f(l_all)) * 0.69314718055994531f : -INFINITY;
+                    lse[(size_t)u * kHeads + hd] = none ? -INFINITY : (m_ref + log2f(l_all)) * 0.69314718055994531f;
                 tc::fence_before_sync();
                 tc::mbar_arrive(&c.o_free);  // the next unit's first O += P V may overwrite the accumulator
             }
@@ -964,7 +1027,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 // the kShares groups of threads, every kShares-th split of four value columns
 // (blockIdx.x), or, with one share, all splits of columns 4 (kGroups blockIdx.x + g).
 // Shares are summed through shared memory in a fixed order.  Bound by latency: the loads of all of a
-// thread's splits are in flight at once.
+// thread's splits are in flight at once.  6.5 us by itself at one unit of 2048 keys in 32 splits (8 MB of partial
+// results), 9 us at 21 units in 3; its start is hidden behind the end of the splits' kernel.
 template <int kShares>
 __global__ void __launch_bounds__(512) combine_kernel(KeySplit sp, uint16_t* __restrict__ out, float* __restrict__ lse)
 {
@@ -1021,7 +1085,7 @@ __global__ void __launch_bounds__(512) combine_kernel(KeySplit sp, uint16_t* __r
 
 }  // namespace
 
-size_t attend_smem_bytes(int) { return attend_layout().bytes; }
+size_t attend_smem_bytes(int) { return attend_layout<false>().bytes; }
 
 cudaError_t tensor_map_encoder(TensorMapEncoder* encode)
 {
@@ -1077,7 +1141,7 @@ cudaError_t launch_attend(const void* hot_map, const Dev& d, const int32_t* req_
                           const int32_t* slots, void* out, float* lse, float sm_scale, int max_sms, int device_sms,
                           cudaStream_t st, bool withhold_keys)
 {
-    const AttnLayout lay = attend_layout();
+    const AttnLayout lay = attend_layout<false>();
     if (d.k > (int)kMaxTopk || lay.bytes > kSmemLimit || device_sms < 2) return cudaErrorInvalidValue;
     // a persistent grid: one cluster per two SMs (one CTA per SM), at most one per unit
     const int units = call_units(d, B);
@@ -1097,7 +1161,7 @@ size_t attend_q4_scratch_bytes(int device_sms)
 cudaError_t launch_attend_q4(const void* hot_map, const Dev& d, const int32_t* req_ids, int B, const void* q, const int32_t* slots, void* out,
                              float* lse, float sm_scale, float* scratch, int max_sms, int device_sms, cudaStream_t st)
 {
-    const AttnLayout lay = attend_layout(kRawStages * kRawBytes);
+    const AttnLayout lay = attend_layout<true>(kRawStages * kRawBytes);
     if (d.k > (int)kMaxTopk || lay.bytes > kSmemLimit || device_sms < 2) return cudaErrorInvalidValue;
     const int units = call_units(d, B);
     const int use_sms = max_sms > 0 ? std::min(max_sms, device_sms) : device_sms;
