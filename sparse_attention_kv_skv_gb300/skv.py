@@ -174,14 +174,22 @@ def check(status: int, what: str) -> None:
         raise SkvError(status, what)
 
 
+def _raw_stream(device: int) -> int:
+    """torch.cuda.current_stream(device).cuda_stream, in 0.1 instead of 4 us (replaced by torch's own at the first call)."""
+    global _raw_stream
+    import torch
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(device)
+
+
 def _stream_handle(stream, device: int | None = None) -> int:
     """A stream argument: None -> torch's current stream (of `device`, if given);
     an int -> as is; a torch.cuda.Stream -> its handle."""
     if stream is None:
-        import torch
         if device is None:
+            import torch
             return torch.cuda.current_stream().cuda_stream
-        return torch._C._cuda_getCurrentRawStream(device)  # current_stream(device).cuda_stream, in 0.1 instead of 4 us
+        return _raw_stream(device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -198,7 +206,7 @@ def _ptr(t) -> int:
 
 
 def _need(t, nbytes: int, what: str) -> None:
-    if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+    if t.nbytes < nbytes or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous and hold {nbytes} bytes")
 
 
@@ -227,12 +235,16 @@ class Index:
         if keys.dim() != 4 or keys.stride(3) != 1 or keys.element_size() != 2 or not keys.is_floating_point():
             raise ValueError("Index: keys must be [requests][layers][keys][dim] bf16 with adjacent values")
         self.keys, self.block = keys, block
-        self._c = skv_index(keys.data_ptr(), 2 * keys.stride(0), 2 * keys.stride(1), 2 * keys.stride(2), 1, keys.shape[3],
-                            block, first, last, int(bool(relu)))
+        self.first, self.last, self.relu = first, last, int(bool(relu))
+        self._c = {}  # by heads: calls of several threads may be under way
 
     def c(self, heads: int = 1):
-        self._c.heads = heads
-        return ctypes.byref(self._c)
+        s = self._c.get(heads)
+        if s is None:
+            k = self.keys
+            s = self._c[heads] = skv_index(k.data_ptr(), 2 * k.stride(0), 2 * k.stride(1), 2 * k.stride(2), heads, k.shape[3],
+                                           self.block, self.first, self.last, self.relu)
+        return ctypes.byref(s)
 
     def fits(self, cfg: Config) -> bool:
         n = self.keys.shape
@@ -361,24 +373,24 @@ class Context:
         _need(w, 4 * units * heads, "select: w")
         _need(topk, 4 * units * self.cfg.topk, "select: topk")
         check(skv_select(self.h, index.c(heads), _ptr(req_ids), B, layer, _ptr(q), _ptr(w), _ptr(topk), _ptr(workspace),
-                         workspace.numel() * workspace.element_size(), _stream_handle(stream, self.cfg.device)), "skv_select")
+                         workspace.nbytes, _stream_handle(stream, self.cfg.device)), "skv_select")
 
     def pack_rows(self, rows, packed, values=None, stream=None) -> None:
         """bf16 rows [n][576] (rows may lie apart: rows.stride(0)) -> packed rows
         [n][336] bytes and, if given, the bf16 values they stand for [n][576]."""
-        if rows.dim() != 2 or rows.shape[1] != 576 or rows.stride(1) != 1 or rows.element_size() != 2:
+        shape, step = rows.shape, rows.stride()
+        if len(shape) != 2 or shape[1] != 576 or step[1] != 1 or rows.element_size() != 2:
             raise ValueError("pack_rows: rows must be [n][576] bf16 with adjacent values")
-        n = rows.shape[0]
-        stride = 2 * rows.stride(0) if n > 1 else 1152
+        n = shape[0]
         _need(packed, 336 * n, "pack_rows: packed")
         if values is not None:
             _need(values, 1152 * n, "pack_rows: values")
-        check(skv_pack_rows(self.h, _ptr(rows), stride, n, _ptr(packed), _ptr(values), _stream_handle(stream, self.cfg.device)),
-              "skv_pack_rows")
+        check(skv_pack_rows(self.h, rows.data_ptr(), 2 * step[0] if n > 1 else 1152, n, packed.data_ptr(),
+                            0 if values is None else values.data_ptr(), _stream_handle(stream, self.cfg.device)), "skv_pack_rows")
 
     def unpack_rows(self, packed, values, stream=None) -> None:
         """Packed rows [n][336] bytes -> the bf16 values they stand for [n][576]."""
-        n, rest = divmod(packed.numel() * packed.element_size(), 336)
+        n, rest = divmod(packed.nbytes, 336)
         if rest:
             raise ValueError("unpack_rows: packed must hold whole rows of 336 bytes")
         _need(packed, 336 * n, "unpack_rows: packed")
