@@ -705,7 +705,8 @@ bool select_shape_ok(const skv_ctx* ctx, const skv_index* ix, int32_t B, int32_t
 }
 int64_t select_bytes(const skv_ctx* ctx, const skv_index* ix, int32_t B, int32_t layer)
 {
-    return (int64_t)B * (layer < 0 ? ctx->cfg.num_layers : 1) * skv::select_stride(ctx->cfg.max_context, ix->block) * 4;
+    // a unit's scores, and the entries' lengths behind them
+    return (int64_t)B * (layer < 0 ? ctx->cfg.num_layers : 1) * skv::select_stride(ctx->cfg.max_context, ix->block) * 4 + (int64_t)B * 4;
 }
 // Strides of an axis are used only where it has more than one entry.
 bool select_stride_ok(int64_t stride, int64_t entries)

@@ -44,10 +44,10 @@ struct SelectShape {
     int64_t stride;        // scores a unit has room for
 };
 
-__device__ __forceinline__ int keys_of(const Dev& d, int32_t r, int block)
-{
-    return (int)((d.len[r] + block - 1) / block);
-}
+// (Lengths are at most 2^30.  A 64-bit division costs 0.2 us, which a call of few keys notices.)
+__device__ __forceinline__ int keys_of_len(int32_t len, int block) { return (int)(((uint32_t)len + block - 1u) / (uint32_t)block); }
+__device__ __forceinline__ int keys_of(const Dev& d, int32_t r, int block) { return keys_of_len((int32_t)d.len[r], block); }
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint32_t b) { return a >> 32 ? a / b : (uint32_t)a / b; }
 
 struct alignas(16) ScoreCtl {
     uint64_t full[8], empty[8];            // key stages
@@ -157,7 +157,7 @@ template <int kDim, bool kRelu>
 __global__ void __launch_bounds__(kScoreThreads, 1)
     score_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap q_map, Dev d,
                  const int32_t* __restrict__ req_ids, const float* __restrict__ w, SelectShape sh, ScoreLayout lay,
-                 uint32_t* __restrict__ scores)
+                 uint32_t* __restrict__ scores, int32_t* __restrict__ lens)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     ScoreCtl& c = *reinterpret_cast<ScoreCtl*>(smem + lay.off_ctl);
@@ -176,10 +176,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
         const int32_t r = req_ids[b];
-        if (r < 0 || r >= d.R || !d.active[r])
+        if (r < 0 || r >= d.R || !d.active[r]) {
             bad = true;
-        else
-            mine += (keys_of(d, r, sh.block) + kTileKeys - 1) / kTileKeys;
+        } else {
+            const int32_t len = (int32_t)d.len[r];
+            mine += (keys_of_len(len, sh.block) + kTileKeys - 1) / kTileKeys;
+            if (blockIdx.x == 0) lens[b] = len;  // for pick_kernel, which has it one read sooner
+        }
     }
     long long upto = mine;
 #pragma unroll
@@ -196,19 +199,22 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         if (i < warp) before += c.sums[i];
         total += c.sums[i];
     }
-    const long long begin = total * sh.layers * blockIdx.x / gridDim.x;
-    const int count = stop ? 0 : (int)(total * sh.layers * (blockIdx.x + 1) / gridDim.x - begin);
-    if (count > 0 && begin >= before * sh.layers && begin < (before + mine) * sh.layers) {  // this thread's entries hold it
-        long long at = before * sh.layers;
+    const uint64_t all = stop ? 0 : (uint64_t)total * sh.layers, share = divide(all, gridDim.x);
+    const uint32_t extra = (uint32_t)(all - share * gridDim.x);  // CTAs with one tile more
+    const uint64_t begin = share * blockIdx.x + min(blockIdx.x, extra);
+    const int count = (int)share + (blockIdx.x < extra ? 1 : 0);
+    if (count > 0 && begin >= (uint64_t)before * sh.layers && begin < (uint64_t)(before + mine) * sh.layers) {  // this thread's entries hold it
+        uint64_t at = (uint64_t)before * sh.layers;
         for (int b = b0; b < b1; ++b) {
-            const long long t = (keys_of(d, req_ids[b], sh.block) + kTileKeys - 1) / kTileKeys;
-            if (begin < at + t * sh.layers) {
+            const uint32_t t = per == 1 ? (uint32_t)mine : (keys_of(d, req_ids[b], sh.block) + kTileKeys - 1) / kTileKeys;
+            if (begin < at + (uint64_t)t * sh.layers) {
+                const uint64_t l = divide(begin - at, t);
                 c.start[0] = b;
-                c.start[1] = (int)((begin - at) / t);
-                c.start[2] = (int)((begin - at) % t);
+                c.start[1] = (int)l;
+                c.start[2] = (int)(begin - at - l * t);
                 break;
             }
-            at += t * sh.layers;
+            at += (uint64_t)t * sh.layers;
         }
     }
     // (The set-up stays behind the wait: with it in front, all CTAs begin to stream in the same moment, which costs
@@ -503,7 +509,7 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* warp_sum, uin
 // scores (101 MB, just written; 55 us of a call, since it starts while score_kernel ends), 86 us at 16 units of 1M (67 MB read
 // from L2 two to three times; 77 us of a call), 8.7 us at 4 units of 4K.
 template <int kC>
-__global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 1) pick_kernel(Dev d, const int32_t* __restrict__ req_ids, SelectShape sh,
+__global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 1) pick_kernel(Dev d, const int32_t* __restrict__ lens, SelectShape sh,
                                                             const uint32_t* __restrict__ scores, int staged,
                                                             int32_t* __restrict__ topk)
 {
@@ -521,9 +527,12 @@ __global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 1) pick_kernel(Dev
     }
     for (int i = tid; i < kBins; i += kPickThreads) c.hist[i] = 0u;
     chain_wait();  // the scores (and the error word) are complete
-    const int32_t r = req_ids[u / sh.layers];
+    const int len = __ldcg(lens + u / sh.layers);  // undefined if the error word is set
     const uint32_t err = d.ctl[CTL_ERR];  // the same for every CTA: nothing writes the word during this kernel
-    const int len = r >= 0 && r < d.R ? (int)d.len[r] : 0, n = (len + sh.block - 1) / sh.block, nb = d.k / sh.block;
+    // A thread's first scores, read before it is known how many there are (a unit's room is a multiple of 128).
+    uint4 first = make_uint4(0, 0, 0, 0);
+    if (kC == 1 && 4 * tid < sh.stride) first = __ldcg(reinterpret_cast<const uint4*>(scores + (size_t)u * sh.stride) + tid);
+    const int n = keys_of_len(len, sh.block), nb = d.k / sh.block;
     if (err != 0u || n <= nb) {  // nothing, or everything there is
         for (int i = rank * kPickThreads + tid; i < d.k; i += kC * kPickThreads) out[i] = err == 0u && i < len ? i : -1;
         return;
@@ -539,13 +548,14 @@ __global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 1) pick_kernel(Dev
     uint32_t lo = 0xFFFFFFFFu, hi = 0u, seen[kSample];
     if (on_chip) {
         const int m4 = m >> 2;
-#pragma unroll 8
-        for (int i = tid; i < m4; i += kPickThreads) {
-            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(s) + i);
+        auto keep = [&](uint4 v, int i) {
             reinterpret_cast<uint4*>(kept)[i] = v;
             lo = min(min(lo, v.x), min(v.y, min(v.z, v.w)));
             hi = max(max(hi, v.x), max(v.y, max(v.z, v.w)));
-        }
+        };
+        if (kC == 1 && tid < m4) keep(first, tid);
+#pragma unroll 8
+        for (int i = kC == 1 ? tid + kPickThreads : tid; i < m4; i += kPickThreads) keep(__ldcg(reinterpret_cast<const uint4*>(s) + i), i);
         const int i = 4 * m4 + tid;
         if (i < m) {
             const uint32_t v = s[i];
@@ -909,12 +919,13 @@ cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_
             return cudaErrorInvalidValue;
     }
     uint32_t* scores = static_cast<uint32_t*>(workspace);
+    int32_t* lens = reinterpret_cast<int32_t*>(scores + units * sh.stride);
     const ScoreLayout lay = score_layout(ix.dim, sh.npad);
     const int64_t tiles = units * ((max_keys + kTileKeys - 1) / kTileKeys);  // at most
     const unsigned grid = (unsigned)std::min<int64_t>(device_sms, tiles);
     auto score = ix.dim == 64 ? (ix.relu ? score_kernel<64, true> : score_kernel<64, false>)
                               : (ix.relu ? score_kernel<128, true> : score_kernel<128, false>);
-    e = launch_chained(score, dim3(grid), kScoreThreads, lay.bytes, st, key_map, q_map, d, req_ids, w, sh, lay, scores);
+    e = launch_chained(score, dim3(grid), kScoreThreads, lay.bytes, st, key_map, q_map, d, req_ids, w, sh, lay, scores, lens);
     if (e != cudaSuccess) return e;
 
     // A unit's scores go to one CTA while they fit its shared memory and units fill the SMs; else a
@@ -937,7 +948,7 @@ cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     auto pick = team == 1 ? pick_kernel<1> : team == 2 ? pick_kernel<2> : team == 4 ? pick_kernel<4> : pick_kernel<8>;
-    return cudaLaunchKernelEx(&cfg, pick, d, req_ids, sh, static_cast<const uint32_t*>(scores), staged, topk);
+    return cudaLaunchKernelEx(&cfg, pick, d, static_cast<const int32_t*>(lens), sh, static_cast<const uint32_t*>(scores), staged, topk);
 }
 
 }  // namespace skv
