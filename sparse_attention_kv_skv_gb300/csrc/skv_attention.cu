@@ -344,11 +344,13 @@ struct KeySplit {
 // (tile::gather4, lane j the rows 4j..4j+3; a masked slot is an out-of-range row,
 // which reads as zeros, and so are its values); the other six turn a raw stage
 // into a key stage, in 18 tasks of 32 times 32 dims (16 bytes of codes, two
-// scales; one a lane): 16 tasks of 16 rows by one 64-dim box of this CTA's value
+// scales; one a lane): 16 tasks of a gather's four rows by this CTA's value
 // dims, and two of 32 rows by its 32 other dims, in this stage's half of a box that
 // two stages share.  The lanes write where the swizzle puts the values -- a
 // quarter warp writes four rows by both halves of a 128-byte line, or eight rows by one
-// 16-byte piece, which the swizzle spreads over all banks.  (Plain loads instead of the raw ring: 1.79 ms at 192 x 8 units of
+// 16-byte piece, which the swizzle spreads over all banks.  (Rows 336 bytes apart are 20 banks apart, but gathers
+// start on the same bank: tasks of 16 rows by one box read scales and exponents with four-way conflicts,
+// 0.9 % at 192 x 8 units of 2048 keys.)  (Plain loads instead of the raw ring: 1.79 ms at 192 x 8 units of
 // 2048 keys against 1.37 in the same version; the scattered 16-byte loads of a block need more lines in
 // flight than the L1 that 227 KB of shared memory leaves, and more blocks in
 // flight make it worse.)
@@ -425,16 +427,18 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
         for (int t = 0; t < kTasks / kConvWarps; ++t) {
             const int task = lw + kConvWarps * t;
             const bool value = task < kValueTasks;
-            const int row = value ? 16 * (task & 3) + (lane >> 1) : 32 * (task & 1) + lane;
-            const int half = value ? lane & 1 : st & 1;                                // of the box's 128-byte lines
-            const int chunk = value ? 8 * h + 2 * (task >> 2) + (lane & 1) : 16 + h;  // of 32 dims, in the row
+            const int row = value ? 4 * task + ((lane >> 1) & 3) : 32 * (task & 1) + lane;
+            // (the last row's second half swaps boxes: its codes would share a bank with the first row's)
+            const int box = value ? (lane & 7) == 7 ? (lane >> 3) ^ 2 : lane >> 3 : 0;
+            const int half = value ? lane & 1 : st & 1;                // of the box's 128-byte lines
+            const int chunk = value ? 8 * h + 2 * box + half : 16 + h;  // of 32 dims, in the row
             const uint8_t* p = raw + (row >> 2) * kRawGroupStride + (row & 3) * q4::kRowBytes;
             const uint4 codes = *reinterpret_cast<const uint4*>(p + 16 * chunk);
             const uint32_t scales = *reinterpret_cast<const uint16_t*>(p + q4::kScalesAt + 2 * chunk);
             const uint32_t eb = p[q4::kExpAt];
             const uint32_t f0 = q4::group_factor(scales & 0xFFu, eb), f1 = q4::group_factor(scales >> 8, eb);
             const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-            uint8_t* line = (value ? stage + (task >> 2) * kBoxBytes : rest) + row * 128;
+            uint8_t* line = (value ? stage + box * kBoxBytes : rest) + row * 128;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<uint4*>(line + (((4 * half + j) ^ (row & 7)) << 4)) = q4::decode8(w[j], j < 2 ? f0 : f1);
@@ -457,7 +461,7 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
 //   6e-8; they would save 3.6 % of the time at 192 x 8 units of 2048 keys, where the pairs' exchange is busiest.)
 // - A NaN key makes its unit's results NaN.
 // - A call of few units splits their keys (KeySplit).
-// Measured: 1.27 ms at 192 x 8 units of 2048 keys, 691 TFLOP/s, 37 % of the tensor rate; 32 us at 21 units of 1337
+// Measured: 1.26 ms at 192 x 8 units of 2048 keys, 695 TFLOP/s, 37 % of the tensor rate; 32 us at 21 units of 1337
 // keys, 16.7 us at one unit of 2048.  What bounds it: a block of 64 keys is a chain of dependent steps between the
 // two CTAs (scores, their exchange, maxima, P, its exchange, the value product) of 3.9K cycles, of which the products
 // fill 1.1K; there is no room in shared memory for more blocks in flight.

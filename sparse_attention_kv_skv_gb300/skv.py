@@ -391,11 +391,11 @@ class Context:
     def unpack_rows(self, packed, values, stream=None) -> None:
         """Packed rows [n][336] bytes -> the bf16 values they stand for [n][576]."""
         n, rest = divmod(packed.nbytes, 336)
-        if rest:
-            raise ValueError("unpack_rows: packed must hold whole rows of 336 bytes")
-        _need(packed, 336 * n, "unpack_rows: packed")
+        if rest or not packed.is_contiguous():
+            raise ValueError("unpack_rows: packed must be contiguous and hold whole rows of 336 bytes")
         _need(values, 1152 * n, "unpack_rows: values")
-        check(skv_unpack_rows(self.h, _ptr(packed), n, _ptr(values), _stream_handle(stream, self.cfg.device)), "skv_unpack_rows")
+        check(skv_unpack_rows(self.h, packed.data_ptr(), n, values.data_ptr(), _stream_handle(stream, self.cfg.device)),
+              "skv_unpack_rows")
 
     def selftest_attend_timeout(self, req_ids, q, slots, out, B: int | None = None, stream=None) -> None:
         """The attention kernel with its key loads withheld: its waits run out
