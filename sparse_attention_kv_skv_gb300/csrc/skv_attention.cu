@@ -284,7 +284,7 @@ __device__ __forceinline__ void issue_scores_q4(uint32_t tbase, uint64_t dk, uin
 {
 #pragma unroll
     for (int st = 0; st < kQKHalf / 16; ++st)
-        tc::mma_bf16_ta(tbase + kColS, tbase + kColQ + 8u * st,
+        tc::mma_bf16_ta_warp(tbase + kColS, tbase + kColQ + 8u * st,
                         st < kVHalf / 16 ? dk + (((st >> 2) * kBoxBytes + (st & 3) * 32u) >> 4) : dr + (st & 3) * 2u, idesc,
                         st > 0 ? 1u : 0u);
 }
@@ -640,37 +640,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             // softmax has read the previous unit's accumulator; S(g) as soon as its keys have landed,
             // S(g-1) has been read out of tensor memory and its unit's Q is in place.  Both streams are
             // issued in order. ----
-            if (lane == 0) {
+            // (Packed rows: the whole warp walks, and a lane that is elected issues; see mma_bf16_warp.)
+            if (kQ4 || lane == 0) {
+                auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
+                    const bool r = tc::mbar_ready(tc::smem_u32(bar), parity);
+                    if constexpr (kQ4) return __all_sync(0xFFFFFFFFu, r);
+                    return r;
+                };
+                auto commit = [&](uint64_t* bar) {
+                    if constexpr (kQ4)
+                        tc::mma_commit_warp(bar);
+                    else
+                        tc::mma_commit(bar);
+                };
+                const uint32_t tb = kQ4 ? __shfl_sync(0xFFFFFFFFu, tbase, 0) : tbase;
+                const int all = kQ4 ? __shfl_sync(0xFFFFFFFFu, gtot, 0) : gtot;
                 const uint32_t idesc_s = tc::idesc_bf16_f32(kHeads, kBlk, 0);
                 const uint32_t idesc_o = tc::idesc_bf16_f32(kHeads, kVHalf, 1);
                 const uint32_t aK = tc::smem_u32(sK), aP = tc::smem_u32(sP);
                 bool ok = true;
                 int js = 0, ipv = 0, qn = 0;  // next S block, next P V block, units whose Q is in place
                 uint32_t idle = 0;
-                while (ok && ipv < gtot) {
+                while (ok && ipv < all) {
                     bool progressed = false;
                     const int pu = ipv / nblk, pi = ipv - pu * nblk;  // unit and block of the next P V
-                    if (ipv < js && tc::mbar_ready(tc::smem_u32(&c.p_full[ipv & 1]), (uint32_t)(ipv >> 1) & 1u) &&
-                        (pi > 0 || pu == 0 || tc::mbar_ready(tc::smem_u32(&c.o_free), (uint32_t)(pu - 1) & 1u))) {
+                    if (ipv < js && ready(&c.p_full[ipv & 1], (uint32_t)(ipv >> 1) & 1u) &&
+                        (pi > 0 || pu == 0 || ready(&c.o_free, (uint32_t)(pu - 1) & 1u))) {
                         const int bb = ipv & 1, s = ipv % nst;
                         tc::fence_smem_async();  // the peer's half arrived through the generic proxy
                         tc::fence_after_sync();
                         const uint32_t vst = aK + s * kStageBytes<kQ4>;  // value dims are the window's first four boxes
 #pragma unroll
                         for (int st = 0; st < kBlk / 16; ++st)
-                            tc::mma_bf16(tbase + kColO, tc::kmajor_desc(aP + bb * kPBytes + 256u * st, kBlk),
-                                         tc::sw128_mnmajor_desc(vst + 2048u * st, kBoxBytes), idesc_o,
-                                         (pi > 0 || st > 0) ? 1u : 0u);
-                        tc::mma_commit(&c.pv_done[bb]);
-                        tc::mma_commit(&c.empty[s]);
+                            (kQ4 ? tc::mma_bf16_warp : tc::mma_bf16)(
+                                tb + kColO, tc::kmajor_desc(aP + bb * kPBytes + 256u * st, kBlk),
+                                tc::sw128_mnmajor_desc(vst + 2048u * st, kBoxBytes), idesc_o, (pi > 0 || st > 0) ? 1u : 0u);
+                        commit(&c.pv_done[bb]);
+                        commit(&c.empty[s]);
                         ++ipv;
                         progressed = true;
                     }
-                    if (js < gtot && js / nblk == qn && tc::mbar_ready(tc::smem_u32(&c.q_ready), (uint32_t)qn & 1u))
+                    if (js < all && js / nblk == qn && ready(&c.q_ready, (uint32_t)qn & 1u))
                         ++qn;
-                    if (js < gtot && js / nblk < qn &&
-                        tc::mbar_ready(tc::smem_u32(&c.full[js % nst]), (uint32_t)(js / nst) & 1u) &&
-                        (js == 0 || tc::mbar_ready(tc::smem_u32(&c.s_empty), (uint32_t)(js - 1) & 1u))) {
+                    if (js < all && js / nblk < qn &&
+                        ready(&c.full[js % nst], (uint32_t)(js / nst) & 1u) &&
+                        (js == 0 || ready(&c.s_empty, (uint32_t)(js - 1) & 1u))) {
                         const int s = js % nst;
                         tc::fence_after_sync();
                         const uint32_t kst = aK + s * kStageBytes<kQ4>;
@@ -678,27 +692,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                         // constant (the MMA issue rate, not the tensor pipe, bounded this loop)
                         const uint64_t dk = tc::sw128_kmajor_desc(kst);
                         if constexpr (kQ4)
-                            issue_scores_q4(tbase, dk,
+                            issue_scores_q4(tb, dk,
                                             tc::sw128_kmajor_desc(tc::smem_u32(smem) + lay.off_rest + (s >> 1) * kBoxBytes + (s & 1) * 64u),
                                             idesc_s);
                         else if (h == 0)
-                            issue_scores<0>(tbase, dk, idesc_s);
+                            issue_scores<0>(tb, dk, idesc_s);
                         else
-                            issue_scores<1>(tbase, dk, idesc_s);
-                        tc::mma_commit(&c.s_full);
+                            issue_scores<1>(tb, dk, idesc_s);
+                        commit(&c.s_full);
                         ++js;
                         progressed = true;
                     }
                     if (progressed) {
                         idle = 0;
-                    } else if (++idle > kMaxPolls || ((idle & 255u) == 0 && *abort)) {
+                    } else if (++idle > kMaxPolls || ((idle & 255u) == 0 && (kQ4 ? __any_sync(0xFFFFFFFFu, *abort != 0u) : *abort != 0u))) {
                         ok = false;
                     } else {
                         __nanosleep(32);  // leave issue slots to the warps on this sub-partition
                     }
                 }
                 if (!ok) give_up(c, &d.ctl[CTL_ERR]);
-                tc::mma_commit(&c.fin);
+                commit(&c.fin);
                 if (!tc::mbar_wait(&c.fin, 0, kMaxPolls)) give_up(c, &d.ctl[CTL_ERR]);
             }
             __syncwarp();
