@@ -285,8 +285,8 @@ __device__ __forceinline__ void issue_scores_q4(uint32_t tbase, uint64_t dk, uin
 #pragma unroll
     for (int st = 0; st < kQKHalf / 16; ++st)
         tc::mma_bf16_ta_warp(tbase + kColS, tbase + kColQ + 8u * st,
-                        st < kVHalf / 16 ? dk + (((st >> 2) * kBoxBytes + (st & 3) * 32u) >> 4) : dr + (st & 3) * 2u, idesc,
-                        st > 0 ? 1u : 0u);
+                             st < kVHalf / 16 ? dk + (((st >> 2) * kBoxBytes + (st & 3) * 32u) >> 4) : dr + (st & 3) * 2u,
+                             idesc, st > 0 ? 1u : 0u);
 }
 
 // A partial score crosses the CTA pair as the upper 24 bits of its fp32
@@ -458,13 +458,15 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
 // - CTA h's score dims are its value dims [256h, 256h + 256) and [512 + 32h, 544 + 32h), so a stage holds 288 dims
 //   instead of 320: a tenth less to convert, and room for
 // - the partial scores to cross the pair as fp32.  (As 24 bits they cost lse a relative error of 2.8e-6 instead of
-//   6e-8; they would save 3.6 % of the time at 192 x 8 units of 2048 keys, where the pairs' exchange is busiest.)
+//   6e-8; they saved 3.6 % of the time at 192 x 8 units of 2048 keys, where the pairs' exchange is busiest.)
 // - A NaN key makes its unit's results NaN.
 // - A call of few units splits their keys (KeySplit).
-// Measured: 1.26 ms at 192 x 8 units of 2048 keys, 695 TFLOP/s, 37 % of the tensor rate; 32 us at 21 units of 1337
-// keys, 16.7 us at one unit of 2048.  What bounds it: a block of 64 keys is a chain of dependent steps between the
-// two CTAs (scores, their exchange, maxima, P, its exchange, the value product) of 3.9K cycles, of which the products
-// fill 1.1K; there is no room in shared memory for more blocks in flight.
+// - The products are issued by an elected lane of a converged warp (mma_bf16_warp): 1.26 -> 1.20 ms.
+// Measured: 1.20 ms at 192 x 8 units of 2048 keys, 729 TFLOP/s, 39 % of the tensor rate; 31 us at 21 units of 1337
+// keys, 16.5 us at one unit of 2048.  What bounds it: a block of 64 keys is a chain of dependent steps between the
+// two CTAs (scores, their exchange, maxima, P, its exchange, the value product) of 3.7K cycles, of which the tensor
+// pipe is busy 1.1K; there is no room in shared or tensor memory for more blocks in flight.  (P as an operand in
+// tensor memory 1.39 ms; a warp for each stream of products 1.41; exponentials taken while the maxima travel 1.21.)
 template <bool kQ4>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap hot_map, Dev d, const int32_t* __restrict__ req_ids,
