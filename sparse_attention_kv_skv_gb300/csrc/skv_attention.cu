@@ -416,21 +416,34 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
         __syncwarp();
         return ok;
     }
+    constexpr int kMine = kTasks / kConvWarps;  // a warp's tasks of a block
     for (int g = 0; g < gtot; ++g) {
         const int st = g % nst, rs = g % kRawStages;
-        if (g >= nst && !__all_sync(0xFFFFFFFFu, wait_phase(&c.empty[st], ((g / nst) - 1) & 1, abort))) return false;
         if (!__all_sync(0xFFFFFFFFu, wait_phase(&c.raw_full[rs], (g / kRawStages) & 1, abort))) return false;
+        // The values are made before the key stage is free (its recycling, from one block's value product to the scores
+        // of the third block after, is what the blocks' period hangs on) and only stored behind the wait.
         uint8_t* stage = sK + st * kStageBytes<true>;
         uint8_t* rest = sRest + (st >> 1) * kBoxBytes;
         const uint8_t* raw = sRaw + rs * kRawBytes;
-#pragma unroll 1  // (unrolled, the tasks' reads and writes come in bursts that the products and the exchange wait for: 0.3 %)
-        for (int t = 0; t < kTasks / kConvWarps; ++t) {
+        uint4 out[kMine][4];
+        // Where the lane's 32 values of task t go: a row's half of a box's 128-byte line.  (Worked out again for the
+        // stores: kept over the wait, the addresses cost 0.8 %.)
+        auto place = [&](int t, int& row, int& half) -> uint8_t* {
             const int task = lw + kConvWarps * t;
             const bool value = task < kValueTasks;
-            const int row = value ? 4 * task + ((lane >> 1) & 3) : 32 * (task & 1) + lane;
+            row = value ? 4 * task + ((lane >> 1) & 3) : 32 * (task & 1) + lane;
             // (the last row's second half swaps boxes: its codes would share a bank with the first row's)
             const int box = value ? (lane & 7) == 7 ? (lane >> 3) ^ 2 : lane >> 3 : 0;
-            const int half = value ? lane & 1 : st & 1;                // of the box's 128-byte lines
+            half = value ? lane & 1 : st & 1;
+            return (value ? stage + box * kBoxBytes : rest) + row * 128;
+        };
+#pragma unroll
+        for (int t = 0; t < kMine; ++t) {
+            const int task = lw + kConvWarps * t;
+            const bool value = task < kValueTasks;
+            int row, half;
+            place(t, row, half);
+            const int box = value ? (lane & 7) == 7 ? (lane >> 3) ^ 2 : lane >> 3 : 0;
             const int chunk = value ? 8 * h + 2 * box + half : 16 + h;  // of 32 dims, in the row
             const uint8_t* p = raw + (row >> 2) * kRawGroupStride + (row & 3) * q4::kRowBytes;
             const uint4 codes = *reinterpret_cast<const uint4*>(p + 16 * chunk);
@@ -438,17 +451,22 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
             const uint32_t eb = p[q4::kExpAt];
             const uint32_t f0 = q4::group_factor(scales & 0xFFu, eb), f1 = q4::group_factor(scales >> 8, eb);
             const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-            uint8_t* line = (value ? stage + box * kBoxBytes : rest) + row * 128;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(line + (((4 * half + j) ^ (row & 7)) << 4)) = q4::decode8(w[j], j < 2 ? f0 : f1);
+            for (int j = 0; j < 4; ++j) out[t][j] = q4::decode8(w[j], j < 2 ? f0 : f1);
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&c.raw_empty[rs]);
+        if (g >= nst && !__all_sync(0xFFFFFFFFu, wait_phase(&c.empty[st], ((g / nst) - 1) & 1, abort))) return false;
+#pragma unroll
+        for (int t = 0; t < kMine; ++t) {
+            int row, half;
+            uint8_t* line = place(t, row, half);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(line + (((4 * half + j) ^ (row & 7)) << 4)) = out[t][j];
         }
         tc::fence_smem_async();  // the tensor core reads the stage
         __syncwarp();
-        if (lane == 0) {
-            tc::mbar_arrive(&c.full[st]);
-            tc::mbar_arrive(&c.raw_empty[rs]);
-        }
+        if (lane == 0) tc::mbar_arrive(&c.full[st]);
     }
     return true;
 }
@@ -462,11 +480,13 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
 // - A NaN key makes its unit's results NaN.
 // - A call of few units splits their keys (KeySplit).
 // - The products are issued by an elected lane of a converged warp (mma_bf16_warp): 1.26 -> 1.20 ms.
-// Measured: 1.20 ms at 192 x 8 units of 2048 keys, 729 TFLOP/s, 39 % of the tensor rate; 31 us at 21 units of 1337
-// keys, 16.5 us at one unit of 2048.  What bounds it: a block of 64 keys is a chain of dependent steps between the
-// two CTAs (scores, their exchange, maxima, P, its exchange, the value product) of 3.7K cycles, of which the tensor
-// pipe is busy 1.1K; there is no room in shared or tensor memory for more blocks in flight.  (P as an operand in
-// tensor memory 1.39 ms; a warp for each stream of products 1.41; exponentials taken while the maxima travel 1.21.)
+// - A block's values are made before its key stage is free: 1.20 -> 1.16.
+// - The exponentials are taken while the maxima travel: 1.16 -> 1.15 (before the step above: no change).
+// Measured: 1.15 ms at 192 x 8 units of 2048 keys, 764 TFLOP/s, 41 % of the tensor rate; 31 us at 21 units of 1337
+// keys, 16.6 us at one unit of 2048.  What bounds it: a block of 64 keys is a chain of dependent steps between the
+// two CTAs (scores, their exchange, maxima, P, its exchange, the value product, the stage's next keys) of 3.5K cycles,
+// of which the tensor pipe is busy 1.1K; there is no room in shared memory for a fourth stage.  (P as an operand
+// in tensor memory 1.39 ms; a warp for each stream of products 1.41; two S in tensor memory, one exchange tile 1.17.)
 template <bool kQ4>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap hot_map, Dev d, const int32_t* __restrict__ req_ids,
@@ -889,51 +909,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                     break;
                 if (tid == 0) tc::mbar_arrive_expect_tx(&c.m_full[bb], kHeads * 4u);
                 tc::st_async4(mx_peer + (uint32_t)bb * kHeads * 4u, mloc, bb ? mf1 : mf0);
-                if (!(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.m_full[bb], ph, abort)))) break;
-                const float mb = fmaxf(mloc, c.mx[bb][hd]) * scale_log2;  // the same in both CTAs
-                tc::mbar_arrive(&c.adv[bb]);  // the exchange warpgroup may now send block g + 2
+                // The block's maxima, the reference they give and, if it rises, the accumulator on it.
                 float factor = 1.0f;
-                if (mb > m_ref + (kQ4 ? kRescaleLog2Q4 : kRescaleLog2)) {
-                    factor = m_ref == -INFINITY ? 0.0f : ex2(m_ref - mb);
-                    m_ref = mb;
-                    l_run *= factor;
-                }
-                if (i > 0 && __any_sync(0xFFFFFFFFu, factor != 1.0f)) {  // rescale this warp's rows of O
-                    if (!(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort))))
-                        break;
-                    tc::fence_after_sync();
-                    for (int c0 = 0; c0 < kVHalf; c0 += 32) {
-                        float ov[32];
-                        tc::tmem_ld32(tl + kColO + c0, ov);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) ov[j] *= factor;
-                        tc::tmem_st32(tl + kColO + c0, ov);
+                auto take_maxima = [&]() -> bool {
+                    if (!__all_sync(0xFFFFFFFFu, wait_phase(&c.m_full[bb], ph, abort))) return false;
+                    const float mb = fmaxf(mloc, c.mx[bb][hd]) * scale_log2;  // the same in both CTAs
+                    tc::mbar_arrive(&c.adv[bb]);  // the exchange warpgroup may now send block g + 2
+                    if (mb > m_ref + (kQ4 ? kRescaleLog2Q4 : kRescaleLog2)) {
+                        factor = m_ref == -INFINITY ? 0.0f : ex2(m_ref - mb);
+                        m_ref = mb;
+                        l_run *= factor;
                     }
-                    tc::fence_before_sync();
-                }
+                    if (i > 0 && __any_sync(0xFFFFFFFFu, factor != 1.0f)) {  // rescale this warp's rows of O
+                        if (!__all_sync(0xFFFFFFFFu, wait_phase(&c.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort))) return false;
+                        tc::fence_after_sync();
+                        for (int c0 = 0; c0 < kVHalf; c0 += 32) {
+                            float ov[32];
+                            tc::tmem_ld32(tl + kColO + c0, ov);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) ov[j] *= factor;
+                            tc::tmem_st32(tl + kColO + c0, ov);
+                        }
+                        tc::fence_before_sync();
+                    }
+                    return true;
+                };
                 // p = 2^(s * scale - m_ref); masked keys give 2^-inf = 0.  While no
                 // real key has been seen (m_ref = -inf for every head) all p are 0.
                 uint32_t pk[kHalfBlk / 2];
-                float ps[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (m_ref != -INFINITY) {
-                    const float neg_m = -m_ref;
+                float ps[4];
+                auto exponentials = [&]() {
 #pragma unroll
-                    for (int j = 0; j < kHalfBlk; j += 2) {
-                        const float p0 = ex2(fmaf(sv[j], scale_log2, neg_m));
-                        const float p1 = ex2(fmaf(sv[j + 1], scale_log2, neg_m));
-                        ps[(j >> 1) & 3] += p0 + p1;
-                        pk[j / 2] = bf2(p0, p1);
-                    }
-                } else if constexpr (kQ4) {  // or only keys whose scores are NaN: the maxima leave those out
+                    for (int j = 0; j < 4; ++j) ps[j] = 0.0f;
+                    if (m_ref != -INFINITY) {
+                        const float neg_m = -m_ref;
 #pragma unroll
-                    for (int j = 0; j < kHalfBlk; j += 2) {
-                        const float p0 = sv[j] != sv[j] ? sv[j] : 0.0f, p1 = sv[j + 1] != sv[j + 1] ? sv[j + 1] : 0.0f;
-                        ps[(j >> 1) & 3] += p0 + p1;
-                        pk[j / 2] = bf2(p0, p1);
+                        for (int j = 0; j < kHalfBlk; j += 2) {
+                            const float p0 = ex2(fmaf(sv[j], scale_log2, neg_m));
+                            const float p1 = ex2(fmaf(sv[j + 1], scale_log2, neg_m));
+                            ps[(j >> 1) & 3] += p0 + p1;
+                            pk[j / 2] = bf2(p0, p1);
+                        }
+                    } else if constexpr (kQ4) {  // or only keys whose scores are NaN: the maxima leave those out
+#pragma unroll
+                        for (int j = 0; j < kHalfBlk; j += 2) {
+                            const float p0 = sv[j] != sv[j] ? sv[j] : 0.0f, p1 = sv[j + 1] != sv[j + 1] ? sv[j + 1] : 0.0f;
+                            ps[(j >> 1) & 3] += p0 + p1;
+                            pk[j / 2] = bf2(p0, p1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kHalfBlk / 2; ++j) pk[j] = 0u;
                     }
+                };
+                if constexpr (kQ4) {
+                    // The reference seldom rises, so the exponentials are taken with the one there is while the
+                    // maxima travel, and again if it has risen.
+                    for (bool settled = false;; settled = true) {
+                        exponentials();
+                        if (settled || !(ok = take_maxima()) || !__any_sync(0xFFFFFFFFu, factor != 1.0f)) break;
+                    }
+                    if (!ok) break;
                 } else {
-#pragma unroll
-                    for (int j = 0; j < kHalfBlk / 2; ++j) pk[j] = 0u;
+                    if (!(ok = take_maxima())) break;
+                    exponentials();
                 }
                 l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
                 // my half of P(g): into my tile and into the peer's, at the same place (keys [32h, 32h + 32))
