@@ -283,34 +283,36 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
             }
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            Walk k(d, sh, req_ids, c.start);
-            const uint32_t idesc = tc::idesc_bf16_f32(kTileKeys, sh.npad, 0);
-            bool ok = true;
-            int units = 0;
-            for (int it = 0; it < count; ++it) {
-                if (k.fresh) {
-                    if (!(ok = wait_phase(&c.q_full[units & 1], (units >> 1) & 1, abort))) break;
-                    ++units;
-                }
-                const int s = it % nst, p = it % kDepth, qb = (units - 1) & 1;
-                if (it >= kDepth && !(ok = wait_phase(&c.d_empty[p], ((it / kDepth) - 1) & 1, abort))) break;
-                if (!(ok = wait_phase(&c.full[s], (it / nst) & 1, abort))) break;
-                tc::fence_after_sync();
-                const uint32_t ka = tc::smem_u32(smem) + s * kStageBytes, qa = tc::smem_u32(smem + lay.off_q) + qb * q_bytes;
-#pragma unroll
-                for (int st = 0; st < kDim / 16; ++st)
-                    tc::mma_bf16(tbase + p * kMaxHeads, tc::sw128_kmajor_desc(ka + (st >> 2) * kBoxBytes + (st & 3) * 32),
-                                 tc::sw128_kmajor_desc(qa + (st >> 2) * q_box + (st & 3) * 32), idesc, st > 0 ? 1u : 0u);
-                tc::mma_commit(&c.empty[s]);
-                tc::mma_commit(&c.d_full[p]);
-                if (k.last_of_unit()) tc::mma_commit(&c.q_empty[qb]);
-                if (it + 1 < count) k.next();
+        // the whole warp walks, and a lane that is elected issues (see mma_bf16_warp)
+        Walk k(d, sh, req_ids, c.start);
+        const uint32_t idesc = tc::idesc_bf16_f32(kTileKeys, sh.npad, 0), tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
+        const int all = __shfl_sync(0xFFFFFFFFu, count, 0);
+        auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, abort)); };
+        bool ok = true;
+        int units = 0;
+        for (int it = 0; it < all; ++it) {
+            if (__all_sync(0xFFFFFFFFu, k.fresh)) {
+                if (!(ok = wait(&c.q_full[units & 1], (units >> 1) & 1))) break;
+                ++units;
             }
-            if (!ok) give_up(c, &d.ctl[CTL_ERR]);
-            tc::mma_commit(&c.fin);  // no product, and no arrival of one, is left when the CTA leaves
-            if (!tc::mbar_wait(&c.fin, 0, 1u << 22)) give_up(c, &d.ctl[CTL_ERR]);
+            const int s = it % nst, p = it % kDepth, qb = (units - 1) & 1;
+            if (it >= kDepth && !(ok = wait(&c.d_empty[p], ((it / kDepth) - 1) & 1))) break;
+            if (!(ok = wait(&c.full[s], (it / nst) & 1))) break;
+            tc::fence_after_sync();
+            const uint32_t ka = tc::smem_u32(smem) + s * kStageBytes, qa = tc::smem_u32(smem + lay.off_q) + qb * q_bytes;
+#pragma unroll
+            for (int st = 0; st < kDim / 16; ++st)
+                tc::mma_bf16_warp(tb + p * kMaxHeads, tc::sw128_kmajor_desc(ka + (st >> 2) * kBoxBytes + (st & 3) * 32),
+                                  tc::sw128_kmajor_desc(qa + (st >> 2) * q_box + (st & 3) * 32), idesc, st > 0 ? 1u : 0u);
+            tc::mma_commit_warp(&c.empty[s]);
+            tc::mma_commit_warp(&c.d_full[p]);
+            if (__all_sync(0xFFFFFFFFu, k.last_of_unit())) tc::mma_commit_warp(&c.q_empty[qb]);
+            if (it + 1 < all) k.next();
         }
+        if (!ok) give_up(c, &d.ctl[CTL_ERR]);
+        tc::mma_commit_warp(&c.fin);  // no product, and no arrival of one, is left when the CTA leaves
+        if (!tc::mbar_wait(&c.fin, 0, 1u << 22)) give_up(c, &d.ctl[CTL_ERR]);
+        __syncwarp();
     } else {
         const int grp = warp >> 2, t = tid & 127;
         const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
