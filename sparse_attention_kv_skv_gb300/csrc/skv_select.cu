@@ -149,9 +149,11 @@ __device__ __forceinline__ uint32_t order_word(float s)
 // What bounds it: the keys' bytes.  128 keys of 128 dims are 32 KB, 0.73 us of
 // this SM's share of HBM; the product takes 128 x 64 x 128 multiply-adds, a fifth of
 // that, and the epilogue 64 max and fma a key.  So tiles need no reuse, only
-// enough stages in flight (6 of 32 KB at 64 heads).  Measured: 986 us at 192 x 8
-// units of 16K keys (6.17 GB, 6.25 TB/s, 92 % of a copy's rate), 693 us at 16
-// units of 1M (4.29 GB, 6.2 TB/s); 8 us at 4 units of 4K, where the set-up and one
+// enough stages in flight (6 of 32 KB at 64 heads), and the products issued at the
+// tensor pipe's rate: from a single lane, with operands that have to be moved to uniform registers
+// one by one, they were what held it back (986 us at 192 x 8 units of 16K keys).
+// Measured: 895 us there (6.17 GB, 6.9 TB/s, a copy's rate), 625 us at 16
+// units of 1M (4.29 GB, 6.9 TB/s); 7.6 us at 4 units of 4K, where the set-up and one
 // tile's way through the roles are all there is.
 template <int kDim, bool kRelu>
 __global__ void __launch_bounds__(kScoreThreads, 1)
@@ -507,11 +509,11 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* warp_sum, uin
 // scan of the words' counts gives each word its place, and the tokens come out
 // ascending without a sort.
 // Bound by latency: a unit is a chain of some twelve barriers, and three CTAs a SM (teams of eight
-// for long contexts) only hide part of it.  Measured by itself: 66 us at 192 x 8 units of 16K
-// scores (101 MB, just written; 55 us of a call, since it starts while score_kernel ends), 86 us at 16 units of 1M (67 MB read
-// from L2 two to three times; 77 us of a call), 8.7 us at 4 units of 4K.
+// for long contexts, two CTAs a SM, so that 16 teams are on the chip at once: with one they were not, 20 us more)
+// only hide part of it.  Measured by itself: 63 us at 192 x 8 units of 16K scores (101 MB, just written), of a
+// call 60; of a call of 16 units of 1M (67 MB read from L2 two to three times) 65; 7.7 us at 4 units of 4K.
 template <int kC>
-__global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 1) pick_kernel(Dev d, const int32_t* __restrict__ lens, SelectShape sh,
+__global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 2) pick_kernel(Dev d, const int32_t* __restrict__ lens, SelectShape sh,
                                                             const uint32_t* __restrict__ scores, int staged,
                                                             int32_t* __restrict__ topk)
 {
