@@ -753,9 +753,8 @@ __global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 2) pick_kernel(Dev
         const uint32_t in = c.count;
         if (need == in) {  // all of the range
             if (!keys) {
-                tv = lo - 1u;  // every score from lo on (lo > 0: fewer than n scores are taken)
-                ti = 0u;
-                if (lo == 0u) ti = 0xFFFFFFFFu, tv = 0u;
+                tv = lo;  // every score from lo on, whatever its key
+                ti = 0xFFFFFFFFu;
             } else {
                 ti = ~lo;
             }
