@@ -361,7 +361,7 @@ constexpr uint32_t kRawBytes = kBlk / 4 * kRawGroupStride;             // a raw 
 constexpr int kValueTasks = kValueBoxes * (kBlk / 16), kTasks = kValueTasks + kBlk / 32;  // warp tasks a block: 16 + 2
 static_assert(kTasks % kConvWarps == 0, "every converting warp has the same number of tasks");
 // The slot of key `key` of block i of split u, -1 masked.
-__device__ __forceinline__ int32_t split_slot(const Dev& d, const int32_t* __restrict__ slots, const KeySplit& sp, int u,
+__device__ __forceinline__ int32_t split_slot(const Dev& d, const int32_t* slots, const KeySplit& sp, int u,
                                               int i, int key)
 {
     key += (sp.block0(u) + i) * kBlk;
@@ -372,7 +372,7 @@ __device__ __forceinline__ int32_t split_slot(const Dev& d, const int32_t* __res
 // Both roles; returns false if a wait gave up.  req_of(u, b, l): the request of unit u or -1.
 template <typename ReqOf>
 __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* hot_map, const Dev& d,
-                                                 const int32_t* __restrict__ slots, const KeySplit& sp, uint8_t* sK,
+                                                 const int32_t* slots, const KeySplit& sp, uint8_t* sK,
                                                  uint8_t* sRest, uint8_t* sRaw, int nst, int gtot, int units, int cl, int ncl, int h,
                                                  int lw, int lane, const int32_t (&first_slots)[2],
                                                  const volatile uint32_t* abort, ReqOf req_of)
@@ -512,7 +512,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         const int32_t r = req_ids[b];
         return r >= 0 && r < d.R ? r : -1;  // not a request: zero output (assemble would have rejected it)
     };
-    if constexpr (kQ4) chain_wait();
+    if constexpr (kQ4) {
+        chain_wait();
+        req_ids = behind_wait(req_ids);
+        q = behind_wait(q);
+        slots = behind_wait(slots);
+    }
     if (tc::smem_u32(smem) & 1023u) {  // the swizzled key stages need 1024-byte-aligned rows of atoms
         if (tid == 0) atomicOr(&d.ctl[CTL_ERR], DEVERR_TIMEOUT);
         return;  // both CTAs of the cluster see the same layout and leave together
@@ -764,14 +769,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             if (req_of(u, b, l) < 0) continue;
             {   // Q of the unit: this head's 288 score dims into columns [kColQ, kColQ + 144)
                 const uint16_t* qrow = q + ((size_t)unit_of(u) * kHeads + hd) * kDim;
-#pragma unroll 3
-                for (int gq = 0; gq < kQKHalf / 32; ++gq) {  // 9 groups of 16 columns
-                    const uint4* qr = reinterpret_cast<const uint4*>(qrow + score_dim(gq));
-                    uint4 a = qr[0], bq = qr[1], cq4 = qr[2], dq = qr[3];
-                    const uint32_t w0[8] = {a.x, a.y, a.z, a.w, bq.x, bq.y, bq.z, bq.w};
-                    const uint32_t w1[8] = {cq4.x, cq4.y, cq4.z, cq4.w, dq.x, dq.y, dq.z, dq.w};
-                    tc::tmem_st8_async(tl + kColQ + 16u * gq, w0);
-                    tc::tmem_st8_async(tl + kColQ + 16u * gq + 8u, w1);
+#pragma unroll 1
+                for (int g3 = 0; g3 < kQKHalf / 32; g3 += 3) {  // 9 groups of 16 columns, three read at a time
+                    uint4 v[3][4];
+#pragma unroll
+                    for (int x = 0; x < 3; ++x)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) v[x][y] = reinterpret_cast<const uint4*>(qrow + score_dim(g3 + x))[y];
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) {
+                        const uint4 a = v[x][0], bq = v[x][1], cq4 = v[x][2], dq = v[x][3];
+                        const uint32_t w0[8] = {a.x, a.y, a.z, a.w, bq.x, bq.y, bq.z, bq.w};
+                        const uint32_t w1[8] = {cq4.x, cq4.y, cq4.z, cq4.w, dq.x, dq.y, dq.z, dq.w};
+                        tc::tmem_st8_async(tl + kColQ + 16u * (g3 + x), w0);
+                        tc::tmem_st8_async(tl + kColQ + 16u * (g3 + x) + 8u, w1);
+                    }
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();

@@ -36,7 +36,8 @@ namespace skv {
 void set_last_error_message(const char* msg);
 // Launches a kernel that may start while the kernel before it on the stream
 // still runs (programmatic dependent launch): it executes griddepcontrol.wait
-// in every CTA before it reads or writes global memory, and lets the next such
+// in every CTA before it reads or writes global memory (its inputs through
+// behind_wait, so that the compiler keeps to it), and lets the next such
 // kernel start early in turn.  Hides the launch and the kernel's set-up where
 // calls follow one another; no kernel waits for one that has not started.
 template <typename... P, typename... A>

@@ -28,6 +28,16 @@ enum : int { STAT_CALLS = 0, STAT_HITS = 1, STAT_MISSES = 2, STAT_WORDS = 3 };
 // The two halves of a chained launch (launch_chained), executed by every CTA.
 __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// An input of a chained kernel, for the reads behind chain_wait: until then the kernel before may still be
+// writing it.  The pointer comes out of an asm that keeps its place behind the wait, so no read through it
+// can be moved in front, and none is taken for a read of memory that nothing writes (the non-coherent path).
+template <typename T>
+__device__ __forceinline__ T* behind_wait(T* p)
+{
+    size_t at = __cvta_generic_to_global(p);
+    asm volatile("" : "+l"(at));
+    return static_cast<T*>(const_cast<void*>(static_cast<const void*>(__cvta_global_to_generic(at))));
+}
 
 enum : uint32_t {
     DEVERR_BAD_REQUEST = 1,

@@ -26,12 +26,12 @@ template <bool kWide>
 __device__ __forceinline__ void load32(const uint8_t* p, uint4& a, uint4& b)
 {
     if constexpr (kWide) {
-        asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-            : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-            : "l"(p));
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                     : "l"(p));
     } else {
-        a = __ldg(reinterpret_cast<const uint4*>(p));
-        b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+        a = reinterpret_cast<const uint4*>(p)[0];
+        b = reinterpret_cast<const uint4*>(p)[1];
     }
 }
 template <bool kWide>
@@ -86,11 +86,12 @@ __device__ __forceinline__ uint32_t code_pair(float lo, float hi)
 // lane, all requested at once.  Bound by HBM: 131072 rows with values, 346 MB, in
 // 53.5 us, 6.5 TB/s (16-byte accesses and streaming hints: 58.8 us).
 template <bool kWide>
-__global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint8_t* __restrict__ rows, int64_t stride, int64_t n,
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint8_t* rows, int64_t stride, int64_t n,
                                                             uint8_t* __restrict__ packed, uint8_t* __restrict__ values)
 {
     chain_next();
     chain_wait();
+    rows = behind_wait(rows);
     const int64_t row = (int64_t)blockIdx.x * kPackRows + threadIdx.x / kLanesPerRow;
     const int t = threadIdx.x % kLanesPerRow;
     const bool real = row < n;
@@ -165,18 +166,19 @@ constexpr int kUnpackThreads = 256;
 // rows, 195 MB, in 29.1 us, 6.7 TB/s (8 values a thread and 16-byte stores: 34.2 us;
 // two or four groups a thread: 29.8 and 31.0).
 template <bool kWide>
-__global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const uint8_t* __restrict__ packed, int64_t n,
+__global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const uint8_t* packed, int64_t n,
                                                                 uint8_t* __restrict__ values)
 {
     chain_next();
     chain_wait();
+    packed = behind_wait(packed);
     const int64_t at = (int64_t)blockIdx.x * kUnpackThreads + threadIdx.x;
     if (at >= n * q4::kGroups) return;
     const int64_t row = at / q4::kGroups;
     const int g = (int)(at - row * q4::kGroups);
     const uint8_t* p = packed + row * q4::kRowBytes;
-    const uint2 code = __ldg(reinterpret_cast<const uint2*>(p + 8 * g));
-    const uint32_t factor = q4::group_factor(__ldg(p + q4::kScalesAt + g), __ldg(p + q4::kExpAt));
+    const uint2 code = *reinterpret_cast<const uint2*>(p + 8 * g);
+    const uint32_t factor = q4::group_factor(p[q4::kScalesAt + g], p[q4::kExpAt]);
     store32<kWide>(values + at * 32, q4::decode8(code.x, factor), q4::decode8(code.y, factor));
 }
 

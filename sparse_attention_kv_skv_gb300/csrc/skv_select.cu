@@ -158,7 +158,7 @@ __device__ __forceinline__ uint32_t order_word(float s)
 template <int kDim, bool kRelu>
 __global__ void __launch_bounds__(kScoreThreads, 1)
     score_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap q_map, Dev d,
-                 const int32_t* __restrict__ req_ids, const float* __restrict__ w, SelectShape sh, ScoreLayout lay,
+                 const int32_t* req_ids, const float* w, SelectShape sh, ScoreLayout lay,
                  uint32_t* __restrict__ scores, int32_t* __restrict__ lens)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -170,6 +170,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 
     chain_next();
     chain_wait();
+    req_ids = behind_wait(req_ids);
+    w = behind_wait(w);
 
     // the call's entries: every id an active request; how many tiles each has
     const int per = (sh.B + kScoreThreads - 1) / kScoreThreads;
@@ -513,8 +515,8 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* warp_sum, uin
 // only hide part of it.  Measured by itself: 63 us at 192 x 8 units of 16K scores (101 MB, just written), of a
 // call 60; of a call of 16 units of 1M (67 MB read from L2 two to three times) 65; 7.7 us at 4 units of 4K.
 template <int kC>
-__global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 2) pick_kernel(Dev d, const int32_t* __restrict__ lens, SelectShape sh,
-                                                            const uint32_t* __restrict__ scores, int staged,
+__global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 2) pick_kernel(Dev d, const int32_t* lens, SelectShape sh,
+                                                            const uint32_t* scores, int staged,
                                                             int32_t* __restrict__ topk)
 {
     extern __shared__ __align__(16) uint32_t kept[];
@@ -531,6 +533,8 @@ __global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 2) pick_kernel(Dev
     }
     for (int i = tid; i < kBins; i += kPickThreads) c.hist[i] = 0u;
     chain_wait();  // the scores (and the error word) are complete
+    lens = behind_wait(lens);
+    scores = behind_wait(scores);
     const int len = __ldcg(lens + u / sh.layers);  // undefined if the error word is set
     const uint32_t err = d.ctl[CTL_ERR];  // the same for every CTA: nothing writes the word during this kernel
     // A thread's first scores, read before it is known how many there are (a unit's room is a multiple of 128).
