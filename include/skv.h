@@ -55,7 +55,8 @@
  * Streams and ordering.  Every call that takes a cudaStream_t only enqueues
  * work on that stream (plus, where stated, a synchronisation of it).  Calls on
  * one context must be ordered: issue them on one stream, or order the streams
- * with events.  Two overlapping calls on one context race.
+ * with events.  Two overlapping calls on one context race (but calls of
+ * skv_select may overlap one another).
  *
  * Errors.  Each call returns an skv_status.  Errors that the host can see
  * (bad handle, bad sizes, null pointers, unknown request in skv_release, no
@@ -436,8 +437,10 @@ SKV_API skv_status skv_select_workspace(skv_ctx *ctx, const skv_index *index, in
  * than once in req_ids_dev (several queries of it).  Device errors:
  * SKV_DEVERR_BAD_REQUEST for an id that is not an active request; the call then
  * (and while the error word is set) only fills topk_dev with -1.  Changes no
- * request.  The workspace is the caller's and holds nothing between calls: two
- * calls, or two captured graphs, that may run at the same time need one each.
+ * request, so calls of skv_select on one context may overlap one another; rows of a
+ * call during which another one sets the error word may be -1.  The workspace is
+ * the caller's and holds nothing between calls: two calls, or two captured
+ * graphs, that may run at the same time need one each.
  * Requires max_context <= 2^30.  B == 0 enqueues nothing.  Captures into a CUDA
  * graph. */
 SKV_API skv_status skv_select(skv_ctx *ctx, const skv_index *index, const int32_t *req_ids_dev, int32_t B, int32_t layer,

@@ -180,13 +180,14 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
         const int32_t r = req_ids[b];
+        int32_t len = 0;
         if (r < 0 || r >= d.R || !d.active[r]) {
             bad = true;
         } else {
-            const int32_t len = (int32_t)d.len[r];
+            len = (int32_t)d.len[r];
             mine += (keys_of_len(len, sh.block) + kTileKeys - 1) / kTileKeys;
-            if (blockIdx.x == 0) lens[b] = len;  // for pick_kernel, which has it one read sooner
         }
+        if (blockIdx.x == 0) lens[b] = len;  // for pick_kernel, which has it one read sooner
     }
     long long upto = mine;
 #pragma unroll
@@ -410,6 +411,7 @@ struct PickCtl {
     uint32_t over;                     // this CTA's scores above the bracket
     uint32_t taken;                    // what this CTA takes
     uint2 last;                        // (score, key) of the last block taken
+    uint32_t err;                      // the error word, read by one thread
     uint32_t warp_sum[32];
 };
 
@@ -535,14 +537,25 @@ __global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 2) pick_kernel(Dev
     chain_wait();  // the scores (and the error word) are complete
     lens = behind_wait(lens);
     scores = behind_wait(scores);
-    const int len = __ldcg(lens + u / sh.layers);  // undefined if the error word is set
-    const uint32_t err = d.ctl[CTL_ERR];  // the same for every CTA: nothing writes the word during this kernel
+    const int len = __ldcg(lens + u / sh.layers);
+    // One read a CTA, and the team goes by all of them: a call on another stream may set the word meanwhile.
+    if (tid == 0) c.err = d.ctl[CTL_ERR];
+    auto team_error = [&]() {  // behind a team_sync
+        uint32_t e = 0;
+        for (int p = 0; p < kC; ++p) e |= team_load<kC>(&c.err, p);
+        return e != 0u;
+    };
+    auto fill = [&](bool nothing) {  // -1, or everything there is
+        for (int i = rank * kPickThreads + tid; i < d.k; i += kC * kPickThreads) out[i] = !nothing && i < len ? i : -1;
+        if constexpr (kC > 1) tc::cluster_sync();  // the peers may still be reading this CTA's memory
+    };
     // A thread's first scores, read before it is known how many there are (a unit's room is a multiple of 128).
     uint4 first = make_uint4(0, 0, 0, 0);
     if (kC == 1 && 4 * tid < sh.stride) first = __ldcg(reinterpret_cast<const uint4*>(scores + (size_t)u * sh.stride) + tid);
     const int n = keys_of_len(len, sh.block), nb = d.k / sh.block;
-    if (err != 0u || n <= nb) {  // nothing, or everything there is
-        for (int i = rank * kPickThreads + tid; i < d.k; i += kC * kPickThreads) out[i] = err == 0u && i < len ? i : -1;
+    if (n <= nb) {
+        team_sync<kC>();
+        fill(team_error());
         return;
     }
     const int chunk = ((n + kC - 1) / kC + 127) & ~127;
@@ -588,6 +601,10 @@ __global__ void __launch_bounds__(kPickThreads, kC == 1 ? 3 : 2) pick_kernel(Dev
         atomicMax(&c.hi, hi);
     }
     team_sync<kC>();
+    if (team_error()) {  // (the scores may never have been written)
+        fill(true);
+        return;
+    }
     lo = c.lo;
     hi = c.hi;
     if constexpr (kC > 1) {
