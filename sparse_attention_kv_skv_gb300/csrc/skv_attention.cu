@@ -182,8 +182,12 @@ constexpr uint32_t kSmemLimit = 227 * 1024;              // dynamic shared memor
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;  // O 256, S 64, Q 144 columns
 constexpr float kRescaleLog2 = 8.0f;                     // lazy rescale threshold (factor 256)
-// The same for packed rows.  P is bf16 and the sums are fp32, so a stale reference costs range, not
-// precision: with 2^24, sums of up to 4096 keys stay finite for values below 2^91.  A rescale moves the
+// The same for packed rows.  With a stale reference the largest P of a head is not 1 but any number, off by up to
+// 2^-8 as bf16; so the output is divided by the sum of the rounded P (a head that one key dominates then
+// gives that key's values, whatever the reference), and lse comes from the sum of the unrounded ones.  The
+// second sum cost 26 us at 192 x 8 units of 2048 keys; with the sums, the scores and the exponents' arguments taken
+// two at a time (f32x2) 6 are left, 1156 against 1150.  The threshold then costs
+// range alone: with 2^24, sums of up to 4096 keys stay finite for values below 2^91.  A rescale moves the
 // whole accumulator through registers; at 192 x 8 units of 2048 keys with scores of 6 standard deviations in
 // log2, the threshold 8 cost 1.37 ms, 24 1.22 ms.
 constexpr float kRescaleLog2Q4 = 24.0f;
@@ -244,7 +248,8 @@ struct alignas(16) AttnCtl {
     uint64_t m_full[2];          // the peer's row maxima of a block have arrived (512 bytes)
     uint64_t p_full[2];          // a P tile is complete: my half written, the peer's half arrived (8192 bytes)
     uint64_t pv_done[2];         // O += P V of a block has completed
-    uint64_t l_full;             // the peer's share of the softmax denominators has arrived (512 bytes; a phase a unit)
+    uint64_t l_full;             // the peer's share of the softmax denominators has arrived (512 bytes, packed rows
+                                 // 1024; a phase a unit)
     uint64_t q_ready;            // a unit's Q is in tensor memory (a phase a unit)
     uint64_t o_free;             // the softmax has read a unit's accumulator out of tensor memory (a phase a unit)
     uint64_t raw_full[kRawStages];   // packed rows: a raw stage has landed
@@ -252,6 +257,7 @@ struct alignas(16) AttnCtl {
     uint64_t fin;                // every MMA this CTA issued has completed
     float mx[2][kHeads];         // [block parity][head] the peer's row maxima of the raw scores
     float lx[kHeads];            // [head] the peer's share of the denominator
+    float rx[kHeads];            // packed rows: the peer's share of the sum of the rounded P
     uint32_t tmem_base;
     uint32_t abort;              // a wait of this CTA gave up
 };
@@ -287,6 +293,27 @@ __device__ __forceinline__ void issue_scores_q4(uint32_t tbase, uint64_t dk, uin
         tc::mma_bf16_ta_warp(tbase + kColS, tbase + kColQ + 8u * st,
                              st < kVHalf / 16 ? dk + (((st >> 2) * kBoxBytes + (st & 3) * 32u) >> 4) : dr + (st & 3) * 2u,
                              idesc, st > 0 ? 1u : 0u);
+}
+
+// Two fp32 numbers side by side, for one instruction on both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void split(uint64_t p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 // A partial score crosses the CTA pair as the upper 24 bits of its fp32
@@ -837,6 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         const uint32_t pf0 = tc::map_to_rank(tc::smem_u32(&c.p_full[0]), peer);
         const uint32_t pf1 = tc::map_to_rank(tc::smem_u32(&c.p_full[1]), peer);
         const uint32_t lx_peer = tc::map_to_rank(tc::smem_u32(&c.lx[0]), peer) + (uint32_t)hd * 4u;
+        const uint32_t rx_peer = tc::map_to_rank(tc::smem_u32(&c.rx[0]), peer) + (uint32_t)hd * 4u;
         const uint32_t lf_peer = tc::map_to_rank(tc::smem_u32(&c.l_full), peer);
         auto own = [&](int j, float (&dst)[kHalfBlk]) -> bool {  // my keys of my partial S(j)
             if (!__all_sync(0xFFFFFFFFu, wait_phase(&c.s_full, (uint32_t)j & 1u, abort))) return false;
@@ -874,6 +902,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             };
             float m_ref = -INFINITY;  // reference maximum (log2 domain) the exponentials use; equal in both CTAs
             float l_run = 0.0f;       // this CTA's share of the softmax denominator
+            float r_run = 0.0f;       // packed rows: of the sum of P as rounded to bf16, which the output is divided by
             int32_t sp = slot_of(0);
             for (int i = 0; ok && i < nblk; ++i) {
                 const int g = g0 + i, bb = g & 1;
@@ -899,8 +928,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                     } else {
                         unpack24(xw + 3 * j, px);
                     }
+                    if constexpr (kQ4) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sv[4 * j + e] = cur[4 * j + e] + px[e];
+                        for (int e = 0; e < 4; e += 2)
+                            split(add2(pair(cur[4 * j + e], cur[4 * j + e + 1]), pair(px[e], px[e + 1])), sv[4 * j + e], sv[4 * j + e + 1]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sv[4 * j + e] = cur[4 * j + e] + px[e];
+                    }
                 }
                 const int32_t sp_next = i + 1 < nblk ? slot_of(i + 1) : -1;  // in flight while this block runs
                 if (g + 1 < gtot && tid == 0) tc::mbar_arrive_expect_tx(&c.x_full[bb ^ 1], kXBytes<kQ4>);
@@ -931,6 +966,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                         factor = m_ref == -INFINITY ? 0.0f : ex2(m_ref - mb);
                         m_ref = mb;
                         l_run *= factor;
+                        if constexpr (kQ4) r_run *= factor;
                     }
                     if (i > 0 && __any_sync(0xFFFFFFFFu, factor != 1.0f)) {  // rescale this warp's rows of O
                         if (!__all_sync(0xFFFFFFFFu, wait_phase(&c.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort))) return false;
@@ -953,7 +989,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 auto exponentials = [&]() {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) ps[j] = 0.0f;
-                    if (m_ref != -INFINITY) {
+                    if (kQ4 && m_ref != -INFINITY) {
+                        const float neg_m = -m_ref;
+                        uint64_t s2[2] = {0u, 0u};  // four sums
+#pragma unroll
+                        for (int j = 0; j < kHalfBlk; j += 2) {
+                            float a0, a1;
+                            split(fma2(pair(sv[j], sv[j + 1]), pair(scale_log2, scale_log2), pair(neg_m, neg_m)), a0, a1);
+                            const float p0 = ex2(a0), p1 = ex2(a1);
+                            s2[(j >> 1) & 1] = add2(s2[(j >> 1) & 1], pair(p0, p1));
+                            pk[j / 2] = bf2(p0, p1);
+                        }
+                        split(s2[0], ps[0], ps[1]);
+                        split(s2[1], ps[2], ps[3]);
+                    } else if (m_ref != -INFINITY) {
                         const float neg_m = -m_ref;
 #pragma unroll
                         for (int j = 0; j < kHalfBlk; j += 2) {
@@ -1007,19 +1056,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 // does not delay the release of this block's key stage.  The next unit's first S waits
                 // for that unit's Q, so it is read after this unit's epilogue instead.
                 if (g + 1 < gtot && i + 1 < nblk && !(ok = own(g + 1, cur))) break;
+                if constexpr (kQ4) {  // the sum of the rounded P, while the next block's scores travel
+                    uint64_t rs[2] = {0u, 0u};
+#pragma unroll
+                    for (int j = 0; j < kHalfBlk / 2; ++j)
+                        rs[j & 1] = add2(rs[j & 1], pair(__uint_as_float(pk[j] << 16), __uint_as_float(pk[j] & 0xFFFF0000u)));
+                    float r0, r1;
+                    split(add2(rs[0], rs[1]), r0, r1);
+                    r_run += r0 + r1;
+                }
             }
             const int gl = g0 + nblk - 1;  // the unit's last block
             // the denominator: CTA 0's share + CTA 1's share, in that order on both CTAs (sent
             // before waiting for the last O += P V, so the two waits overlap)
-            if (tid == 0) tc::mbar_arrive_expect_tx(&c.l_full, kHeads * 4u);
+            if (tid == 0) tc::mbar_arrive_expect_tx(&c.l_full, kHeads * (kQ4 ? 8u : 4u));
             tc::st_async4(lx_peer, l_run, lf_peer);
+            if constexpr (kQ4) tc::st_async4(rx_peer, r_run, lf_peer);
             if (ok) ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.pv_done[gl & 1], ((gl >> 1) & 1), abort));
             if (ok) ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.l_full, (uint32_t)n & 1u, abort));
             if (ok) {
                 const float l_all = h == 0 ? l_run + c.lx[hd] : c.lx[hd] + l_run;
                 tc::fence_after_sync();
                 const bool none = kQ4 ? l_all == 0.0f : !(l_all > 0.0f);  // over packed rows a NaN stays one
-                const float inv = none ? 0.0f : 1.0f / l_all;
+                const float sum = !kQ4 ? l_all : h == 0 ? r_run + c.rx[hd] : c.rx[hd] + r_run;
+                const float inv = none ? 0.0f : 1.0f / sum;
                 // O goes out through shared memory so that every store instruction writes whole rows:
                 // thread hd puts its row (this CTA's 256 value dims as bf16) into a staging area, 128
                 // columns at a time; then the warp stores its 32 rows two at a time, 16 lanes a row.
