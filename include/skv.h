@@ -383,7 +383,8 @@ SKV_API skv_status skv_unpack_rows(skv_ctx *ctx, const void *packed, int64_t n, 
  * at slots[unit][j] stands for.  Requires row_bytes == SKV_Q4_ROW_BYTES.  The
  * rows are turned into bf16 on their way into shared memory (exactly), and P
  * enters the value product rounded to bf16, as in skv_attend; the output is divided by
- * the sum of the rounded P, lse is that of the unrounded ones; the rest is fp32.
+ * the sum of the rounded P, lse is that of the unrounded ones; the rest is fp32.  Sums stay finite
+ * for values below 2^107 in size, as in skv_attend.
  * A row whose score is a NaN (one that holds a NaN group, or a NaN in q) makes
  * the head's out and lse NaN.  When a call has fewer units than the device has
  * SM pairs (or than skv_set_attend_sms leaves it), each unit's keys are split

@@ -186,11 +186,12 @@ constexpr float kRescaleLog2 = 8.0f;                     // lazy rescale thresho
 // 2^-8 as bf16; so the output is divided by the sum of the rounded P (a head that one key dominates then
 // gives that key's values, whatever the reference), and lse comes from the sum of the unrounded ones.  The
 // second sum cost 26 us at 192 x 8 units of 2048 keys; with the sums, the scores and the exponents' arguments taken
-// two at a time (f32x2) 6 are left, 1156 against 1150.  The threshold then costs
-// range alone: with 2^24, sums of up to 4096 keys stay finite for values below 2^91.  A rescale moves the
+// two at a time (f32x2) 6 are left, 1156 against 1150.  A rescale moves the
 // whole accumulator through registers; at 192 x 8 units of 2048 keys with scores of 6 standard deviations in
-// log2, the threshold 8 cost 1.37 ms, 24 1.22 ms.
-constexpr float kRescaleLog2Q4 = 24.0f;
+// log2, a rise of 8 cost 1.37 ms, of 24 1.22 ms.  The reference is set 16 above the maximum it is taken from, so
+// that P stays at most 2^8 all the same, and sums of up to 4096 keys are finite for values below 2^107, as
+// in the kernel of bf16 rows.  (Weights below 2^-110 of the largest become 0 instead of those below 2^-126.)
+constexpr float kRiseLog2 = 24.0f, kReferenceAbove = kRiseLog2 - kRescaleLog2;
 static_assert(kColQ + kQKHalf / 2 <= kTmemCols && kColS + kBlk <= kColQ, "tensor-memory columns");
 
 struct alignas(16) AttnCtl;
@@ -962,9 +963,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                     if (!__all_sync(0xFFFFFFFFu, wait_phase(&c.m_full[bb], ph, abort))) return false;
                     const float mb = fmaxf(mloc, c.mx[bb][hd]) * scale_log2;  // the same in both CTAs
                     tc::mbar_arrive(&c.adv[bb]);  // the exchange warpgroup may now send block g + 2
-                    if (mb > m_ref + (kQ4 ? kRescaleLog2Q4 : kRescaleLog2)) {
-                        factor = m_ref == -INFINITY ? 0.0f : ex2(m_ref - mb);
-                        m_ref = mb;
+                    if (mb > m_ref + kRescaleLog2) {
+                        const float ref = kQ4 ? mb + kReferenceAbove : mb;
+                        factor = m_ref == -INFINITY ? 0.0f : ex2(m_ref - ref);
+                        m_ref = ref;
                         l_run *= factor;
                         if constexpr (kQ4) r_run *= factor;
                     }
@@ -1080,6 +1082,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 const bool none = kQ4 ? l_all == 0.0f : !(l_all > 0.0f);  // over packed rows a NaN stays one
                 const float sum = !kQ4 ? l_all : h == 0 ? r_run + c.rx[hd] : c.rx[hd] + r_run;
                 const float inv = none ? 0.0f : 1.0f / sum;
+                // (two numbers of lse's own size are added, not one 16 above it)
+                const float lse2 = kQ4 ? (m_ref - kReferenceAbove) + log2f(l_all * exp2f(kReferenceAbove)) : m_ref + log2f(l_all);
                 // O goes out through shared memory so that every store instruction writes whole rows:
                 // thread hd puts its row (this CTA's 256 value dims as bf16) into a staging area, 128
                 // columns at a time; then the warp stores its 32 rows two at a time, 16 lanes a row.
@@ -1100,7 +1104,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                             po[(size_t)(c0 + j) / 4 * kHeads] =
                                 make_float4(ov[j] * inv, ov[j + 1] * inv, ov[j + 2] * inv, ov[j + 3] * inv);
                     }
-                    if (h == 0) ks.lse[(size_t)u * kHeads + hd] = l_all == 0.0f ? -INFINITY : m_ref + log2f(l_all);
+                    if (h == 0) ks.lse[(size_t)u * kHeads + hd] = l_all == 0.0f ? -INFINITY : lse2;
                 }
                 uint8_t* stage = sP + 4096u * (uint32_t)warp;
                 uint16_t* orow = out + ((size_t)u * kHeads + (hd & ~31)) * 512 + h * kVHalf;  // the warp's first row
@@ -1127,7 +1131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                     __syncwarp();
                 }
                 if (h == 0 && lse && nsp == 1)
-                    lse[(size_t)u * kHeads + hd] = none ? -INFINITY : (m_ref + log2f(l_all)) * 0.69314718055994531f;
+                    lse[(size_t)u * kHeads + hd] = none ? -INFINITY : lse2 * 0.69314718055994531f;
                 tc::fence_before_sync();
                 tc::mbar_arrive(&c.o_free);  // the next unit's first O += P V may overwrite the accumulator
             }

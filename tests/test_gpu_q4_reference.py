@@ -157,3 +157,22 @@ def test_rows_as_a_cache_holds_them_within_the_tight_bound(scale, sms):
     for n in range(2):
         check(q[n], q4.values(packed[n, 0]), scale, out[n], lse[n], n)
     u.ctx.close()
+
+
+@pytest.mark.parametrize("sms", [2, 0])
+@pytest.mark.parametrize("rise", [20, 23.9, 24.1, 40])
+def test_large_values_under_a_stale_reference_stay_finite(rise, sms):
+    """Values up to 2^103.5, eight of whose keys rise by `rise` above the reference of the block before: under that
+    reference their sum of P v would pass the range of fp32 at 2^23.9, under one that keeps P at 2^8 it does not."""
+    rng = np.random.default_rng(47)
+    k = 192
+    x = np.zeros(k)
+    x[100:108] = 6
+    packed = _rows(rng, x, exponent=100)[None, None]
+    packed[0, 0, 100:108, :256] = 0x77  # the largest code, all of one sign
+    u = Units(packed)
+    q = _queries(rng, 1, np.array([rise]) * 4 / 3, unit=2.0 ** -100)
+    out, lse = u.attend(q, SCALE, sms)
+    assert np.isfinite(out).all()
+    check(q[0], q4.values(packed[0, 0]), SCALE, out[0], lse[0], "")
+    u.ctx.close()
