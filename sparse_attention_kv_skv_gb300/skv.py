@@ -205,9 +205,33 @@ def _ptr(t) -> int:
     return t.ctypes.data  # numpy
 
 
-def _need(t, nbytes: int, what: str) -> None:
+_dtypes = {}  # torch's, by the names used here (filled at the first use: this module does not import torch)
+
+
+def _is_type(t, dtype: str) -> bool:
+    if not _dtypes:
+        import torch
+        _dtypes.update(bf16=torch.bfloat16, fp32=torch.float32, int32=torch.int32)
+    return t.dtype is _dtypes[dtype]
+
+
+def _need(t, dtype: str | None, nbytes: int, device: int, what: str, pinned: bool = False) -> None:
+    """t is contiguous, of the type and size, and on the context's device (or, if allowed, in pinned host memory).
+    An address given as an int is taken as it is."""
+    if isinstance(t, int):
+        return
+    if dtype is not None and t.dtype is not _dtypes.get(dtype) and not _is_type(t, dtype):
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
     if t.nbytes < nbytes or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous and hold {nbytes} bytes")
+    if t.get_device() != device:
+        _elsewhere(t, device, what, pinned)
+
+
+def _elsewhere(t, device: int, what: str, pinned: bool = False) -> None:
+    """Of a tensor that is not on the context's device."""
+    if not (pinned and not t.is_cuda and t.is_pinned()):
+        raise ValueError(f"{what} must be on the context's device (cuda:{device})" + (" or in pinned host memory" if pinned else ""))
 
 
 @dataclasses.dataclass
@@ -232,7 +256,7 @@ class Index:
     key for `block` tokens (see skv_index)."""
 
     def __init__(self, keys, block: int = 1, first: int = 0, last: int = 0, relu: bool = True):
-        if keys.dim() != 4 or keys.stride(3) != 1 or keys.element_size() != 2 or not keys.is_floating_point():
+        if keys.dim() != 4 or keys.stride(3) != 1 or not _is_type(keys, "bf16"):
             raise ValueError("Index: keys must be [requests][layers][keys][dim] bf16 with adjacent values")
         self.keys, self.block = keys, block
         self.first, self.last, self.relu = first, last, int(bool(relu))
@@ -348,6 +372,14 @@ class Context:
         """attend() over a hot buffer of packed rows (row_bytes == SKV_Q4_ROW_BYTES; see skv_attend_q4)."""
         B = req_ids.numel() if B is None else B
         scale = (1.0 / 576 ** 0.5) if sm_scale is None else sm_scale
+        units = B if layer >= 0 else B * self.cfg.num_layers
+        dev = self.cfg.device
+        _need(req_ids, "int32", 4 * B, dev, "attend_q4: req_ids")
+        _need(q, "bf16", units * 128 * 1152, dev, "attend_q4: q")
+        _need(slots, "int32", 4 * units * self.cfg.topk, dev, "attend_q4: slots")
+        _need(out, "bf16", units * 128 * 1024, dev, "attend_q4: out")
+        if lse is not None:
+            _need(lse, "fp32", units * 512, dev, "attend_q4: lse")
         check(skv_attend_q4(self.h, _ptr(req_ids), B, layer, _ptr(q), _ptr(slots), _ptr(out), _ptr(lse), scale,
                             _stream_handle(stream, self.cfg.device)), "skv_attend_q4")
 
@@ -369,9 +401,14 @@ class Context:
             raise ValueError("select: the index has fewer requests, layers or keys than the context")
         if dim != index.keys.shape[3]:
             raise ValueError("select: q and the index keys differ in width")
-        _need(q, 2 * units * heads * dim, "select: q")
-        _need(w, 4 * units * heads, "select: w")
-        _need(topk, 4 * units * self.cfg.topk, "select: topk")
+        dev = self.cfg.device
+        if index.keys.get_device() != dev:
+            _elsewhere(index.keys, dev, "select: the index")
+        _need(req_ids, "int32", 4 * B, dev, "select: req_ids")
+        _need(q, "bf16", 2 * units * heads * dim, dev, "select: q")
+        _need(w, "fp32", 4 * units * heads, dev, "select: w")
+        _need(topk, "int32", 4 * units * self.cfg.topk, dev, "select: topk")
+        _need(workspace, None, 0, dev, "select: workspace")
         check(skv_select(self.h, index.c(heads), _ptr(req_ids), B, layer, _ptr(q), _ptr(w), _ptr(topk), _ptr(workspace),
                          workspace.nbytes, _stream_handle(stream, self.cfg.device)), "skv_select")
 
@@ -379,23 +416,33 @@ class Context:
         """bf16 rows [n][576] (rows may lie apart: rows.stride(0)) -> packed rows
         [n][336] bytes and, if given, the bf16 values they stand for [n][576]."""
         shape, step = rows.shape, rows.stride()
-        if len(shape) != 2 or shape[1] != 576 or step[1] != 1 or rows.element_size() != 2:
+        if len(shape) != 2 or shape[1] != 576 or step[1] != 1 or (rows.dtype is not _dtypes.get("bf16") and not _is_type(rows, "bf16")):
             raise ValueError("pack_rows: rows must be [n][576] bf16 with adjacent values")
-        n = shape[0]
-        _need(packed, 336 * n, "pack_rows: packed")
+        n, dev = shape[0], self.cfg.device
+        if rows.get_device() != dev:
+            _elsewhere(rows, dev, "pack_rows: rows", True)
+        _need(packed, None, 336 * n, dev, "pack_rows: packed", True)
         if values is not None:
-            _need(values, 1152 * n, "pack_rows: values")
-        check(skv_pack_rows(self.h, rows.data_ptr(), 2 * step[0] if n > 1 else 1152, n, packed.data_ptr(),
-                            0 if values is None else values.data_ptr(), _stream_handle(stream, self.cfg.device)), "skv_pack_rows")
+            _need(values, "bf16", 1152 * n, dev, "pack_rows: values", True)
+        status = skv_pack_rows(self.h, rows.data_ptr(), 2 * step[0] if n > 1 else 1152, n, packed.data_ptr(),
+                               0 if values is None else values.data_ptr(),
+                               _raw_stream(dev) if stream is None else _stream_handle(stream))
+        if status:
+            check(status, "skv_pack_rows")
 
     def unpack_rows(self, packed, values, stream=None) -> None:
         """Packed rows [n][336] bytes -> the bf16 values they stand for [n][576]."""
         n, rest = divmod(packed.nbytes, 336)
         if rest or not packed.is_contiguous():
             raise ValueError("unpack_rows: packed must be contiguous and hold whole rows of 336 bytes")
-        _need(values, 1152 * n, "unpack_rows: values")
-        check(skv_unpack_rows(self.h, packed.data_ptr(), n, values.data_ptr(), _stream_handle(stream, self.cfg.device)),
-              "skv_unpack_rows")
+        dev = self.cfg.device
+        if packed.get_device() != dev:
+            _elsewhere(packed, dev, "unpack_rows: packed", True)
+        _need(values, "bf16", 1152 * n, dev, "unpack_rows: values", True)
+        status = skv_unpack_rows(self.h, packed.data_ptr(), n, values.data_ptr(),
+                                 _raw_stream(dev) if stream is None else _stream_handle(stream))
+        if status:
+            check(status, "skv_unpack_rows")
 
     def selftest_attend_timeout(self, req_ids, q, slots, out, B: int | None = None, stream=None) -> None:
         """The attention kernel with its key loads withheld: its waits run out
