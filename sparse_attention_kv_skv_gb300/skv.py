@@ -178,17 +178,15 @@ def _raw_stream(device: int) -> int:
     """torch.cuda.current_stream(device).cuda_stream, in 0.1 instead of 4 us (replaced by torch's own at the first call)."""
     global _raw_stream
     import torch
+    torch.cuda.init()
     _raw_stream = torch._C._cuda_getCurrentRawStream
     return _raw_stream(device)
 
 
-def _stream_handle(stream, device: int | None = None) -> int:
-    """A stream argument: None -> torch's current stream (of `device`, if given);
-    an int -> as is; a torch.cuda.Stream -> its handle."""
+def _stream_handle(stream, device: int) -> int:
+    """A stream argument of a context on `device`: None -> torch's current stream of
+    that device; an int -> as is; a torch.cuda.Stream -> its handle."""
     if stream is None:
-        if device is None:
-            import torch
-            return torch.cuda.current_stream().cuda_stream
         return _raw_stream(device)
     if isinstance(stream, int):
         return stream
@@ -305,31 +303,31 @@ class Context:
     # lifecycle -------------------------------------------------------------
     def publish(self, T: int, rows=None, stream=None) -> int:
         r = ctypes.c_int32()
-        check(skv_publish(self.h, _ptr(rows), T, ctypes.byref(r), _stream_handle(stream)), "skv_publish")
+        check(skv_publish(self.h, _ptr(rows), T, ctypes.byref(r), _stream_handle(stream, self.cfg.device)), "skv_publish")
         return r.value
 
     def release(self, req: int, stream=None) -> None:
-        check(skv_release(self.h, req, _stream_handle(stream)), "skv_release")
+        check(skv_release(self.h, req, _stream_handle(stream, self.cfg.device)), "skv_release")
 
     def write_back(self, req_ids, rows, n: int | None = None, stream=None) -> None:
         n = req_ids.numel() if n is None else n
-        check(skv_write_back(self.h, _ptr(req_ids), n, _ptr(rows), _stream_handle(stream)), "skv_write_back")
+        check(skv_write_back(self.h, _ptr(req_ids), n, _ptr(rows), _stream_handle(stream, self.cfg.device)), "skv_write_back")
 
     def extend(self, req: int, rows, n: int, stream=None) -> None:
         """Append n tokens' rows [L][n][row_bytes] to request req."""
-        check(skv_extend(self.h, req, _ptr(rows), n, _stream_handle(stream)), "skv_extend")
+        check(skv_extend(self.h, req, _ptr(rows), n, _stream_handle(stream, self.cfg.device)), "skv_extend")
 
     def assemble(self, req_ids, topk, slots, hits, misses, B: int | None = None, stream=None) -> None:
         B = req_ids.numel() if B is None else B
         check(skv_assemble(self.h, _ptr(req_ids), B, _ptr(topk), _ptr(slots), _ptr(hits), _ptr(misses),
-                           _stream_handle(stream)), "skv_assemble")
+                           _stream_handle(stream, self.cfg.device)), "skv_assemble")
 
     def assemble_layer(self, layer: int, req_ids, topk, slots, hits, misses, B: int | None = None,
                        stream=None) -> None:
         """One layer's assemble: topk / slots are [B][k], hits / misses [B]."""
         B = req_ids.numel() if B is None else B
         check(skv_assemble_layer(self.h, _ptr(req_ids), B, layer, _ptr(topk), _ptr(slots), _ptr(hits),
-                                 _ptr(misses), _stream_handle(stream)), "skv_assemble_layer")
+                                 _ptr(misses), _stream_handle(stream, self.cfg.device)), "skv_assemble_layer")
 
     def prefetch(self, req_ids, cand, layer: int = -1, hits=None, misses=None, B: int | None = None,
                  stream=None) -> None:
@@ -337,26 +335,26 @@ class Context:
         (layer -1) or [B][k]; hits / misses ([B][L] or [B]) are optional."""
         B = req_ids.numel() if B is None else B
         check(skv_prefetch(self.h, _ptr(req_ids), B, layer, _ptr(cand), _ptr(hits), _ptr(misses),
-                           _stream_handle(stream)), "skv_prefetch")
+                           _stream_handle(stream, self.cfg.device)), "skv_prefetch")
 
     def prefetch_recent(self, req_ids, n: int, layer: int = -1, hits=None, misses=None, B: int | None = None,
                         stream=None) -> None:
         """Prefetch of each request's n newest tokens (every layer, or one)."""
         B = req_ids.numel() if B is None else B
         check(skv_prefetch_recent(self.h, _ptr(req_ids), B, layer, n, _ptr(hits), _ptr(misses),
-                                  _stream_handle(stream)), "skv_prefetch_recent")
+                                  _stream_handle(stream, self.cfg.device)), "skv_prefetch_recent")
 
     def assemble_noalloc(self, req_ids, topk, slots, hits, misses, B: int | None = None, stream=None) -> None:
         """skv_assemble with the gather work list in the library's static
         device array (allocates nothing; see include/skv.h)."""
         B = req_ids.numel() if B is None else B
         check(skv_assemble_noalloc(self.h, _ptr(req_ids), B, _ptr(topk), _ptr(slots), _ptr(hits), _ptr(misses),
-                                   _stream_handle(stream)), "skv_assemble_noalloc")
+                                   _stream_handle(stream, self.cfg.device)), "skv_assemble_noalloc")
 
     def assemble_host(self, req_ids, topk, slots, hits, misses, B: int | None = None, stream=None) -> None:
         B = len(req_ids) if B is None else B
         check(skv_assemble_host(self.h, _ptr(req_ids), B, _ptr(topk), _ptr(slots), _ptr(hits), _ptr(misses),
-                                _stream_handle(stream)), "skv_assemble_host")
+                                _stream_handle(stream, self.cfg.device)), "skv_assemble_host")
 
     def attend(self, req_ids, q, slots, out, lse=None, layer: int = -1, sm_scale: float | None = None,
                B: int | None = None, stream=None) -> None:
@@ -365,7 +363,7 @@ class Context:
         B = req_ids.numel() if B is None else B
         scale = (1.0 / 576 ** 0.5) if sm_scale is None else sm_scale
         check(skv_attend(self.h, _ptr(req_ids), B, layer, _ptr(q), _ptr(slots), _ptr(out), _ptr(lse), scale,
-                         _stream_handle(stream)), "skv_attend")
+                         _stream_handle(stream, self.cfg.device)), "skv_attend")
 
     def attend_q4(self, req_ids, q, slots, out, lse=None, layer: int = -1, sm_scale: float | None = None,
                   B: int | None = None, stream=None) -> None:
@@ -426,7 +424,7 @@ class Context:
             _need(values, "bf16", 1152 * n, dev, "pack_rows: values", True)
         status = skv_pack_rows(self.h, rows.data_ptr(), 2 * step[0] if n > 1 else 1152, n, packed.data_ptr(),
                                0 if values is None else values.data_ptr(),
-                               _raw_stream(dev) if stream is None else _stream_handle(stream))
+                               _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
         if status:
             check(status, "skv_pack_rows")
 
@@ -440,7 +438,7 @@ class Context:
             _elsewhere(packed, dev, "unpack_rows: packed", True)
         _need(values, "bf16", 1152 * n, dev, "unpack_rows: values", True)
         status = skv_unpack_rows(self.h, packed.data_ptr(), n, values.data_ptr(),
-                                 _raw_stream(dev) if stream is None else _stream_handle(stream))
+                                 _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
         if status:
             check(status, "skv_unpack_rows")
 
@@ -449,12 +447,12 @@ class Context:
         and it reports SKV_DEVERR_TIMEOUT (see skv_selftest_attend_timeout)."""
         B = req_ids.numel() if B is None else B
         check(skv_selftest_attend_timeout(self.h, _ptr(req_ids), B, _ptr(q), _ptr(slots), _ptr(out),
-                                          _stream_handle(stream)), "skv_selftest_attend_timeout")
+                                          _stream_handle(stream, self.cfg.device)), "skv_selftest_attend_timeout")
 
     # inspection ------------------------------------------------------------
     def get_device_error(self, stream=None) -> int:
         bits = ctypes.c_int32()
-        check(skv_get_device_error(self.h, ctypes.byref(bits), _stream_handle(stream)), "skv_get_device_error")
+        check(skv_get_device_error(self.h, ctypes.byref(bits), _stream_handle(stream, self.cfg.device)), "skv_get_device_error")
         return bits.value
 
     def hot_buffer(self):
@@ -477,23 +475,23 @@ class Context:
         ln = np.zeros(1, np.int64)
         act = np.zeros(1, np.int32)
         check(skv_export_state(self.h, req, _ptr(s2t), _ptr(ts), _ptr(t2s), _ptr(lru), _ptr(ln), _ptr(act),
-                               _stream_handle(stream)), "skv_export_state")
+                               _stream_handle(stream, self.cfg.device)), "skv_export_state")
         return {"slot2tok": s2t, "ts": ts, "lru": lru, "tok2slot": t2s, "len": int(ln[0]), "active": int(act[0])}
 
     def export_hot(self, req: int, stream=None):
         import numpy as np
         out = np.empty((self.cfg.num_layers, self.cfg.hot_slots, self.cfg.row_bytes), np.uint8)
-        check(skv_export_hot(self.h, req, _ptr(out), _stream_handle(stream)), "skv_export_hot")
+        check(skv_export_hot(self.h, req, _ptr(out), _stream_handle(stream, self.cfg.device)), "skv_export_hot")
         return out
 
     def clock(self, stream=None) -> int:
         c = ctypes.c_uint32()
-        check(skv_get_clock(self.h, ctypes.byref(c), _stream_handle(stream)), "skv_get_clock")
+        check(skv_get_clock(self.h, ctypes.byref(c), _stream_handle(stream, self.cfg.device)), "skv_get_clock")
         return c.value
 
     def stats(self, stream=None):
         a, b, c = ctypes.c_uint64(), ctypes.c_uint64(), ctypes.c_uint64()
-        check(skv_get_stats(self.h, ctypes.byref(a), ctypes.byref(b), ctypes.byref(c), _stream_handle(stream)),
+        check(skv_get_stats(self.h, ctypes.byref(a), ctypes.byref(b), ctypes.byref(c), _stream_handle(stream, self.cfg.device)),
               "skv_get_stats")
         return {"calls": a.value, "hits": b.value, "misses": c.value}
 
