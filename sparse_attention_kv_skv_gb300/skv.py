@@ -254,11 +254,15 @@ class Index:
     key for `block` tokens (see skv_index)."""
 
     def __init__(self, keys, block: int = 1, first: int = 0, last: int = 0, relu: bool = True):
-        if keys.dim() != 4 or keys.stride(3) != 1 or not _is_type(keys, "bf16"):
-            raise ValueError("Index: keys must be [requests][layers][keys][dim] bf16 with adjacent values")
         self.keys, self.block = keys, block
         self.first, self.last, self.relu = first, last, int(bool(relu))
-        self._c = {}  # by heads: calls of several threads may be under way
+
+    def __setattr__(self, name, value):
+        if name == "keys" and (value.dim() != 4 or value.stride(3) != 1 or not _is_type(value, "bf16")):
+            raise ValueError("Index: keys must be [requests][layers][keys][dim] bf16 with adjacent values")
+        object.__setattr__(self, name, value)
+        # the C descriptions of what the index is now, by heads: calls of several threads may be under way
+        object.__setattr__(self, "_c", {})
 
     def c(self, heads: int = 1):
         s = self._c.get(heads)

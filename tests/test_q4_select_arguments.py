@@ -80,3 +80,16 @@ def test_tensors_that_are_not_contiguous_are_refused(ctx):
     slots, out = torch.zeros((6, 8), dtype=torch.int32), torch.zeros((6, 128, 512), dtype=BF16)
     with pytest.raises(ValueError, match="contiguous"):
         ctx.attend_q4(torch.zeros(2, dtype=torch.int32), q, slots, out)
+
+
+def test_an_index_that_is_changed_after_a_call_is_described_anew():
+    keys = torch.zeros((2, 3, 40, 64), dtype=BF16)
+    index = Index(keys, block=2, first=1, last=1)
+    before = index.c(4)._obj
+    index.block, index.first, index.last, index.relu = 4, 0, 2, False
+    index.keys = torch.zeros((2, 3, 20, 128), dtype=BF16)
+    s = index.c(4)._obj
+    assert (s.block, s.first, s.last, s.relu, s.dim, s.key_stride) == (4, 0, 2, 0, 128, 256)
+    assert s.keys == index.keys.data_ptr() and (before.block, before.dim) == (2, 64)  # a call under way keeps its own
+    with pytest.raises(ValueError):
+        index.keys = keys.half()
