@@ -553,9 +553,10 @@ SKV_API skv_status skv_set_attend_sms(skv_ctx *ctx, int32_t sms);
 SKV_API skv_status skv_selftest_mma(const void *a_dev, const void *b_dev, float *d_dev, int32_t n, int32_t k,
                                     int32_t mode, skv_stream_t stream);
 
-/* Diagnostic of skv_attend's bounded waits (not part of any decode step):
+/* Diagnostic of the bounded waits of skv_attend, or of skv_attend_q4 on a context
+ * of packed rows (not part of any decode step):
  * launches the attention kernel over the call's units (all layers; arguments
- * as skv_attend, out_dev [units][128][512] bf16) exactly as skv_attend would,
+ * as skv_attend, out_dev [units][128][512] bf16) exactly as skv_attend (skv_attend_q4) would,
  * except that the kernel never issues a key load.  Its first wait for keys
  * therefore runs out (within about two seconds) with no copy and no
  * tensor-core product in flight; the kernel sets SKV_DEVERR_TIMEOUT in the
@@ -565,6 +566,13 @@ SKV_API skv_status skv_selftest_mma(const void *a_dev, const void *b_dev, float 
  * or hanging a GPU.  Host errors as skv_attend. */
 SKV_API skv_status skv_selftest_attend_timeout(skv_ctx *ctx, const int32_t *req_ids_dev, int32_t B, const void *q_dev,
                                                const int32_t *slots_dev, void *out_dev, skv_stream_t stream);
+
+/* The same for skv_select (all layers; arguments as there): the scoring kernel
+ * never issues a load, its first wait for one runs out, SKV_DEVERR_TIMEOUT is set
+ * and topk_dev filled with -1. */
+SKV_API skv_status skv_selftest_select_timeout(skv_ctx *ctx, const skv_index *index, const int32_t *req_ids_dev, int32_t B,
+                                               const void *q_dev, const float *w_dev, int32_t *topk_dev,
+                                               void *workspace_dev, int64_t workspace_bytes, skv_stream_t stream);
 
 /* The message of the last failing CUDA call on this thread ("" if none). */
 SKV_API const char *skv_last_cuda_error(void);

@@ -403,9 +403,10 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
                                                  const int32_t* slots, const KeySplit& sp, uint8_t* sK,
                                                  uint8_t* sRest, uint8_t* sRaw, int nst, int gtot, int units, int cl, int ncl, int h,
                                                  int lw, int lane, const int32_t (&first_slots)[2],
-                                                 const volatile uint32_t* abort, ReqOf req_of)
+                                                 const volatile uint32_t* abort, bool withhold_keys, ReqOf req_of)
 {
     if (lw == kConvWarps) {
+        if (withhold_keys) return true;  // the timeout self-test: the first wait for rows runs out with nothing in flight
         int g = 0;
         bool ok = true;
         for (int u = cl; ok && u < units; u += ncl) {
@@ -612,7 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         if (kQ4 && warp >= kLoadWarp0) {
             if constexpr (kQ4) {
                 const bool ok = load_packed_keys(c, &hot_map, d, slots, ks, sK, smem + lay.off_rest, smem + lay.off_raw, nst, gtot, units, cl, ncl,
-                                                 (int)h, warp - kLoadWarp0, lane, first_slots, abort, req_of);
+                                                 (int)h, warp - kLoadWarp0, lane, first_slots, abort, withhold_keys != 0, req_of);
                 if (!ok && lane == 0) give_up(c, &d.ctl[CTL_ERR]);
                 __syncwarp();
             }
@@ -1294,7 +1295,8 @@ size_t attend_q4_scratch_bytes(int device_sms)
 }
 
 cudaError_t launch_attend_q4(const void* hot_map, const Dev& d, const int32_t* req_ids, int B, const void* q, const int32_t* slots, void* out,
-                             float* lse, float sm_scale, float* scratch, int max_sms, int device_sms, cudaStream_t st)
+                             float* lse, float sm_scale, float* scratch, int max_sms, int device_sms, cudaStream_t st,
+                             bool withhold_keys)
 {
     const AttnLayout lay = attend_layout<true>(kRawStages * kRawBytes);
     if (d.k > (int)kMaxTopk || lay.bytes > kSmemLimit || device_sms < 2) return cudaErrorInvalidValue;
@@ -1316,7 +1318,7 @@ cudaError_t launch_attend_q4(const void* hot_map, const Dev& d, const int32_t* r
     cudaError_t e = launch_chained(attend_kernel<true>, dim3((unsigned)clusters * 2), kAttnThreads, lay.bytes, st,
                                    *static_cast<const CUtensorMap*>(hot_map), d, req_ids, static_cast<const uint16_t*>(q),
                                    slots, static_cast<uint16_t*>(out), lse, sm_scale * 1.4426950408889634f, lay,
-                                   units * sp.n, 0, sp);
+                                   units * sp.n, withhold_keys ? 1 : 0, sp);
     if (e != cudaSuccess || sp.n == 1) return e;
     if (sp.n > 8)
         return launch_chained(combine_kernel<4>, dim3(128, (unsigned)units), 512, 0, st, sp, static_cast<uint16_t*>(out), lse);
@@ -1350,7 +1352,7 @@ skv_status attend_impl(skv_ctx* ctx, const int32_t* req_ids_dev, int32_t B, int3
     d.layer_sel = layer;
     if (e == cudaSuccess && q4)
         e = skv::launch_attend_q4(&ctx->hot_map, d, req_ids_dev, B, q_dev, slots_dev, out_dev, lse_dev, sm_scale, ctx->q4_scratch,
-                                  ctx->attend_sms, ctx->device_sms, stream);
+                                  ctx->attend_sms, ctx->device_sms, stream, withhold_keys);
     else if (e == cudaSuccess)
         e = skv::launch_attend(&ctx->hot_map, d, req_ids_dev, B, q_dev, slots_dev, out_dev, lse_dev, sm_scale,
                                ctx->attend_sms, ctx->device_sms, stream, withhold_keys);
@@ -1384,7 +1386,7 @@ extern "C" skv_status skv_selftest_attend_timeout(skv_ctx* ctx, const int32_t* r
                                                   skv_stream_t stream)
 {
     return attend_impl(ctx, req_ids_dev, B, -1, q_dev, slots_dev, out_dev, nullptr, 1.0f, stream, true,
-                       "skv_selftest_attend_timeout");
+                       "skv_selftest_attend_timeout", ctx && ctx->cfg.row_bytes == skv::q4::kRowBytes);
 }
 
 extern "C" skv_status skv_set_attend_sms(skv_ctx* ctx, int32_t sms)

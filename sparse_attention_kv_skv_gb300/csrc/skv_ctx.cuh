@@ -65,7 +65,7 @@ cudaError_t tensor_map_encoder(TensorMapEncoder* encode);
 int64_t select_stride(int64_t max_context, int block);
 cudaError_t prepare_select();  // once per context, on its device
 cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_ids, int B, const void* q, const float* w,
-                          int32_t* topk, void* workspace, int device_sms, cudaStream_t st);
+                          int32_t* topk, void* workspace, int device_sms, cudaStream_t st, bool withhold_keys = false);
 // Loads skv_assemble_noalloc's static work list on `device` (current) and
 // caches its address, so that no later call loads or allocates anything.
 cudaError_t noalloc_prepare(int device);

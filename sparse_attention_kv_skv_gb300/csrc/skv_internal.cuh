@@ -104,7 +104,8 @@ cudaError_t launch_attend(const void* hot_map, const Dev& d, const int32_t* req_
 // results go to `scratch` (attend_q4_scratch_bytes(device_sms) bytes, one call at a time).
 size_t attend_q4_scratch_bytes(int device_sms);
 cudaError_t launch_attend_q4(const void* hot_map, const Dev& d, const int32_t* req_ids, int B, const void* q, const int32_t* slots, void* out,
-                             float* lse, float sm_scale, float* scratch, int max_sms, int device_sms, cudaStream_t st);
+                             float* lse, float sm_scale, float* scratch, int max_sms, int device_sms, cudaStream_t st,
+                             bool withhold_keys = false);
 // Once per context, on its device: the kernel's shared-memory attribute; *device_sms = the SM count.
 cudaError_t prepare_attend(int* device_sms);
 

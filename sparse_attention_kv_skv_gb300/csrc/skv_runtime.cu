@@ -713,20 +713,10 @@ bool select_stride_ok(int64_t stride, int64_t entries)
 {
     return entries <= 1 || (stride > 0 && stride % 16 == 0 && stride < ((int64_t)1 << 40));
 }
-}  // namespace
 
-extern "C" {
-
-skv_status skv_select_workspace(skv_ctx* ctx, const skv_index* index, int32_t B, int32_t layer, int64_t* bytes)
-{
-    if (!select_shape_ok(ctx, index, B, layer) || !bytes) return SKV_ERR_INVALID_ARG;
-    *bytes = select_bytes(ctx, index, B, layer);
-    return SKV_OK;
-}
-
-skv_status skv_select(skv_ctx* ctx, const skv_index* index, const int32_t* req_ids_dev, int32_t B, int32_t layer,
-                      const void* q_dev, const float* w_dev, int32_t* topk_dev, void* workspace_dev,
-                      int64_t workspace_bytes, skv_stream_t stream)
+skv_status select_impl(skv_ctx* ctx, const skv_index* index, const int32_t* req_ids_dev, int32_t B, int32_t layer,
+                       const void* q_dev, const float* w_dev, int32_t* topk_dev, void* workspace_dev,
+                       int64_t workspace_bytes, skv_stream_t stream, bool withhold_keys)
 {
     if (!select_shape_ok(ctx, index, B, layer)) return SKV_ERR_INVALID_ARG;
     const skv_config& c = ctx->cfg;
@@ -748,8 +738,33 @@ skv_status skv_select(skv_ctx* ctx, const skv_index* index, const int32_t* req_i
     if (!g.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
     Dev d = ctx->d;
     d.layer_sel = layer;
-    SKV_CUDA(skv::launch_select(d, ix, req_ids_dev, B, q_dev, w_dev, topk_dev, workspace_dev, ctx->device_sms, stream));
+    SKV_CUDA(skv::launch_select(d, ix, req_ids_dev, B, q_dev, w_dev, topk_dev, workspace_dev, ctx->device_sms, stream,
+                                withhold_keys));
     return SKV_OK;
+}
+}  // namespace
+
+extern "C" {
+
+skv_status skv_select_workspace(skv_ctx* ctx, const skv_index* index, int32_t B, int32_t layer, int64_t* bytes)
+{
+    if (!select_shape_ok(ctx, index, B, layer) || !bytes) return SKV_ERR_INVALID_ARG;
+    *bytes = select_bytes(ctx, index, B, layer);
+    return SKV_OK;
+}
+
+skv_status skv_select(skv_ctx* ctx, const skv_index* index, const int32_t* req_ids_dev, int32_t B, int32_t layer,
+                      const void* q_dev, const float* w_dev, int32_t* topk_dev, void* workspace_dev,
+                      int64_t workspace_bytes, skv_stream_t stream)
+{
+    return select_impl(ctx, index, req_ids_dev, B, layer, q_dev, w_dev, topk_dev, workspace_dev, workspace_bytes, stream, false);
+}
+
+skv_status skv_selftest_select_timeout(skv_ctx* ctx, const skv_index* index, const int32_t* req_ids_dev, int32_t B,
+                                       const void* q_dev, const float* w_dev, int32_t* topk_dev, void* workspace_dev,
+                                       int64_t workspace_bytes, skv_stream_t stream)
+{
+    return select_impl(ctx, index, req_ids_dev, B, -1, q_dev, w_dev, topk_dev, workspace_dev, workspace_bytes, stream, true);
 }
 
 skv_status skv_get_device_error(skv_ctx* ctx, int32_t* bits, skv_stream_t stream)

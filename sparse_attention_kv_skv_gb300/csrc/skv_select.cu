@@ -41,6 +41,7 @@ struct SelectShape {
     int B, layers;         // units b * layers + l (layers: L, or 1 for a call on one layer)
     int heads, npad;       // npad: heads rounded up to the MMA's multiple of 16
     int block, first, last;
+    int withhold_keys;     // the timeout self-test: no load is issued, so the first wait for one runs out
     int64_t stride;        // scores a unit has room for
 };
 
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     if (count == 0) {
         // no tile for this CTA
     } else if (warp == kLoadWarp) {
-        if (lane == 0) {
+        if (lane == 0 && !sh.withhold_keys) {
             Walk k(d, sh, req_ids, c.start);
             const uint64_t stream_once = tc::evict_first_policy();  // keys pass L2 by; the scores stay for pick_kernel
             bool ok = true;
@@ -902,7 +903,7 @@ cudaError_t prepare_select()
 }
 
 cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_ids, int B, const void* q, const float* w,
-                          int32_t* topk, void* workspace, int device_sms, cudaStream_t st)
+                          int32_t* topk, void* workspace, int device_sms, cudaStream_t st, bool withhold_keys)
 {
     const int64_t max_keys = (d.T_max + ix.block - 1) / ix.block;
     TensorMapEncoder encode = nullptr;
@@ -916,6 +917,7 @@ cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_
     sh.block = ix.block;
     sh.first = ix.first;
     sh.last = ix.last;
+    sh.withhold_keys = withhold_keys ? 1 : 0;
     sh.stride = select_stride(d.T_max, ix.block);
     const int64_t units = (int64_t)B * sh.layers;
 

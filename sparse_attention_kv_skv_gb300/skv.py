@@ -100,6 +100,7 @@ def _load():
         "skv_unpack_rows": [vp, vp, i64, vp, vp],
         "skv_select_workspace": [vp, P(skv_index), i32, i32, P(i64)],
         "skv_select": [vp, P(skv_index), vp, i32, i32, vp, vp, vp, vp, i64, vp],
+        "skv_selftest_select_timeout": [vp, P(skv_index), vp, i32, vp, vp, vp, vp, i64, vp],
         "skv_pool_placement": [vp, P(i32), P(i32), P(ctypes.c_float)],
         "skv_host_node_for_pci": [ctypes.c_char_p, ctypes.c_char_p, P(i32)],
     }
@@ -146,6 +147,7 @@ skv_select_workspace = lib.skv_select_workspace
 skv_pack_rows = lib.skv_pack_rows
 skv_unpack_rows = lib.skv_unpack_rows
 skv_selftest_attend_timeout = lib.skv_selftest_attend_timeout
+skv_selftest_select_timeout = lib.skv_selftest_select_timeout
 skv_pool_placement = lib.skv_pool_placement
 skv_host_node_for_pci = lib.skv_host_node_for_pci
 skv_last_cuda_error = lib.skv_last_cuda_error
@@ -452,6 +454,13 @@ class Context:
         B = req_ids.numel() if B is None else B
         check(skv_selftest_attend_timeout(self.h, _ptr(req_ids), B, _ptr(q), _ptr(slots), _ptr(out),
                                           _stream_handle(stream, self.cfg.device)), "skv_selftest_attend_timeout")
+
+    def selftest_select_timeout(self, index: Index, req_ids, q, w, topk, workspace, B: int | None = None, stream=None) -> None:
+        """select() with its loads withheld (see skv_selftest_select_timeout)."""
+        B = req_ids.numel() if B is None else B
+        check(skv_selftest_select_timeout(self.h, index.c(q.shape[-2]), _ptr(req_ids), B, _ptr(q), _ptr(w), _ptr(topk),
+                                          _ptr(workspace), workspace.nbytes, _stream_handle(stream, self.cfg.device)),
+              "skv_selftest_select_timeout")
 
     # inspection ------------------------------------------------------------
     def get_device_error(self, stream=None) -> int:

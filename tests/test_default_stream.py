@@ -33,6 +33,9 @@ CALLS = {
     "pack_rows": lambda c, **k: c.pack_rows(torch.zeros((1, 576), dtype=torch.bfloat16), torch.zeros(336, dtype=torch.uint8), **k),
     "unpack_rows": lambda c, **k: c.unpack_rows(torch.zeros(336, dtype=torch.uint8), torch.zeros(576, dtype=torch.bfloat16), **k),
     "selftest_attend_timeout": lambda c, **k: c.selftest_attend_timeout(I[:1], I, I, I, **k),
+    "selftest_select_timeout": lambda c, **k: c.selftest_select_timeout(
+        Index(torch.zeros((1, 1, 8, 64), dtype=torch.bfloat16)), I[:1], torch.zeros((1, 1, 64), dtype=torch.bfloat16),
+        torch.zeros((1, 1)), I, I, **k),
     "get_device_error": lambda c, **k: c.get_device_error(**k),
     "export_state": lambda c, **k: c.export_state(0, **k),
     "export_hot": lambda c, **k: c.export_hot(0, **k),
