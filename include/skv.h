@@ -39,7 +39,8 @@
  *   ts       [R][L][S] uint32       device; clock of the step that last used the slot (0 = never)
  *   lru      [R][L][S] uint16       device; the S slots ordered by (ts, slot), least recent first
  *   len/active per request, the step clock and the sticky error word -- all
- *   device memory.
+ *   device memory; with packed rows (SKV_Q4_ROW_BYTES) also the scratch in which
+ *   skv_attend_q4 joins the parts of a unit (20 MB).
  * No call after skv_create allocates; skv_assemble and skv_write_back are
  * therefore safe to capture in a CUDA graph.
  *
@@ -78,8 +79,8 @@
  *
  * Why the configuration gives row_bytes rather than an element count and an
  * element size: the assembly path moves rows as bytes and never reads an
- * element; only skv_attend interprets them, and it requires 576 bf16 (1152
- * bytes).  row_bytes = elements x element size.
+ * element; only the attention interprets them: skv_attend requires 576 bf16 (1152
+ * bytes: elements x element size), skv_attend_q4 packed rows (336 bytes).
  */
 #ifndef SKV_H_
 #define SKV_H_
@@ -121,7 +122,7 @@ typedef enum {
 #define SKV_DEVERR_BAD_INDEX 2     /* a Top-k entry that is neither -1 nor in [0, len of its request) */
 #define SKV_DEVERR_DUPLICATE 4     /* a token that appears twice in one (request, layer) Top-k row */
 #define SKV_DEVERR_CONTEXT_FULL 8  /* skv_write_back / skv_extend beyond max_context tokens */
-#define SKV_DEVERR_TIMEOUT 16      /* skv_attend: a tensor-core product did not complete within its bounded wait */
+#define SKV_DEVERR_TIMEOUT 16      /* skv_attend, skv_attend_q4, skv_select: a copy or a tensor-core product did not complete within its bounded wait */
 
 typedef struct {
     int32_t max_requests;  /* R >= 1: request slots */
@@ -339,7 +340,8 @@ SKV_API skv_status skv_attend(skv_ctx *ctx, const int32_t *req_ids_dev, int32_t 
 /* KV rows in 4 bits.  A context whose row_bytes is SKV_Q4_ROW_BYTES can hold
  * packed rows: publish, write back, extend, assemble and prefetch move rows as
  * bytes and work on them as they are, at 336 instead of 1152 bytes a token
- * over the host link.  skv_pack_rows makes packed rows from bf16 rows,
+ * over the host link (whose rate is lower for the shorter rows: 2.9 times as many
+ * tokens a second at 192 requests x 8 layers of 16K tokens).  skv_pack_rows makes packed rows from bf16 rows,
  * skv_unpack_rows reads them back, skv_attend_q4 attends over a hot buffer of
  * them.
  *
@@ -533,7 +535,7 @@ SKV_API skv_status skv_set_gather_events(skv_ctx *ctx, skv_event_t before, skv_e
  * the same time on other streams -- e.g. the next layer's skv_assemble_layer,
  * which is bound by the host link and needs few SMs to keep it busy.  0 (the
  * default) uses every SM.  Negative: SKV_ERR_INVALID_ARG.  Results do not
- * depend on it. */
+ * depend on it (those of skv_attend_q4, which it bounds as well, in their rounding only). */
 SKV_API skv_status skv_set_attend_sms(skv_ctx *ctx, int32_t sms);
 
 /* Diagnostic: one 128 x n x k bf16 matrix product on the tensor cores through

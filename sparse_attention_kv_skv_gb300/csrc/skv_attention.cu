@@ -511,8 +511,9 @@ __device__ __forceinline__ bool load_packed_keys(AttnCtl& c, const CUtensorMap* 
 // - The products are issued by an elected lane of a converged warp (mma_bf16_warp): 1.26 -> 1.20 ms.
 // - A block's values are made before its key stage is free: 1.20 -> 1.16.
 // - The exponentials are taken while the maxima travel: 1.16 -> 1.15 (before the step above: no change).
-// Measured: 1.15 ms at 192 x 8 units of 2048 keys, 764 TFLOP/s, 41 % of the tensor rate; 31 us at 21 units of 1337
-// keys, 16.6 us at one unit of 2048.  What bounds it: a block of 64 keys is a chain of dependent steps between the
+// - The output is divided by the sum of the rounded P (kReferenceAbove): 1.15 -> 1.16 ms.
+// Measured: 1.16 ms at 192 x 8 units of 2048 keys, 757 TFLOP/s, 41 % of the tensor rate; 31 us at 21 units of 1337
+// keys, 16.8 us at one unit of 2048.  What bounds it: a block of 64 keys is a chain of dependent steps between the
 // two CTAs (scores, their exchange, maxima, P, its exchange, the value product, the stage's next keys) of 3.5K cycles,
 // of which the tensor pipe is busy 1.1K; there is no room in shared memory for a fourth stage.  (P as an operand
 // in tensor memory 1.39 ms; a warp for each stream of products 1.41; two S in tensor memory, one exchange tile 1.17.)
@@ -1320,6 +1321,9 @@ cudaError_t launch_attend_q4(const void* hot_map, const Dev& d, const int32_t* r
                                    slots, static_cast<uint16_t*>(out), lse, sm_scale * 1.4426950408889634f, lay,
                                    units * sp.n, withhold_keys ? 1 : 0, sp);
     if (e != cudaSuccess || sp.n == 1) return e;
+    // Many splits are shared by four threads a head and column, at four times the CTAs.  Measured with each, calls of
+    // 2048 keys a unit: one unit of 32 splits 21.7 us without sharing and 16.7 with it, four of 16 splits 24.3 and
+    // 20.7, six of 11 25.0 and 23.7; nine of 8 24.7 and 25.6, 21 of 3 35.6 and 39.4.
     if (sp.n > 8)
         return launch_chained(combine_kernel<4>, dim3(128, (unsigned)units), 512, 0, st, sp, static_cast<uint16_t*>(out), lse);
     return launch_chained(combine_kernel<1>, dim3(32, (unsigned)units), 512, 0, st, sp, static_cast<uint16_t*>(out), lse);

@@ -44,7 +44,7 @@ enum : uint32_t {
     DEVERR_BAD_INDEX = 2,
     DEVERR_DUPLICATE = 4,
     DEVERR_CONTEXT_FULL = 8,
-    DEVERR_TIMEOUT = 16  // a tensor-core product did not signal completion within its bounded wait
+    DEVERR_TIMEOUT = 16  // a copy or a tensor-core product did not signal completion within its bounded wait
 };
 
 // Everything a kernel needs to find the state of unit u = r*L + l.
