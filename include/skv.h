@@ -341,8 +341,9 @@ SKV_API skv_status skv_attend(skv_ctx *ctx, const int32_t *req_ids_dev, int32_t 
  * packed rows: publish, write back, extend, assemble and prefetch move rows as
  * bytes and work on them as they are, at 336 instead of 1152 bytes a token
  * over the host link (whose rate is lower for the shorter rows: 2.9 times as many
- * tokens a second at 192 requests x 8 layers of 16K tokens).  skv_pack_rows makes packed rows from bf16 rows,
- * skv_unpack_rows reads them back, skv_attend_q4 attends over a hot buffer of
+ * tokens a second at 192 requests x 8 layers of 16K tokens).  skv_pack_rows makes
+ * packed rows from bf16 rows, skv_unpack_rows reads them back, skv_attend_q4
+ * attends over a hot buffer of
  * them.
  *
  * The packed row of 576 values x[0..576), in 36 groups of 16:
@@ -390,7 +391,8 @@ SKV_API skv_status skv_unpack_rows(skv_ctx *ctx, const void *packed, int64_t n, 
  * A row whose score is a NaN (one that holds a NaN group, or a NaN in q) makes
  * the head's out and lse NaN.  When a call has fewer units than the device has
  * SM pairs (or than skv_set_attend_sms leaves it), each unit's keys are split
- * over several pairs and the partial results, in scratch the context owns, are
+ * over several pairs and the partial results, in scratch the context owns (so two
+ * calls on one context, or two captured graphs, must not overlap), are
  * joined by a second kernel; the sums are then taken in another order, so
  * results may differ in rounding with the SM count (never from call to call). */
 SKV_API skv_status skv_attend_q4(skv_ctx *ctx, const int32_t *req_ids_dev, int32_t B, int32_t layer, const void *q_dev,
