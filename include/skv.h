@@ -122,7 +122,7 @@ typedef enum {
 #define SKV_DEVERR_BAD_INDEX 2     /* a Top-k entry that is neither -1 nor in [0, len of its request) */
 #define SKV_DEVERR_DUPLICATE 4     /* a token that appears twice in one (request, layer) Top-k row */
 #define SKV_DEVERR_CONTEXT_FULL 8  /* skv_write_back / skv_extend beyond max_context tokens */
-#define SKV_DEVERR_TIMEOUT 16      /* skv_attend, skv_attend_q4, skv_select: a copy or a tensor-core product did not complete within its bounded wait */
+#define SKV_DEVERR_TIMEOUT 16      /* skv_attend, skv_attend_q4, skv_select, skv_attend_prefix, skv_weigh_prefix: a copy or a tensor-core product did not complete within its bounded wait */
 
 typedef struct {
     int32_t max_requests;  /* R >= 1: request slots */
@@ -452,6 +452,93 @@ SKV_API skv_status skv_select_workspace(skv_ctx *ctx, const skv_index *index, in
 SKV_API skv_status skv_select(skv_ctx *ctx, const skv_index *index, const int32_t *req_ids_dev, int32_t B, int32_t layer,
                               const void *q_dev, const float *w_dev, int32_t *topk_dev, void *workspace_dev,
                               int64_t workspace_bytes, skv_stream_t stream);
+
+/* A prefix that a whole batch shares: the KV rows of a text that every request of
+ * the batch starts with, kept once, in device memory the caller owns.  Row j of layer
+ * l (576 bf16, adjacent: 512 values, then 64 rope dims) lies at
+ *   rows + l*layer_stride + j*row_stride   (strides in bytes).
+ * Nothing behind row n - 1 of a layer is read.
+ * Source: [xm] section "为何稀疏注意力需要快速高容量内存层" (sessions that share most
+ * of their KV); the pages give no operator for it. */
+typedef struct {
+    const void *rows;      /* 16-byte aligned; may be null where n is 0 */
+    int64_t layer_stride;  /* multiples of 16, > 0, < 2^40 (free where the axis has one entry) */
+    int64_t row_stride;    /* >= 1152 */
+    int64_t n;             /* tokens, 0 <= n <= 2^30 */
+} skv_prefix;
+
+/* Bytes of workspace that an skv_attend_prefix of this shape needs.  Host code only. */
+SKV_API skv_status skv_attend_prefix_workspace(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads,
+                                               int32_t layer, int64_t *bytes);
+
+/* MLA attention of a batch over a prefix that all of it shares, each of the
+ * prefix's rows read from memory once for all.  Units as in skv_attend: all layers when layer
+ * == -1 (b*L + l), else only `layer` (b); `heads` (1 .. 128) is what a unit has here:
+ *   s_hj = sm_scale * sum_{d<576} q[unit][h][d] * row(l, j)[d]     j < n
+ *   out[unit][h][0..512) = sum_j softmax_j(s_h)_j * row(l, j)[0..512)
+ *   lse[unit][h] = log sum_j exp(s_hj)   (n == 0: -inf, and zero output)
+ * q_dev [units][heads][576] bf16, out_dev [units][heads][512] bf16, lse_dev
+ * [units][heads] fp32 (may be null); device memory, q, out and workspace 16-byte
+ * aligned; sm_scale finite and > 0.  Products on the tensor cores in fp32, P
+ * rounded to bf16; the output is divided by the sum of the rounded P, lse is that of the
+ * unrounded ones.  A head with a NaN score has NaN results.  With skv_join the result
+ * combines with those of skv_attend or skv_attend_q4 over the request's own tokens.
+ * The context gives the device, L and max_batch (B <= max_batch) and the error word
+ * (SKV_DEVERR_TIMEOUT); its requests and its row_bytes do not matter.  The workspace is the caller's and
+ * holds nothing between calls: two calls, or two captured graphs, that may run at the same time need
+ * one each.  Few units are split along the prefix, so results may differ in rounding with B,
+ * never from call to call.  B == 0 enqueues nothing.  Captures into a CUDA graph. */
+SKV_API skv_status skv_attend_prefix(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads, int32_t layer,
+                                     const void *q_dev, void *out_dev, float *lse_dev, float sm_scale,
+                                     void *workspace_dev, int64_t workspace_bytes, skv_stream_t stream);
+
+/* Join attention results over disjoint sets of tokens: for every row i < rows (a unit's head),
+ *   lse[i] = log sum_p exp(lses[p][i]),   out[i] = sum_p exp(lses[p][i] - lse[i]) * outs[p][i]
+ * A part whose lse is -inf drops out, whatever its out holds; if all do, out is zero and lse -inf.
+ * outs[p] [rows][512] bf16 and lses[p] [rows] fp32, 1 <= parts <= 8 (both arrays in host memory, read before the call
+ * returns); out_dev like outs[p], lse_dev like lses[p] (may be null).  Device memory, outs and out
+ * 16-byte aligned.  out_dev and lse_dev may be those of a part; they overlap no part otherwise.  Sums in fp32.
+ * 0 <= rows <= 2^32.  The context gives the device.  Captures into a CUDA graph. */
+SKV_API skv_status skv_join(skv_ctx *ctx, int32_t parts, const void *const *outs, const float *const *lses, int64_t rows,
+                            void *out_dev, float *lse_dev, skv_stream_t stream);
+
+/* Bytes of workspace that an skv_weigh_prefix of this shape needs.  Host code only. */
+SKV_API skv_status skv_weigh_prefix_workspace(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads,
+                                              int32_t layer, int64_t *bytes);
+
+/* Accumulate the attention weight that each token of the prefix receives from the batch: with s as
+ * in skv_attend_prefix, for each layer l of the call and j < n,
+ *   out[l][j] = weights[l][j] + gain * sum_{units of l} sum_h exp(s_hj - lse[unit][h])
+ * lse_dev [units][heads] fp32 is the log of the sum the weights are shares of: that of skv_join for shares of
+ * a request's whole attention, that of skv_attend_prefix for shares within the prefix.  A head whose lse is -inf adds nothing.
+ * weights_dev (null: zeros) and out_dev (may be the same) hold row l at l*weights_stride and l*out_stride
+ * floats, in calls on one layer too; nothing behind out[l][n - 1] is written.  gain finite (a gain
+ * that grows from step to step lets older weights fade).  The rest as in skv_attend_prefix.
+ * Sums are fp32 in a fixed order: the same call gives the same result. */
+SKV_API skv_status skv_weigh_prefix(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads, int32_t layer,
+                                    const void *q_dev, const float *lse_dev, const float *weights_dev,
+                                    int64_t weights_stride, float *out_dev, int64_t out_stride, float sm_scale, float gain,
+                                    void *workspace_dev, int64_t workspace_bytes, skv_stream_t stream);
+
+/* Bytes of workspace that an skv_evict_prefix needs.  Host code only. */
+SKV_API skv_status skv_evict_prefix_workspace(skv_ctx *ctx, const skv_prefix *prefix, int32_t layer, int64_t *bytes);
+
+/* Evict the tokens of a prefix that received the least weight: for each layer of the call (all when
+ * layer == -1) there stay its first `first` and last `last` tokens and, of the others, the
+ * heaviest, `keep` in all (or all n, if that is fewer); of equal weights the lower token, a NaN
+ * is lighter than every other.  For the i-th of the tokens that stay, in ascending order:
+ *   kept[c][i] = token, rows_out[c][i] = its row, weights_out[c][i] = its weight
+ * and kept is -1 behind the last (nothing is written to the others there).  c counts the layers of the call.
+ * kept_dev [layers of the call][keep] int32, rows_out_dev [..][keep][576] bf16 and weights_out_dev [..][keep] fp32
+ * (either may be null), contiguous, device memory, rows_out 16-byte aligned; they overlap neither the
+ * prefix nor the weights.  weights_dev holds row l at l*weights_stride floats.  1 <= keep <= 2^30, first and last >= 0,
+ * first + last <= keep.  What was evicted is the caller's to drop: a
+ * prefix of rows_out and keep takes the old one's place.  While the error word is set kept is filled with -1 and
+ * nothing else written.  The workspace as in skv_attend_prefix.  Captures into a CUDA graph. */
+SKV_API skv_status skv_evict_prefix(skv_ctx *ctx, const skv_prefix *prefix, int32_t layer, const float *weights_dev,
+                                    int64_t weights_stride, int32_t keep, int32_t first, int32_t last, int32_t *kept_dev,
+                                    void *rows_out_dev, float *weights_out_dev, void *workspace_dev,
+                                    int64_t workspace_bytes, skv_stream_t stream);
 
 /* Read the sticky device error word into *bits (SKV_DEVERR_* mask, 0 = none)
  * and clear it.  Synchronises `stream`.

@@ -63,6 +63,15 @@ class skv_index(ctypes.Structure):
     ]
 
 
+class skv_prefix(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_void_p),
+        ("layer_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("n", ctypes.c_int64),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m sparse_attention_kv_skv_gb300.build` "
@@ -101,6 +110,13 @@ def _load():
         "skv_select_workspace": [vp, P(skv_index), i32, i32, P(i64)],
         "skv_select": [vp, P(skv_index), vp, i32, i32, vp, vp, vp, vp, i64, vp],
         "skv_selftest_select_timeout": [vp, P(skv_index), vp, i32, vp, vp, vp, vp, i64, vp],
+        "skv_attend_prefix_workspace": [vp, P(skv_prefix), i32, i32, i32, P(i64)],
+        "skv_attend_prefix": [vp, P(skv_prefix), i32, i32, i32, vp, vp, vp, ctypes.c_float, vp, i64, vp],
+        "skv_join": [vp, i32, P(vp), P(vp), i64, vp, vp, vp],
+        "skv_weigh_prefix_workspace": [vp, P(skv_prefix), i32, i32, i32, P(i64)],
+        "skv_weigh_prefix": [vp, P(skv_prefix), i32, i32, i32, vp, vp, vp, i64, vp, i64, ctypes.c_float, ctypes.c_float, vp, i64, vp],
+        "skv_evict_prefix_workspace": [vp, P(skv_prefix), i32, P(i64)],
+        "skv_evict_prefix": [vp, P(skv_prefix), i32, vp, i64, i32, i32, i32, vp, vp, vp, vp, i64, vp],
         "skv_pool_placement": [vp, P(i32), P(i32), P(ctypes.c_float)],
         "skv_host_node_for_pci": [ctypes.c_char_p, ctypes.c_char_p, P(i32)],
     }
@@ -148,6 +164,13 @@ skv_pack_rows = lib.skv_pack_rows
 skv_unpack_rows = lib.skv_unpack_rows
 skv_selftest_attend_timeout = lib.skv_selftest_attend_timeout
 skv_selftest_select_timeout = lib.skv_selftest_select_timeout
+skv_attend_prefix_workspace = lib.skv_attend_prefix_workspace
+skv_attend_prefix = lib.skv_attend_prefix
+skv_join = lib.skv_join
+skv_weigh_prefix_workspace = lib.skv_weigh_prefix_workspace
+skv_weigh_prefix = lib.skv_weigh_prefix
+skv_evict_prefix_workspace = lib.skv_evict_prefix_workspace
+skv_evict_prefix = lib.skv_evict_prefix
 skv_pool_placement = lib.skv_pool_placement
 skv_host_node_for_pci = lib.skv_host_node_for_pci
 skv_last_cuda_error = lib.skv_last_cuda_error
@@ -277,6 +300,28 @@ class Index:
     def fits(self, cfg: Config) -> bool:
         n = self.keys.shape
         return n[0] >= cfg.max_requests and n[1] >= cfg.num_layers and n[2] * self.block >= cfg.max_context
+
+
+class Prefix:
+    """The rows of a text that a whole batch starts with: rows [L][n][576] bf16 on
+    the device (any strides with adjacent values; see skv_prefix)."""
+
+    def __init__(self, rows):
+        self.rows = rows
+
+    def __setattr__(self, name, value):
+        if name == "rows":
+            if value.dim() != 3 or value.shape[2] != 576 or value.stride(2) != 1 or not _is_type(value, "bf16"):
+                raise ValueError("Prefix: rows must be [layers][tokens][576] bf16 with adjacent values")
+            object.__setattr__(self, "_c", skv_prefix(value.data_ptr(), 2 * value.stride(0), 2 * value.stride(1), value.shape[1]))
+        object.__setattr__(self, name, value)
+
+    def c(self):
+        return ctypes.byref(self._c)
+
+    @property
+    def n(self) -> int:
+        return self.rows.shape[1]
 
 
 class Context:
@@ -447,6 +492,135 @@ class Context:
                                  _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
         if status:
             check(status, "skv_unpack_rows")
+
+    # a prefix that the batch shares ------------------------------------------
+    def _prefix(self, prefix: Prefix, what: str) -> int:
+        """The context's device, which the prefix, with a row of every layer, is on."""
+        dev = self.cfg.device
+        if prefix.rows.shape[0] < self.cfg.num_layers:
+            raise ValueError(f"{what}: the prefix has fewer layers than the context")
+        if prefix.rows.get_device() != dev:
+            _elsewhere(prefix.rows, dev, f"{what}: the prefix")
+        return dev
+
+    def _units(self, q, layer: int, B: int | None, what: str):
+        """(B, units, heads) of queries q [units][heads][576]."""
+        if q.dim() != 3 or q.shape[2] != 576:
+            raise ValueError(f"{what}: q must be [units][heads][576]")
+        layers = 1 if layer >= 0 else self.cfg.num_layers
+        if B is None:
+            B, rest = divmod(q.shape[0], layers)
+            if rest:
+                raise ValueError(f"{what}: q must hold a unit of every layer for each entry of the batch")
+        return B, B * layers, q.shape[1]
+
+    def _weights(self, t, prefix: Prefix, dev: int, what: str) -> int:
+        """The row stride of weights [L][n] fp32 with adjacent values."""
+        if t.dim() != 2 or t.shape[0] < self.cfg.num_layers or t.shape[1] < prefix.n or not _is_type(t, "fp32") or \
+                (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{what} must be [layers][tokens] fp32 with adjacent values")
+        if t.get_device() != dev:
+            _elsewhere(t, dev, what)
+        return t.stride(0)
+
+    def attend_prefix_workspace(self, prefix: Prefix, B: int, heads: int = 128, layer: int = -1) -> int:
+        """Bytes of workspace an attend_prefix() of B entries needs."""
+        n = ctypes.c_int64()
+        check(skv_attend_prefix_workspace(self.h, prefix.c(), B, heads, layer, ctypes.byref(n)), "skv_attend_prefix_workspace")
+        return n.value
+
+    def attend_prefix(self, prefix: Prefix, q, out, lse, workspace, layer: int = -1, sm_scale: float | None = None,
+                      B: int | None = None, stream=None) -> None:
+        """MLA attention of a batch over a prefix that all of it shares (see skv_attend_prefix):
+        q [units][heads][576] bf16 -> out [units][heads][512] bf16, lse [units][heads] (or None).
+        workspace: attend_prefix_workspace() bytes."""
+        dev = self._prefix(prefix, "attend_prefix")
+        B, units, heads = self._units(q, layer, B, "attend_prefix")
+        scale = (1.0 / 576 ** 0.5) if sm_scale is None else sm_scale
+        _need(q, "bf16", units * heads * 1152, dev, "attend_prefix: q")
+        _need(out, "bf16", units * heads * 1024, dev, "attend_prefix: out")
+        if lse is not None:
+            _need(lse, "fp32", units * heads * 4, dev, "attend_prefix: lse")
+        _need(workspace, None, 0, dev, "attend_prefix: workspace")
+        status = skv_attend_prefix(self.h, prefix.c(), B, heads, layer, q.data_ptr(), _ptr(out), _ptr(lse), scale,
+                                   workspace.data_ptr(), workspace.nbytes,
+                                   _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
+        if status:
+            check(status, "skv_attend_prefix")
+
+    def join(self, outs, lses, out, lse=None, stream=None) -> None:
+        """Join attention results over disjoint sets of tokens (see skv_join): outs, up to 8 of
+        [...][512] bf16, and lses [...] fp32 -> out, lse, which may take a part's place."""
+        parts, dev = len(outs), self.cfg.device
+        if len(lses) != parts or not 1 <= parts <= 8:
+            raise ValueError("join: 1 to 8 parts, each with its lse")
+        if out.shape[-1] != 512:
+            raise ValueError("join: out must be [...][512]")
+        rows = out.numel() // 512
+        for o, e in zip(outs, lses):
+            if o.shape != out.shape or e.numel() != rows:
+                raise ValueError("join: the parts and the result differ in shape")
+            _need(o, "bf16", rows * 1024, dev, "join: outs")
+            _need(e, "fp32", rows * 4, dev, "join: lses")
+        _need(out, "bf16", rows * 1024, dev, "join: out")
+        if lse is not None:
+            _need(lse, "fp32", rows * 4, dev, "join: lse")
+        pointers = ctypes.c_void_p * parts
+        status = skv_join(self.h, parts, pointers(*[o.data_ptr() for o in outs]), pointers(*[e.data_ptr() for e in lses]), rows,
+                          out.data_ptr(), _ptr(lse), _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
+        if status:
+            check(status, "skv_join")
+
+    def weigh_prefix_workspace(self, prefix: Prefix, B: int, heads: int = 128, layer: int = -1) -> int:
+        """Bytes of workspace a weigh_prefix() of B entries needs."""
+        n = ctypes.c_int64()
+        check(skv_weigh_prefix_workspace(self.h, prefix.c(), B, heads, layer, ctypes.byref(n)), "skv_weigh_prefix_workspace")
+        return n.value
+
+    def weigh_prefix(self, prefix: Prefix, q, lse, weights, out, workspace, layer: int = -1, sm_scale: float | None = None,
+                     gain: float = 1.0, B: int | None = None, stream=None) -> None:
+        """out = weights (or 0 for None) + gain times the attention weight that each of the prefix's
+        tokens receives from the batch (see skv_weigh_prefix): q [units][heads][576] bf16, lse
+        [units][heads], weights and out [L][n] fp32 (may be the same)."""
+        dev = self._prefix(prefix, "weigh_prefix")
+        B, units, heads = self._units(q, layer, B, "weigh_prefix")
+        scale = (1.0 / 576 ** 0.5) if sm_scale is None else sm_scale
+        _need(q, "bf16", units * heads * 1152, dev, "weigh_prefix: q")
+        _need(lse, "fp32", units * heads * 4, dev, "weigh_prefix: lse")
+        w_stride = 0 if weights is None else self._weights(weights, prefix, dev, "weigh_prefix: weights")
+        o_stride = self._weights(out, prefix, dev, "weigh_prefix: out")
+        _need(workspace, None, 0, dev, "weigh_prefix: workspace")
+        status = skv_weigh_prefix(self.h, prefix.c(), B, heads, layer, q.data_ptr(), _ptr(lse), _ptr(weights), w_stride,
+                                  out.data_ptr(), o_stride, scale, gain, workspace.data_ptr(), workspace.nbytes,
+                                  _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
+        if status:
+            check(status, "skv_weigh_prefix")
+
+    def evict_prefix_workspace(self, prefix: Prefix, layer: int = -1) -> int:
+        """Bytes of workspace an evict_prefix() needs."""
+        n = ctypes.c_int64()
+        check(skv_evict_prefix_workspace(self.h, prefix.c(), layer, ctypes.byref(n)), "skv_evict_prefix_workspace")
+        return n.value
+
+    def evict_prefix(self, prefix: Prefix, weights, kept, rows, kept_weights, workspace, first: int = 0, last: int = 0,
+                     layer: int = -1, stream=None) -> None:
+        """Keep a prefix's heaviest tokens (see skv_evict_prefix): weights [L][n] fp32 -> kept
+        [layers of the call][keep] int32, ascending, their rows [..][keep][576] bf16 and weights [..][keep] (either may be
+        None).  Prefix(rows) takes the old one's place."""
+        dev = self._prefix(prefix, "evict_prefix")
+        layers, keep = 1 if layer >= 0 else self.cfg.num_layers, kept.shape[-1]
+        stride = self._weights(weights, prefix, dev, "evict_prefix: weights")
+        _need(kept, "int32", 4 * layers * keep, dev, "evict_prefix: kept")
+        if rows is not None:
+            _need(rows, "bf16", 1152 * layers * keep, dev, "evict_prefix: rows")
+        if kept_weights is not None:
+            _need(kept_weights, "fp32", 4 * layers * keep, dev, "evict_prefix: kept_weights")
+        _need(workspace, None, 0, dev, "evict_prefix: workspace")
+        status = skv_evict_prefix(self.h, prefix.c(), layer, weights.data_ptr(), stride, keep, first, last, kept.data_ptr(),
+                                  _ptr(rows), _ptr(kept_weights), workspace.data_ptr(), workspace.nbytes,
+                                  _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
+        if status:
+            check(status, "skv_evict_prefix")
 
     def selftest_attend_timeout(self, req_ids, q, slots, out, B: int | None = None, stream=None) -> None:
         """The attention kernel with its key loads withheld: its waits run out
