@@ -6,6 +6,7 @@
 //   s_hj = scale * q_h . k_j;   out_h = sum_j softmax_j(s_h) k_j[0..512);   lse_h = log sum_j exp s_hj
 // Units that share a layer read the same rows, so their heads are rows of one product.
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -13,6 +14,7 @@
 #include <string>
 
 #include "skv_ctx.cuh"
+#include "tcgen05.cuh"
 
 namespace skv {
 namespace {
@@ -71,7 +73,7 @@ __device__ __forceinline__ float dot(const float* a, const __nv_bfloat16* b)
 __global__ void __launch_bounds__(kThreads) attend_tile_kernel(PrefixShape p, const uint16_t* __restrict__ q,
                                                                uint16_t* __restrict__ out, float* __restrict__ lse, float scale_log2)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ float sp[kQRows][kKeys + 1];
     float* sq = reinterpret_cast<float*>(smem);
     uint4* sk = reinterpret_cast<uint4*>(smem + (size_t)kQRows * kDim * 4);
@@ -118,38 +120,359 @@ __global__ void __launch_bounds__(kThreads) attend_tile_kernel(PrefixShape p, co
     if (t == 0 && lse) lse[at] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
 }
 
-// Thirty-two tokens a CTA, all query rows of the layer in groups of 16.
-__global__ void __launch_bounds__(kThreads) weigh_tile_kernel(PrefixShape p, const uint16_t* __restrict__ q,
-                                                              const float* __restrict__ lse, const float* weights,
-                                                              int64_t weights_stride, float* out, int64_t out_stride,
-                                                              float scale_log2, float gain)
+// ---------------------------------------------------------------------------
+// The kernels on the tensor cores run as clusters of two CTAs that multiply as one
+// (cta_group::2).  Query rows go in tiles of 128: the heads of 128 / heads entries
+// of a layer, in order; rows that are left over are zeros.
+constexpr uint32_t kMaxSleepPolls = 1u << 20;  // bound of a wait whose polls may each sleep (about 2 s)
+constexpr int kTileRows = 128;
+constexpr int kBoxes = kDim / 64;              // 64-dim columns of a row, 128 bytes wide
+constexpr uint32_t kTileBox = kTileRows * 128; // such a column of a tile of 128 rows
+constexpr uint32_t kSmemLimit = 227 * 1024;    // dynamic shared memory a CTA may have
+
+__host__ __device__ __forceinline__ int entries_a_tile(int heads) { return kTileRows / heads; }
+
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float part[kQRows][kKeys];
-    float* sq = reinterpret_cast<float*>(smem);
-    uint4* sk = reinterpret_cast<uint4*>(smem + (size_t)kQRows * kDim * 4);
-    const __nv_bfloat16* kb = reinterpret_cast<const __nv_bfloat16*>(sk);
-    const int l = blockIdx.y, j0 = blockIdx.x * kKeys, r = threadIdx.x / 16, t = threadIdx.x % 16;
-    const int64_t rows = (int64_t)p.B * p.heads;
-    load_keys(p, l, j0, sk);
-    float sum[2] = {0.0f, 0.0f};
-    for (int64_t i0 = 0; i0 < rows; i0 += kQRows) {
-        __syncthreads();
-        load_queries(p, l, i0, q, sq);
-        __syncthreads();
-        const float e = i0 + r < rows ? lse[p.q_row(l, i0 + r)] : -INFINITY;
-        if (e == -INFINITY) continue;
-        for (int x = 0; x < 2; ++x) sum[x] += exp2f(fmaf(dot(sq + r * kDim, kb + (t + 16 * x) * kDim), scale_log2, -e * kLog2e));
+    const uint32_t a = tc::smem_u32(bar);
+    for (uint32_t i = 0; i < kMaxSleepPolls; ++i) {
+        if (tc::mbar_test(a, parity)) return true;
+        if ((i & 7u) == 7u && *abort) return false;
     }
-    for (int x = 0; x < 2; ++x) part[r][t + 16 * x] = sum[x];
+    return false;
+}
+// The same for a barrier that threads of both CTAs arrive on.
+__device__ __forceinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort)
+{
+    const uint32_t a = tc::smem_u32(bar);
+    for (uint32_t i = 0; i < kMaxSleepPolls; ++i) {
+        if (tc::mbar_test_cluster(a, parity)) return true;
+        if ((i & 7u) == 7u && *abort) return false;
+    }
+    return false;
+}
+__device__ __forceinline__ void give_up(uint32_t* abort, uint32_t* err)
+{
+    if (!*(volatile uint32_t*)abort) {
+        *(volatile uint32_t*)abort = 1u;
+        atomicOr(err, DEVERR_TIMEOUT);
+    }
+}
+
+// The end of a kernel of a CTA pair, by all threads of both; rank 0 has committed `fin` behind its last product.
+// `owner`: the warp that holds the tensor memory.
+__device__ __forceinline__ void pair_exit(uint64_t* fin, uint32_t* abort, uint32_t* err, uint32_t tbase, bool owner, uint32_t cols)
+{
+    tc::fence_before_sync();
     __syncthreads();
-    const int j = j0 + threadIdx.x;
-    if (threadIdx.x < kKeys && j < p.n) {
-        float w = 0.0f;
-        for (int x = 0; x < kQRows; ++x) w += part[x][threadIdx.x];
-        const float before = weights ? weights[(p.layer0 + l) * weights_stride + j] : 0.0f;
-        out[(p.layer0 + l) * out_stride + j] = fmaf(gain, w, before);
+    if (threadIdx.x == 0) {
+        // no product, and no arrival of one, is left when either CTA leaves
+        if (!tc::mbar_wait(fin, 0, 1u << 22)) give_up(abort, err);
+        if (*(volatile uint32_t*)abort)  // copies of a call that gave up may still be landing: they take microseconds
+            for (int i = 0; i < 256; ++i) __nanosleep(1000);
     }
+    __syncthreads();
+    tc::cluster_sync();  // neither CTA leaves while the other's products or copies may still reach it
+    if (owner) {
+        tc::fence_after_sync();
+        tc::tmem2_dealloc(tbase, cols);
+    }
+}
+
+// 2^x on the special-function unit (approximate; -inf gives 0)
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The query row that lies in row r of tile `tile`: its unit's first head's row plus its head, or -1.
+__device__ __forceinline__ int64_t tile_row(const PrefixShape& p, int l, int tile, int r)
+{
+    const int per = entries_a_tile(p.heads), e = r / p.heads, b = tile * per + e;
+    return e < per && b < p.B ? ((int64_t)b * p.layers + l) * p.heads + (r - e * p.heads) : -1;
+}
+
+// ---------------------------------------------------------------------------
+// Weights.  S^T = K Q^T with the keys as the product's rows (128 a CTA, 256 a
+// pair) and 256 query rows as its columns (a tile of 128 from either CTA), so a thread of the
+// epilogue owns a key and sums its query rows alone, without any exchange:
+//   sum_i exp2(s_ij scale log2 e - lse_i log2 e)
+// A piece of the work is 256 keys of a layer by a share of its query rows; the
+// keys stay in shared memory (147 KB a CTA) while the queries stream past them through a ring of
+// 64-dim columns.  Shares are summed in their order by a second kernel.
+constexpr int kWRing = 4;                      // query columns in flight (16 KB each)
+constexpr int kWEpilogue = 128, kWLoadWarp = 4, kWMmaWarp = 5, kWThreads = 192;
+constexpr uint32_t kWTmemCols = 512;           // two products of 256 columns
+struct alignas(16) WeighCtl {
+    uint64_t a_full[kBoxes], a_free[kBoxes];   // key columns (full: in rank 0, the bytes of both CTAs)
+    uint64_t b_full[kWRing], b_free[kWRing];   // query columns
+    uint64_t d_full[2], d_free[2];             // products (free: in rank 0, a warp of either CTA's epilogue)
+    uint64_t fin;                              // every product has completed
+    alignas(16) float neg[2][2 * kTileRows];   // -lse log2 e of a product's query rows
+    uint32_t tmem_base, abort;
+};
+constexpr uint32_t kWOffRing = kBoxes * kTileBox, kWOffCtl = kWOffRing + kWRing * kTileBox, kWSmem = kWOffCtl + sizeof(WeighCtl);
+static_assert(kWSmem <= kSmemLimit, "shared memory of weigh_kernel");
+
+struct WeighPlan {
+    int tiles;     // of 256 keys, a layer
+    int pairs;     // of tiles of query rows
+    int shares;    // of the query rows
+    int pieces;    // tiles * layers * shares, in this order (the tile fastest)
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
+    weigh_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap q_map, PrefixShape p,
+                 WeighPlan plan, const float* lse, const float* weights, int64_t weights_stride, float* out, int64_t out_stride,
+                 float* part, float scale_log2, float gain, uint32_t* err, int withhold)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    WeighCtl& c = *reinterpret_cast<WeighCtl*>(smem + kWOffCtl);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    const uint32_t rank = blockIdx.x & 1u;
+    const int per = entries_a_tile(p.heads);
+    volatile uint32_t* abort = &c.abort;
+
+    chain_next();
+    if (tid == 0) {
+        for (int i = 0; i < kBoxes; ++i) {
+            tc::mbar_init(&c.a_full[i], 1);
+            tc::mbar_init(&c.a_free[i], 1);
+        }
+        for (int i = 0; i < kWRing; ++i) {
+            tc::mbar_init(&c.b_full[i], 1);
+            tc::mbar_init(&c.b_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&c.d_full[i], 1);
+            tc::mbar_init(&c.d_free[i], 2 * kWEpilogue / 32);
+        }
+        tc::mbar_init(&c.fin, 1);
+        c.abort = 0u;
+    }
+    // query rows behind the last of a tile are zeros for good (a copy writes whole entries only)
+    for (uint32_t i = tid; i < kWRing * kTileBox / 16; i += kWThreads)
+        reinterpret_cast<uint4*>(smem + kWOffRing)[i] = make_uint4(0, 0, 0, 0);
+    tc::fence_smem_async();
+    if (warp == kWMmaWarp) tc::tmem2_alloc(&c.tmem_base, kWTmemCols);
+    tc::fence_before_sync();
+    tc::cluster_sync();  // both CTAs' barriers exist
+    tc::fence_after_sync();
+    const uint32_t tbase = c.tmem_base;
+    chain_wait();
+    lse = behind_wait(lse);
+    const float* before = weights ? behind_wait(weights) : nullptr;
+
+    auto first_pair = [&](int share) { return (int)((int64_t)share * plan.pairs / plan.shares); };
+    auto piece_of = [&](int i, int& l, int& tile, int& p0, int& p1) {
+        tile = i % plan.tiles;
+        const int rest = i / plan.tiles, share = rest / p.layers;
+        l = rest - share * p.layers;
+        p0 = first_pair(share);
+        p1 = first_pair(share + 1);
+        return share;
+    };
+
+    if (warp == kWLoadWarp) {
+        if (lane == 0 && !withhold) {
+            // rank 0's barriers count the bytes of both CTAs
+            const uint32_t af = tc::map_to_rank(tc::smem_u32(&c.a_full[0]), 0), bf = tc::map_to_rank(tc::smem_u32(&c.b_full[0]), 0);
+            const uint32_t q_bytes = (uint32_t)(per * p.heads) * 128u;
+            bool ok = true;
+            int g = 0, n = 0;  // query columns, pieces
+            for (int i = cl; ok && i < plan.pieces; i += ncl, ++n) {
+                int l, tile, p0, p1;
+                piece_of(i, l, tile, p0, p1);
+                for (int pr = p0; ok && pr < p1; ++pr)
+                    for (int x = 0; x < kBoxes; ++x, ++g) {
+                        if (pr == p0) {
+                            if (n > 0 && !(ok = wait_phase(&c.a_free[x], (n - 1) & 1, abort))) break;
+                            if (rank == 0) tc::mbar_arrive_expect_tx(&c.a_full[x], 2 * kTileBox);
+                            tc::tma2_load3(tc::smem_u32(smem) + x * kTileBox, &key_map, 64 * x, 256 * tile + 128 * (int)rank,
+                                           p.layer0 + l, af + 8 * x);
+                        }
+                        const int st = g % kWRing;
+                        if (g >= kWRing && !(ok = wait_phase(&c.b_free[st], ((g / kWRing) - 1) & 1, abort))) break;
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&c.b_full[st], 2 * q_bytes);
+                        tc::tma2_load4(tc::smem_u32(smem) + kWOffRing + st * kTileBox, &q_map, 64 * x, 0, l, (2 * pr + (int)rank) * per,
+                                       bf + 8 * st);
+                    }
+            }
+            if (!ok) give_up(&c.abort, err);
+        }
+        __syncwarp();
+    } else if (warp == kWMmaWarp) {
+        if (rank == 0) {
+            const uint32_t idesc = tc::idesc_bf16_f32(256, 256, 0), tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
+            const uint64_t da = tc::sw128_kmajor_desc(tc::smem_u32(smem)), db = tc::sw128_kmajor_desc(tc::smem_u32(smem) + kWOffRing);
+            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, abort)); };
+            bool ok = true;
+            int g = 0, n = 0, it = 0;
+            for (int i = cl; ok && i < plan.pieces; i += ncl, ++n) {
+                int l, tile, p0, p1;
+                piece_of(i, l, tile, p0, p1);
+                for (int pr = p0; ok && pr < p1; ++pr, ++it) {
+                    const int d = it & 1;
+                    if (it >= 2 && !(ok = __all_sync(0xFFFFFFFFu, wait_phase_cluster(&c.d_free[d], ((it >> 1) - 1) & 1, abort)))) break;
+                    for (int x = 0; x < kBoxes; ++x, ++g) {
+                        const int st = g % kWRing;
+                        if (pr == p0 && !(ok = wait(&c.a_full[x], n & 1))) break;
+                        if (!(ok = wait(&c.b_full[st], (g / kWRing) & 1))) break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma2_bf16_warp(tb + 256 * d, da + ((x * kTileBox + 32 * k) >> 4), db + ((st * kTileBox + 32 * k) >> 4),
+                                               idesc, x > 0 || k > 0 ? 1u : 0u);
+                        tc::mma2_commit_warp(&c.b_free[st]);
+                        if (pr + 1 == p1) tc::mma2_commit_warp(&c.a_free[x]);
+                    }
+                    if (ok) tc::mma2_commit_warp(&c.d_full[d]);
+                }
+            }
+            if (!ok && lane == 0) give_up(&c.abort, err);
+            tc::mma2_commit_warp(&c.fin);
+        }
+    } else {
+        const uint32_t tl = tbase + ((uint32_t)(warp * 32) << 16);
+        const uint32_t df = tc::map_to_rank(tc::smem_u32(&c.d_free[0]), 0);
+        auto neg_of = [&](int l, int tile) {
+            const int64_t r = tile_row(p, l, tile, tid);
+            const float e = r >= 0 ? lse[r] : -INFINITY;
+            return e == -INFINITY ? -INFINITY : -e * kLog2e;  // a row that is none, or attended to nothing, adds 2^-inf
+        };
+        bool ok = true;
+        int it = 0;
+        for (int i = cl; i < plan.pieces; i += ncl) {
+            int l, tile, p0, p1;
+            const int share = piece_of(i, l, tile, p0, p1);
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int pr = p0; pr < p1; ++pr, ++it) {
+                const int d = it & 1;
+                float* neg = c.neg[d];
+                neg[tid] = neg_of(l, 2 * pr);
+                neg[kTileRows + tid] = neg_of(l, 2 * pr + 1);
+                tc::named_sync(1, kWEpilogue);
+                // a give-up must not leave the other threads at a barrier
+                ok = ok && wait_phase(&c.d_full[d], (it >> 1) & 1, abort);
+                if (__all_sync(0xFFFFFFFFu, ok)) {
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 2 * kTileRows; c0 += 32) {
+                        float v[32];
+                        tc::tmem_ld32(tl + 256 * d + c0, v);
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(neg + c0 + x);
+                            acc[0] += ex2(fmaf(v[x], scale_log2, f.x));
+                            acc[1] += ex2(fmaf(v[x + 1], scale_log2, f.y));
+                            acc[2] += ex2(fmaf(v[x + 2], scale_log2, f.z));
+                            acc[3] += ex2(fmaf(v[x + 3], scale_log2, f.w));
+                        }
+                    }
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(df + 8 * d);
+                }
+            }
+            const int j = 256 * tile + 128 * (int)rank + tid;
+            const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            if (ok && j < p.n) {
+                if (plan.shares > 1)
+                    part[((int64_t)share * p.layers + l) * p.n + j] = sum;
+                else
+                    out[(p.layer0 + l) * out_stride + j] =
+                        fmaf(gain, sum, before ? before[(p.layer0 + l) * weights_stride + j] : 0.0f);
+            }
+        }
+        if (!ok) give_up(&c.abort, err);
+    }
+    pair_exit(&c.fin, &c.abort, err, tbase, warp == kWMmaWarp, kWTmemCols);
+}
+
+__global__ void __launch_bounds__(256) weigh_sum_kernel(PrefixShape p, int shares, const float* part, const float* weights,
+                                                        int64_t weights_stride, float* out, int64_t out_stride, float gain)
+{
+    chain_next();
+    chain_wait();
+    part = behind_wait(part);
+    const int l = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
+    if (j >= p.n) return;
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < shares; ++i) sum += part[((int64_t)i * p.layers + l) * p.n + j];
+    const float before = weights ? behind_wait(weights)[(p.layer0 + l) * weights_stride + j] : 0.0f;
+    out[(p.layer0 + l) * out_stride + j] = fmaf(gain, sum, before);
+}
+
+// Shares of the query rows such that the clusters' last round is full: rounds * (a share's products + reading the keys,
+// which takes as long as one product).
+WeighPlan weigh_plan(int64_t n, int B, int heads, int layers, int device_sms)
+{
+    const int ncl = std::max(1, device_sms / 2);
+    const int64_t tiles = (n + 255) / 256, rows = ((int64_t)B + entries_a_tile(heads) - 1) / entries_a_tile(heads), pairs = (rows + 1) / 2;
+    WeighPlan best{(int)tiles, (int)pairs, 1, (int)(tiles * layers)};
+    int64_t least = INT64_MAX;
+    for (int64_t s = 1; s <= std::min<int64_t>(pairs, 32); ++s) {
+        const int64_t rounds = (tiles * layers * s + ncl - 1) / ncl, cost = rounds * ((pairs + s - 1) / s + 1) + (s > 1 ? 1 : 0);
+        if (cost < least && tiles * layers * s <= INT32_MAX) {
+            least = cost;
+            best.shares = (int)s;
+            best.pieces = (int)(tiles * layers * s);
+        }
+    }
+    return best;
+}
+
+// The prefix as [layers][n][576], box `box` rows by 64 columns; the queries as [B][layers][heads][576], box the
+// entries of a tile by 64 columns.  128-byte swizzle; what lies outside reads as zeros.
+cudaError_t encode_rows(const PrefixShape& p, int all_layers, int box, CUtensorMap* map)
+{
+    TensorMapEncoder encode = nullptr;
+    const cudaError_t e = tensor_map_encoder(&encode);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[3] = {kDim, (cuuint64_t)p.n, (cuuint64_t)all_layers};
+    // the stride of an axis with one entry is never used
+    const cuuint64_t strides[2] = {(cuuint64_t)(p.n > 1 ? p.row_stride : kRowBytes), (cuuint64_t)(all_layers > 1 ? p.layer_stride : kRowBytes)};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(p.rows), dims, strides, boxes, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+cudaError_t encode_queries(const PrefixShape& p, const void* q, CUtensorMap* map)
+{
+    TensorMapEncoder encode = nullptr;
+    const cudaError_t e = tensor_map_encoder(&encode);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[4] = {kDim, (cuuint64_t)p.heads, (cuuint64_t)p.layers, (cuuint64_t)p.B};
+    const cuuint64_t strides[3] = {kRowBytes, (cuuint64_t)kRowBytes * p.heads, (cuuint64_t)kRowBytes * p.heads * p.layers};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)p.heads, 1, (cuuint32_t)entries_a_tile(p.heads)}, ones[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, boxes, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_weigh(const PrefixShape& p, int all_layers, const void* q, const float* lse, const float* weights,
+                         int64_t weights_stride, float* out, int64_t out_stride, float sm_scale, float gain, float* part,
+                         uint32_t* err, int device_sms, cudaStream_t st, bool withhold = false)
+{
+    const WeighPlan plan = weigh_plan(p.n, p.B, p.heads, p.layers, device_sms);
+    CUtensorMap key_map, q_map;
+    cudaError_t e = encode_rows(p, all_layers, kTileRows, &key_map);
+    if (e == cudaSuccess) e = encode_queries(p, q, &q_map);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = 2u * (unsigned)std::min(plan.pieces, std::max(1, device_sms / 2));
+    e = launch_chained(weigh_kernel, dim3(grid), kWThreads, kWSmem, st, key_map, q_map, p, plan, lse, weights, weights_stride, out,
+                       out_stride, part, sm_scale * kLog2e, gain, err, withhold ? 1 : 0);
+    if (e != cudaSuccess || plan.shares == 1) return e;
+    return launch_chained(weigh_sum_kernel, dim3((unsigned)((p.n + 255) / 256), (unsigned)p.layers), 256, 0, st, p, plan.shares,
+                          static_cast<const float*>(part), weights, weights_stride, out, out_stride, gain);
 }
 
 // ---------------------------------------------------------------------------
@@ -249,7 +572,7 @@ int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 cudaError_t prepare_prefix()
 {
     cudaError_t e = cudaFuncSetAttribute(attend_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(weigh_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(weigh_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWSmem);
     return e;
 }
 
@@ -361,7 +684,9 @@ skv_status skv_weigh_prefix_workspace(skv_ctx* ctx, const skv_prefix* prefix, in
                                       int64_t* bytes)
 {
     if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !bytes) return SKV_ERR_INVALID_ARG;
-    *bytes = 16;
+    const int layers = layer < 0 ? ctx->cfg.num_layers : 1;
+    const int shares = B > 0 && prefix->n > 0 ? skv::weigh_plan(prefix->n, B, heads, layers, ctx->device_sms).shares : 1;
+    *bytes = shares > 1 ? skv::align16((int64_t)shares * layers * prefix->n * 4) : 16;
     return SKV_OK;
 }
 
@@ -384,10 +709,8 @@ skv_status skv_weigh_prefix(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, i
         return SKV_ERR_INVALID_ARG;
     const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);
     return on_device(ctx, "skv_weigh_prefix", [&] {
-        skv::weigh_tile_kernel<<<dim3((unsigned)((p.n + skv::kKeys - 1) / skv::kKeys), (unsigned)p.layers), skv::kThreads, skv::kTileSmem, stream>>>(
-            p, static_cast<const uint16_t*>(q_dev), lse_dev, weights_dev, weights_stride, out_dev, out_stride,
-            sm_scale * skv::kLog2e, gain);
-        return cudaGetLastError();
+        return skv::launch_weigh(p, ctx->cfg.num_layers, q_dev, lse_dev, weights_dev, weights_stride, out_dev, out_stride, sm_scale,
+                                 gain, static_cast<float*>(workspace_dev), &ctx->d.ctl[skv::CTL_ERR], ctx->device_sms, stream);
     });
 }
 
