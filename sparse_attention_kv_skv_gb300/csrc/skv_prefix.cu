@@ -33,92 +33,7 @@ struct PrefixShape {
     {
         return reinterpret_cast<const uint4*>(rows + (layer0 + l) * layer_stride + j * row_stride);
     }
-    // A layer's query rows, entries and their heads in order: where row i lies among all [B][layers][heads].
-    __device__ __forceinline__ int64_t q_row(int l, int64_t i) const
-    {
-        const int64_t b = i / heads;
-        return (b * layers + l) * heads + (i - b * heads);
-    }
 };
-
-// ---------------------------------------------------------------------------
-// Sixteen query rows a CTA, the keys in blocks of 32; fp32 products on the cores.
-constexpr int kQRows = 16, kKeys = 32, kThreads = 256;
-constexpr size_t kTileSmem = (size_t)kQRows * kDim * 4 + (size_t)kKeys * kRowBytes;
-
-__device__ __forceinline__ void load_keys(const PrefixShape& p, int l, int j0, uint4* sk)
-{
-    for (int i = threadIdx.x; i < kKeys * (kRowBytes / 16); i += kThreads) {
-        const int j = i / (kRowBytes / 16), c = i % (kRowBytes / 16);
-        sk[i] = j0 + j < p.n ? p.row(l, j0 + j)[c] : make_uint4(0, 0, 0, 0);
-    }
-}
-__device__ __forceinline__ void load_queries(const PrefixShape& p, int l, int64_t i0, const uint16_t* q, float* sq)
-{
-    const int64_t rows = (int64_t)p.B * p.heads;
-    for (int i = threadIdx.x; i < kQRows * kDim; i += kThreads) {
-        const int64_t r = i0 + i / kDim;
-        sq[i] = r < rows ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(q)[p.q_row(l, r) * kDim + i % kDim]) : 0.0f;
-    }
-}
-__device__ __forceinline__ float dot(const float* a, const __nv_bfloat16* b)
-{
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int d = 0; d < kDim; d += 4)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[x] = fmaf(a[d + x], __bfloat162float(b[d + x]), s[x]);
-    return (s[0] + s[1]) + (s[2] + s[3]);
-}
-
-__global__ void __launch_bounds__(kThreads) attend_tile_kernel(PrefixShape p, const uint16_t* __restrict__ q,
-                                                               uint16_t* __restrict__ out, float* __restrict__ lse, float scale_log2)
-{
-    extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ float sp[kQRows][kKeys + 1];
-    float* sq = reinterpret_cast<float*>(smem);
-    uint4* sk = reinterpret_cast<uint4*>(smem + (size_t)kQRows * kDim * 4);
-    const __nv_bfloat16* kb = reinterpret_cast<const __nv_bfloat16*>(sk);
-    const int l = blockIdx.y, r = threadIdx.x / 16, t = threadIdx.x % 16;
-    const int64_t i0 = (int64_t)blockIdx.x * kQRows, rows = (int64_t)p.B * p.heads;
-    load_queries(p, l, i0, q, sq);
-    float acc[32] = {}, m = -INFINITY, total = 0.0f;
-    for (int j0 = 0; j0 < p.n; j0 += kKeys) {
-        __syncthreads();
-        load_keys(p, l, j0, sk);
-        __syncthreads();
-        float s[2], mb = -INFINITY;
-        for (int x = 0; x < 2; ++x) {
-            const int j = t + 16 * x;
-            s[x] = j0 + j < p.n ? dot(sq + r * kDim, kb + j * kDim) * scale_log2 : -INFINITY;
-            mb = fmaxf(mb, s[x]);
-        }
-        for (int o = 1; o < 16; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, o));
-        const float m2 = fmaxf(m, mb), base = m2 == -INFINITY ? 0.0f : m2, fix = exp2f(m - base);
-        float ps = 0.0f;
-        for (int x = 0; x < 2; ++x) {
-            const float e = exp2f(s[x] - base);
-            sp[r][t + 16 * x] = e;
-            ps += e;
-        }
-        for (int o = 1; o < 16; o <<= 1) ps += __shfl_xor_sync(0xFFFFFFFFu, ps, o);
-        total = total * fix + ps;
-        m = m2;
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 32; ++c) acc[c] *= fix;
-        for (int j = 0; j < kKeys; ++j) {
-            const float e = sp[r][j];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) acc[c] = fmaf(e, __bfloat162float(kb[j * kDim + t + 16 * c]), acc[c]);
-        }
-    }
-    if (i0 + r >= rows) return;
-    const int64_t at = p.q_row(l, i0 + r);
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    for (int c = 0; c < 32; ++c)
-        reinterpret_cast<__nv_bfloat16*>(out)[at * kVDim + t + 16 * c] = __float2bfloat16_rn(acc[c] * inv);
-    if (t == 0 && lse) lse[at] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
-}
 
 // ---------------------------------------------------------------------------
 // The kernels on the tensor cores run as clusters of two CTAs that multiply as one
@@ -476,17 +391,436 @@ cudaError_t launch_weigh(const PrefixShape& p, int all_layers, const void* q, co
 }
 
 // ---------------------------------------------------------------------------
-struct JoinParts {
-    const uint4* out[kMaxParts];
-    const float* lse[kMaxParts];
+// Attention.  Tensor memory holds half of a tile's 128 x 512 output beside two score
+// products, so an item of the work is a pair of query tiles (one a CTA, 256 rows of one
+// product) by half of the value dims; both halves take the scores, 1664 instead of 1088 multiply-adds a
+// row and key.  Keys come in blocks of 128:
+//   S = Q K^T   K's rows split over the pair (64 a CTA), 576 dims in columns of 64
+//   O += P V    V's dims split over the pair (128 a CTA)
+// The softmax has a query row a thread (the row's tensor-memory lane); P takes
+// the place of S in tensor memory, as the A operand of the second product.  The scores of
+// block j + 1 are multiplied while the softmax of block j runs.
+// Items that do not fill the clusters evenly are split along the keys; combine_kernel joins their parts.
+constexpr int kBlk = 128;                      // keys of a block
+constexpr int kKRing = 6, kVRing = 2;          // key columns (64 keys x 64 dims, 8 KB), value stages (64 keys x 128 dims, 16 KB)
+constexpr uint32_t kKBox = 64 * 128, kVStage = 2 * kKBox;
+constexpr int kAKeyWarp = 4, kAValueWarp = 5, kAMmaWarp = 6, kAThreads = 224;
+constexpr int kVHalf = kVDim / 2;
+constexpr uint32_t kColO = 0, kColS = 256;     // tensor memory: O 256 columns, S two times 128
+constexpr float kRescaleLog2 = 8.0f;           // the reference maximum is raised when a score passes it by 2^8
+struct alignas(16) AttendCtl {
+    uint64_t q_full[kBoxes], q_free[kBoxes];   // query columns (full: in rank 0, the bytes of both CTAs)
+    uint64_t k_full[kKRing], k_free[kKRing];
+    uint64_t v_full[kVRing], v_free[kVRing];
+    uint64_t s_full[2];                        // scores of a block
+    uint64_t p_full[2];                        // P of a block (in rank 0, a warp of either CTA's softmax)
+    uint64_t pv_done[2];                       // O += P V of a block
+    uint64_t o_free;                           // an item's output has been read (in rank 0, a warp of either CTA)
+    uint64_t fin;                              // every product has completed
+    uint32_t tmem_base, abort;
 };
+constexpr uint32_t kAOffK = kBoxes * kTileBox, kAOffV = kAOffK + kKRing * kKBox, kAOffCtl = kAOffV + kVRing * kVStage,
+                   kASmem = kAOffCtl + sizeof(AttendCtl);
+static_assert(kASmem <= kSmemLimit, "shared memory of attend_prefix_kernel");
 
+struct AttendPlan {
+    int pairs;            // of query tiles, a layer
+    int direct, rest;     // items that clusters do whole, and those that are split
+    int splits, blocks;   // of one of the latter; key blocks a split
+    int all_blocks;       // key blocks of the prefix
+    float* o;             // results of the splits: [rest * splits * 2][256 / 4][128 rows][4], normalised
+    float* lse;           // [rest * splits * 2][128], log2
+    __host__ __device__ int pieces() const { return direct + rest * splits; }
+    // Pieces: the whole items, then the first splits of the others, then their second ones (so that neighbours read the same keys).
+    __device__ int item(int piece) const { return piece < direct ? piece : direct + (piece - direct) % rest; }
+    __device__ int split(int piece) const { return piece < direct ? 0 : (piece - direct) / rest; }
+};
 __device__ __forceinline__ uint32_t bf2(float lo, float hi)
 {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
+    attend_prefix_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap q_map, PrefixShape p,
+                         AttendPlan plan, uint16_t* out, float* lse, float scale_log2, uint32_t* err, int withhold)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    AttendCtl& c = *reinterpret_cast<AttendCtl*>(smem + kAOffCtl);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    const uint32_t rank = blockIdx.x & 1u;
+    const int per = entries_a_tile(p.heads), pieces = plan.pieces();
+    volatile uint32_t* abort = &c.abort;
+
+    chain_next();
+    if (tid == 0) {
+        for (int i = 0; i < kBoxes; ++i) {
+            tc::mbar_init(&c.q_full[i], 1);
+            tc::mbar_init(&c.q_free[i], 1);
+        }
+        for (int i = 0; i < kKRing; ++i) {
+            tc::mbar_init(&c.k_full[i], 1);
+            tc::mbar_init(&c.k_free[i], 1);
+        }
+        for (int i = 0; i < kVRing; ++i) {
+            tc::mbar_init(&c.v_full[i], 1);
+            tc::mbar_init(&c.v_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&c.s_full[i], 1);
+            tc::mbar_init(&c.p_full[i], 8);
+            tc::mbar_init(&c.pv_done[i], 1);
+        }
+        tc::mbar_init(&c.o_free, 8);
+        tc::mbar_init(&c.fin, 1);
+        c.abort = 0u;
+    }
+    if (per * p.heads < kTileRows) {  // query rows behind the last of a tile are zeros for good (a copy writes whole entries only)
+        for (uint32_t i = tid; i < kBoxes * kTileBox / 16; i += kAThreads)
+            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+        tc::fence_smem_async();
+    }
+    if (warp == kAMmaWarp) tc::tmem2_alloc(&c.tmem_base, 512);
+    tc::fence_before_sync();
+    tc::cluster_sync();  // both CTAs' barriers exist
+    tc::fence_after_sync();
+    const uint32_t tbase = c.tmem_base;
+    chain_wait();
+
+    // a piece of the work: layer, pair of query tiles, half of the value dims, key blocks [b0, b1)
+    struct Piece {
+        int l, pair, half, b0, b1;
+    };
+    auto piece_of = [&](int i) {
+        const int item = plan.item(i), rest = item >> 1;
+        Piece w;
+        w.half = item & 1;
+        w.l = rest / plan.pairs;
+        w.pair = rest - w.l * plan.pairs;
+        w.b0 = i < plan.direct ? 0 : plan.split(i) * plan.blocks;
+        w.b1 = i < plan.direct ? plan.all_blocks : min(plan.all_blocks, w.b0 + plan.blocks);
+        return w;
+    };
+
+    if (warp == kAKeyWarp) {
+        if (lane == 0 && !withhold) {
+            // rank 0's barriers count the bytes of both CTAs
+            const uint32_t qf = tc::map_to_rank(tc::smem_u32(&c.q_full[0]), 0), kf = tc::map_to_rank(tc::smem_u32(&c.k_full[0]), 0);
+            const uint32_t q_bytes = (uint32_t)(per * p.heads) * 128u;
+            bool ok = true;
+            int g = 0, n = 0;  // key columns, pieces
+            for (int i = cl; ok && i < pieces; i += ncl, ++n) {
+                const Piece w = piece_of(i);
+                for (int b = w.b0; ok && b < w.b1; ++b)
+                    for (int x = 0; x < kBoxes; ++x, ++g) {
+                        if (b == w.b0) {
+                            if (n > 0 && !(ok = wait_phase(&c.q_free[x], (n - 1) & 1, abort))) break;
+                            if (rank == 0) tc::mbar_arrive_expect_tx(&c.q_full[x], 2 * q_bytes);
+                            tc::tma2_load4(tc::smem_u32(smem) + x * kTileBox, &q_map, 64 * x, 0, w.l, (2 * w.pair + (int)rank) * per,
+                                           qf + 8 * x);
+                        }
+                        const int st = g % kKRing;
+                        if (g >= kKRing && !(ok = wait_phase(&c.k_free[st], ((g / kKRing) - 1) & 1, abort))) break;
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&c.k_full[st], 2 * kKBox);
+                        tc::tma2_load3(tc::smem_u32(smem) + kAOffK + st * kKBox, &key_map, 64 * x, kBlk * b + 64 * (int)rank,
+                                       p.layer0 + w.l, kf + 8 * st);
+                    }
+            }
+            if (!ok) give_up(&c.abort, err);
+        }
+        __syncwarp();
+    } else if (warp == kAValueWarp) {
+        if (lane == 0 && !withhold) {
+            const uint32_t vf = tc::map_to_rank(tc::smem_u32(&c.v_full[0]), 0);
+            bool ok = true;
+            int g = 0;  // value stages
+            for (int i = cl; ok && i < pieces; i += ncl) {
+                const Piece w = piece_of(i);
+                for (int b = 2 * w.b0; b < 2 * w.b1; ++b, ++g) {
+                    const int st = g % kVRing;
+                    if (g >= kVRing && !(ok = wait_phase(&c.v_free[st], ((g / kVRing) - 1) & 1, abort))) break;
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&c.v_full[st], 2 * kVStage);
+                    for (int x = 0; x < 2; ++x)
+                        tc::tma2_load3(tc::smem_u32(smem) + kAOffV + st * kVStage + x * kKBox, &key_map,
+                                       kVHalf * w.half + 128 * (int)rank + 64 * x, 64 * b, p.layer0 + w.l, vf + 8 * st);
+                }
+            }
+            if (!ok) give_up(&c.abort, err);
+        }
+        __syncwarp();
+    } else if (warp == kAMmaWarp) {
+        if (rank == 0) {
+            const uint32_t idesc_s = tc::idesc_bf16_f32(256, kBlk, 0), idesc_o = tc::idesc_bf16_f32(256, kVHalf, 1);
+            const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), base = tc::smem_u32(smem);
+            const uint64_t dq = tc::sw128_kmajor_desc(base), dk = tc::sw128_kmajor_desc(base + kAOffK),
+                           dv = tc::sw128_mnmajor_desc(base + kAOffV, kKBox);
+            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, abort)); };
+            auto wait_both = [&](uint64_t* bar, uint32_t parity) -> bool {
+                return __all_sync(0xFFFFFFFFu, wait_phase_cluster(bar, parity, abort));
+            };
+            bool ok = true;
+            int gk = 0, gv = 0, n = 0, g = 0;  // key columns, value stages, pieces, blocks
+            // O += P V of block j of the call (the piece's first: O = P V, once the piece before has read its O)
+            auto values = [&](int j, bool first) -> bool {
+                if (!wait_both(&c.p_full[j & 1], (j >> 1) & 1)) return false;
+                if (first && n > 0 && !wait_both(&c.o_free, (n - 1) & 1)) return false;
+                for (int h = 0; h < 2; ++h, ++gv) {
+                    const int st = gv % kVRing;
+                    if (!wait(&c.v_full[st], (gv / kVRing) & 1)) return false;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc::mma2_bf16_ta_warp(tb + kColO, tb + kColS + kBlk * (j & 1) + 32 * h + 8 * k,
+                                              dv + ((st * kVStage + 2048 * k) >> 4), idesc_o, !first || h > 0 || k > 0 ? 1u : 0u);
+                    tc::mma2_commit_warp(&c.v_free[st]);
+                }
+                tc::mma2_commit_warp(&c.pv_done[j & 1]);
+                return true;
+            };
+            for (int i = cl; ok && i < pieces; i += ncl, ++n) {
+                const Piece w = piece_of(i);
+                for (int b = w.b0; ok && b < w.b1; ++b, ++g) {
+                    // S into the buffer whose P the product before the last one read
+                    for (int x = 0; x < kBoxes; ++x, ++gk) {
+                        const int st = gk % kKRing;
+                        if (b == w.b0 && !(ok = wait(&c.q_full[x], n & 1))) break;
+                        if (!(ok = wait(&c.k_full[st], (gk / kKRing) & 1))) break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma2_bf16_warp(tb + kColS + kBlk * (g & 1), dq + ((x * kTileBox + 32 * k) >> 4),
+                                               dk + ((st * kKBox + 32 * k) >> 4), idesc_s, x > 0 || k > 0 ? 1u : 0u);
+                        tc::mma2_commit_warp(&c.k_free[st]);
+                        if (b + 1 == w.b1) tc::mma2_commit_warp(&c.q_free[x]);
+                    }
+                    if (!ok) break;
+                    tc::mma2_commit_warp(&c.s_full[g & 1]);
+                    if (b > w.b0) ok = values(g - 1, b == w.b0 + 1);
+                }
+                if (ok) ok = values(g - 1, w.b1 == w.b0 + 1);
+            }
+            if (!ok && lane == 0) give_up(&c.abort, err);
+            tc::mma2_commit_warp(&c.fin);
+        }
+    } else {
+        const uint32_t tl = tbase + ((uint32_t)(warp * 32) << 16);
+        const uint32_t pf = tc::map_to_rank(tc::smem_u32(&c.p_full[0]), 0), of = tc::map_to_rank(tc::smem_u32(&c.o_free), 0);
+        bool ok = true;
+        int g = 0;
+        for (int i = cl; ok && i < pieces; i += ncl) {
+            const Piece w = piece_of(i);
+            float m_ref = -INFINITY;  // reference maximum (log2) that the exponentials use
+            float l_run = 0.0f;       // the sum of P
+            float r_run = 0.0f;       // of P as rounded to bf16, which the output is divided by
+            for (int b = w.b0; b < w.b1; ++b, ++g) {
+                const uint32_t ts = tl + kColS + kBlk * (g & 1);
+                const int left = p.n - kBlk * b;  // keys of the block that exist
+                if (!(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.s_full[g & 1], (g >> 1) & 1, abort)))) break;
+                tc::fence_after_sync();
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c0 = 0; c0 < kBlk; c0 += 32) {
+                    float v[32];
+                    tc::tmem_ld32(ts + c0, v);
+                    if (left < kBlk) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = c0 + j < left ? v[j] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+                }
+                const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
+                float factor = 1.0f;
+                if (mb > m_ref + kRescaleLog2) {
+                    factor = ex2(m_ref - mb);  // (0 from -inf)
+                    m_ref = mb;
+                    l_run *= factor;
+                    r_run *= factor;
+                }
+                if (b > w.b0 && __any_sync(0xFFFFFFFFu, factor != 1.0f)) {  // rescale this warp's rows of O
+                    if (!(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort)))) break;
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kVHalf; c0 += 32) {
+                        float ov[32];
+                        tc::tmem_ld32(tl + kColO + c0, ov);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) ov[j] *= factor;
+                        tc::tmem_st32(tl + kColO + c0, ov);
+                    }
+                }
+                const float neg_m = m_ref == -INFINITY ? 0.0f : -m_ref;  // (only keys that are masked, or NaN)
+                float ls[2] = {0.0f, 0.0f}, rs[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int c0 = 0; c0 < kBlk; c0 += 32) {
+                    float v[32];
+                    tc::tmem_ld32(ts + c0, v);
+                    if (left < kBlk) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = c0 + j < left ? v[j] : -INFINITY;
+                    }
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float p0 = ex2(fmaf(v[2 * j], scale_log2, neg_m)), p1 = ex2(fmaf(v[2 * j + 1], scale_log2, neg_m));
+                        pk[j] = bf2(p0, p1);
+                        ls[0] += p0;
+                        ls[1] += p1;
+                        rs[0] += __uint_as_float(pk[j] << 16);
+                        rs[1] += __uint_as_float(pk[j] & 0xFFFF0000u);
+                    }
+                    // P of keys c0.. into columns c0 / 2.., whose scores have been read
+                    tc::tmem_st8_async(ts + c0 / 2, pk);
+                    tc::tmem_st8_async(ts + c0 / 2 + 8, pk + 8);
+                }
+                l_run += ls[0] + ls[1];
+                r_run += rs[0] + rs[1];
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(pf + 8 * (g & 1));
+            }
+            if (!ok || !(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort)))) break;
+            tc::fence_after_sync();
+            const float inv = r_run == 0.0f ? 0.0f : 1.0f / r_run, lse2 = m_ref + log2f(l_run);  // (0: scores of -inf alone)
+            if (i < plan.direct) {
+                const int64_t row = tile_row(p, w.l, 2 * w.pair + (int)rank, tid);
+                uint16_t* o = out + row * kVDim + kVHalf * w.half;
+#pragma unroll 1
+                for (int c0 = 0; c0 < kVHalf; c0 += 32) {
+                    float ov[32];
+                    tc::tmem_ld32(tl + kColO + c0, ov);
+                    if (row >= 0) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            *reinterpret_cast<uint4*>(o + c0 + j) =
+                                make_uint4(bf2(ov[j] * inv, ov[j + 1] * inv), bf2(ov[j + 2] * inv, ov[j + 3] * inv),
+                                           bf2(ov[j + 4] * inv, ov[j + 5] * inv), bf2(ov[j + 6] * inv, ov[j + 7] * inv));
+                    }
+                }
+                if (w.half == 0 && lse && row >= 0) lse[row] = lse2 * kLn2;
+            } else {
+                const int64_t slot = ((int64_t)(plan.item(i) - plan.direct) * plan.splits + plan.split(i)) * 2 + rank;
+                float4* o = reinterpret_cast<float4*>(plan.o) + slot * (kVHalf / 4) * kTileRows + tid;
+#pragma unroll 1
+                for (int c0 = 0; c0 < kVHalf; c0 += 32) {
+                    float ov[32];
+                    tc::tmem_ld32(tl + kColO + c0, ov);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        o[(c0 + j) / 4 * kTileRows] = make_float4(ov[j] * inv, ov[j + 1] * inv, ov[j + 2] * inv, ov[j + 3] * inv);
+                }
+                plan.lse[slot * kTileRows + tid] = lse2;
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(of);
+        }
+        if (!ok) give_up(&c.abort, err);
+    }
+    pair_exit(&c.fin, &c.abort, err, tbase, warp == kAMmaWarp, 512);
+}
+
+// The splits of an item joined: with lse_i their log2 sums and M the largest, out = sum 2^(lse_i - M) o_i / sum 2^(lse_i - M).
+// A thread a row and four columns.
+__global__ void __launch_bounds__(512) combine_prefix_kernel(PrefixShape p, AttendPlan plan, uint16_t* out, float* lse)
+{
+    chain_next();
+    chain_wait();
+    const int r = threadIdx.x % kTileRows, col4 = blockIdx.x * 4 + threadIdx.x / kTileRows, rank = blockIdx.y & 1;
+    const int item = plan.direct + (int)(blockIdx.y >> 1), half = item & 1, l = (item >> 1) / plan.pairs, pair = (item >> 1) % plan.pairs;
+    const int64_t row = tile_row(p, l, 2 * pair + rank, r);
+    if (row < 0) return;
+    const int64_t slot0 = (int64_t)(item - plan.direct) * plan.splits * 2 + rank;
+    const float* ls = behind_wait(plan.lse) + slot0 * kTileRows + r;
+    const float4* po = reinterpret_cast<const float4*>(behind_wait(plan.o)) + (slot0 * (kVHalf / 4) + col4) * kTileRows + r;
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int i = 0; i < plan.splits; ++i) m = fmaxf(m, ls[(int64_t)i * 2 * kTileRows]);
+    const float base = m == -INFINITY ? 0.0f : m;  // (only NaN)
+    float acc[4] = {}, total = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < plan.splits; ++i) {
+        const float w = ex2(ls[(int64_t)i * 2 * kTileRows] - base);
+        const float4 o = po[(int64_t)i * 2 * (kVHalf / 4) * kTileRows];
+        total += w;
+        acc[0] = fmaf(w, o.x, acc[0]);
+        acc[1] = fmaf(w, o.y, acc[1]);
+        acc[2] = fmaf(w, o.z, acc[2]);
+        acc[3] = fmaf(w, o.w, acc[3]);
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    *reinterpret_cast<uint2*>(out + row * kVDim + kVHalf * half + 4 * col4) =
+        make_uint2(bf2(acc[0] * inv, acc[1] * inv), bf2(acc[2] * inv, acc[3] * inv));
+    if (col4 == 0 && half == 0 && lse) lse[row] = (base + log2f(total)) * kLn2;
+}
+
+// What an attention over an empty prefix returns.
+__global__ void __launch_bounds__(256) nothing_kernel(int64_t rows, uint4* out, float* lse)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * (kVDim / 8); i += (int64_t)gridDim.x * 256) {
+        out[i] = make_uint4(0, 0, 0, 0);
+        if (lse && i < rows) lse[i] = -INFINITY;
+    }
+}
+
+// Whole items for full rounds of the clusters; the rest in splits such that its rounds are short: rounds * (blocks + what
+// a piece costs besides, 1.5 blocks), and the joining of the parts.
+AttendPlan attend_plan(int64_t n, int B, int heads, int layers, int device_sms)
+{
+    const int ncl = std::max(1, device_sms / 2), nblk = (int)((n + kBlk - 1) / kBlk);
+    const int64_t tiles = ((int64_t)B + entries_a_tile(heads) - 1) / entries_a_tile(heads), pairs = (tiles + 1) / 2, items = pairs * layers * 2;
+    AttendPlan a{(int)pairs, (int)(items / ncl * ncl), (int)(items % ncl), 1, nblk, nblk, nullptr, nullptr};
+    if (a.rest == 0) return a;
+    double least = 1e30;
+    for (int k = 1; k <= std::min(nblk, 64); ++k) {
+        const int blocks = (nblk + k - 1) / k;
+        if ((nblk + blocks - 1) / blocks != k) continue;  // the last splits would be empty
+        const double cost = (double)((a.rest * (int64_t)k + ncl - 1) / ncl) * (blocks + 1.5) + (k > 1 ? 1.5 + 0.05 * k : 0.0);
+        if (cost < least) {
+            least = cost;
+            a.splits = k;
+            a.blocks = blocks;
+        }
+    }
+    if (a.splits == 1) {
+        a.direct += a.rest;
+        a.rest = 0;
+    }
+    return a;
+}
+int64_t attend_bytes(const AttendPlan& a) { return (int64_t)a.rest * a.splits * 2 * kTileRows * (kVHalf + 1) * 4; }
+
+cudaError_t launch_attend_prefix(const PrefixShape& p, int all_layers, const void* q, void* out, float* lse, float sm_scale,
+                                 void* workspace, uint32_t* err, int device_sms, cudaStream_t st, bool withhold = false)
+{
+    if (p.n == 0) {
+        const int64_t rows = (int64_t)p.B * p.layers * p.heads;
+        nothing_kernel<<<(unsigned)std::min<int64_t>((rows * (kVDim / 8) + 255) / 256, 1 << 16), 256, 0, st>>>(rows, static_cast<uint4*>(out), lse);
+        return cudaGetLastError();
+    }
+    AttendPlan plan = attend_plan(p.n, p.B, p.heads, p.layers, device_sms);
+    plan.o = static_cast<float*>(workspace);
+    plan.lse = plan.o + (int64_t)plan.rest * plan.splits * 2 * kTileRows * kVHalf;
+    CUtensorMap key_map, q_map;
+    cudaError_t e = encode_rows(p, all_layers, 64, &key_map);
+    if (e == cudaSuccess) e = encode_queries(p, q, &q_map);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = 2u * (unsigned)std::min(plan.pieces(), std::max(1, device_sms / 2));
+    e = launch_chained(attend_prefix_kernel, dim3(grid), kAThreads, kASmem, st, key_map, q_map, p, plan, static_cast<uint16_t*>(out), lse,
+                       sm_scale * kLog2e, err, withhold ? 1 : 0);
+    if (e != cudaSuccess || plan.rest == 0) return e;
+    return launch_chained(combine_prefix_kernel, dim3(kVHalf / 16, 2u * (unsigned)plan.rest), 512, 0, st, p, plan,
+                          static_cast<uint16_t*>(out), lse);
+}
+
+// ---------------------------------------------------------------------------
+struct JoinParts {
+    const uint4* out[kMaxParts];
+    const float* lse[kMaxParts];
+};
 
 // A warp a row, 16 columns a lane.  All of a row is read before any of it is written, so the result may
 // take a part's place.
@@ -571,7 +905,7 @@ int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 cudaError_t prepare_prefix()
 {
-    cudaError_t e = cudaFuncSetAttribute(attend_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
+    cudaError_t e = cudaFuncSetAttribute(attend_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kASmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(weigh_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWSmem);
     return e;
 }
@@ -634,6 +968,8 @@ skv_status skv_attend_prefix_workspace(skv_ctx* ctx, const skv_prefix* prefix, i
 {
     if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !bytes) return SKV_ERR_INVALID_ARG;
     *bytes = 16;
+    if (B > 0 && prefix->n > 0)
+        *bytes = std::max<int64_t>(16, skv::attend_bytes(skv::attend_plan(prefix->n, B, heads, layer < 0 ? ctx->cfg.num_layers : 1, ctx->device_sms)));
     return SKV_OK;
 }
 
@@ -651,10 +987,8 @@ skv_status skv_attend_prefix(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, 
         return SKV_ERR_INVALID_ARG;
     const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);
     return on_device(ctx, "skv_attend_prefix", [&] {
-        const int64_t groups = ((int64_t)B * heads + skv::kQRows - 1) / skv::kQRows;
-        skv::attend_tile_kernel<<<dim3((unsigned)groups, (unsigned)p.layers), skv::kThreads, skv::kTileSmem, stream>>>(
-            p, static_cast<const uint16_t*>(q_dev), static_cast<uint16_t*>(out_dev), lse_dev, sm_scale * skv::kLog2e);
-        return cudaGetLastError();
+        return skv::launch_attend_prefix(p, ctx->cfg.num_layers, q_dev, out_dev, lse_dev, sm_scale, workspace_dev,
+                                         &ctx->d.ctl[skv::CTL_ERR], ctx->device_sms, stream);
     });
 }
 
