@@ -26,6 +26,7 @@ struct skv_ctx {
     float* q4_scratch = nullptr;  // partial results of skv_attend_q4 (contexts of packed rows only)
     int attend_sms = 0;     // SMs the attention kernel may occupy (0: all)
     int device_sms = 0;     // SMs of the context's device
+    int prefix_clusters = 0;  // clusters of skv_attend_prefix that fit on it at once
     int pool_node_wanted = -1;   // host NUMA node the pool was asked to live on (-1: none)
     int pool_node_seen = -1;     // node holding most sampled pool pages (-1: not reported)
     float pool_node_frac = 0.0f; // share of the sampled pages on pool_node_seen
@@ -72,7 +73,7 @@ cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_
 cudaError_t launch_heaviest(const Dev& d, const float* weights, int64_t weights_stride, int units, int n, int keep,
                             int first, int last, int32_t* kept, void* workspace, int device_sms, cudaStream_t st);
 // Kernels around a shared prefix (skv_prefix.cu): once per context, on its device.
-cudaError_t prepare_prefix();
+cudaError_t prepare_prefix(int* clusters);  // *clusters: those of skv_attend_prefix that are on the chip at once
 // Loads skv_assemble_noalloc's static work list on `device` (current) and
 // caches its address, so that no later call loads or allocates anything.
 cudaError_t noalloc_prepare(int device);

@@ -56,16 +56,6 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const
     }
     return false;
 }
-// The same for a barrier that threads of both CTAs arrive on.
-__device__ __forceinline__ bool wait_phase_cluster(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort)
-{
-    const uint32_t a = tc::smem_u32(bar);
-    for (uint32_t i = 0; i < kMaxSleepPolls; ++i) {
-        if (tc::mbar_test_cluster(a, parity)) return true;
-        if ((i & 7u) == 7u && *abort) return false;
-    }
-    return false;
-}
 __device__ __forceinline__ void give_up(uint32_t* abort, uint32_t* err)
 {
     if (!*(volatile uint32_t*)abort) {
@@ -231,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
                 piece_of(i, l, tile, p0, p1);
                 for (int pr = p0; ok && pr < p1; ++pr, ++it) {
                     const int d = it & 1;
-                    if (it >= 2 && !(ok = __all_sync(0xFFFFFFFFu, wait_phase_cluster(&c.d_free[d], ((it >> 1) - 1) & 1, abort)))) break;
+                    if (it >= 2 && !(ok = wait(&c.d_free[d], ((it >> 1) - 1) & 1))) break;
                     for (int x = 0; x < kBoxes; ++x, ++g) {
                         const int st = g % kWRing;
                         if (pr == p0 && !(ok = wait(&c.a_full[x], n & 1))) break;
@@ -241,14 +231,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
                         for (int k = 0; k < 4; ++k)
                             tc::mma2_bf16_warp(tb + 256 * d, da + ((x * kTileBox + 32 * k) >> 4), db + ((st * kTileBox + 32 * k) >> 4),
                                                idesc, x > 0 || k > 0 ? 1u : 0u);
-                        tc::mma2_commit_warp(&c.b_free[st]);
-                        if (pr + 1 == p1) tc::mma2_commit_warp(&c.a_free[x]);
+                        tc::mma2_commit_warp(&c.b_free[st], 3);
+                        if (pr + 1 == p1) tc::mma2_commit_warp(&c.a_free[x], 3);
                     }
-                    if (ok) tc::mma2_commit_warp(&c.d_full[d]);
+                    if (ok) tc::mma2_commit_warp(&c.d_full[d], 3);
                 }
             }
             if (!ok && lane == 0) give_up(&c.abort, err);
-            tc::mma2_commit_warp(&c.fin);
+            tc::mma2_commit_warp(&c.fin, 3);
         }
     } else {
         const uint32_t tl = tbase + ((uint32_t)(warp * 32) << 16);
@@ -289,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
                     }
                     tc::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(df + 8 * d);
+                    if (lane == 0) tc::mbar_arrive_at(df + 8 * d);
                 }
             }
             const int j = 256 * tile + 128 * (int)rank + tid;
@@ -391,45 +381,58 @@ cudaError_t launch_weigh(const PrefixShape& p, int all_layers, const void* q, co
 }
 
 // ---------------------------------------------------------------------------
-// Attention.  Tensor memory holds half of a tile's 128 x 512 output beside two score
-// products, so an item of the work is a pair of query tiles (one a CTA, 256 rows of one
-// product) by half of the value dims; both halves take the scores, 1664 instead of 1088 multiply-adds a
-// row and key.  Keys come in blocks of 128:
-//   S = Q K^T   K's rows split over the pair (64 a CTA), 576 dims in columns of 64
-//   O += P V    V's dims split over the pair (128 a CTA)
-// The softmax has a query row a thread (the row's tensor-memory lane); P takes
-// the place of S in tensor memory, as the A operand of the second product.  The scores of
-// block j + 1 are multiplied while the softmax of block j runs.
-// Items that do not fill the clusters evenly are split along the keys; combine_kernel joins their parts.
-constexpr int kBlk = 128;                      // keys of a block
-constexpr int kKRing = 6, kVRing = 2;          // key columns (64 keys x 64 dims, 8 KB), value stages (64 keys x 128 dims, 16 KB)
-constexpr uint32_t kKBox = 64 * 128, kVStage = 2 * kKBox;
-constexpr int kAKeyWarp = 4, kAValueWarp = 5, kAMmaWarp = 6, kAThreads = 224;
+// Attention.  Tensor memory holds half of a tile's 128 x 512 output beside the scores, so
+// a cluster of four CTAs, two pairs that multiply as one each, takes an item of the work: a pair
+// of query tiles (256 rows of a product).  CTA (h, r), of pair h and row tile r, owns the value dims
+// [256h, 256h + 256) of tile r, and of every block of 128 keys its pair scores the keys [64h, 64h + 64):
+//   S = Q K^T   256 rows, the pair's 64 keys (32 from either CTA), 576 dims in columns of 64
+//   O += P V    256 rows, 128 keys, the pair's 256 value dims (128 from either CTA)
+// so nothing is multiplied twice.  The CTAs (0, r) and (1, r) swap their row maxima (both take the same reference
+// maximum) and their halves of P, and at an item's end their shares of the sums.
+// The softmax has a query row a thread (the row's tensor-memory lane).  It takes the exponentials with the
+// reference there is while the maxima travel, and again if it has risen.  P goes into shared memory, by
+// a bulk copy into the other pair's as well.  O += P V of a block is issued kLag scores later, which
+// hides the way from S to P.
+// Items that do not fill the clusters evenly are split along the keys; combine_prefix_kernel joins their parts.
+constexpr int kBlk = 128, kHalfBlk = 64;       // keys of a block, and those that a pair scores
+constexpr int kKRing = 2, kVRing = 2;          // key stages (32 keys, 36 KB), value stages (64 keys x 128 dims, 16 KB)
+constexpr uint32_t kKBox = 32 * 128, kKStage = kBoxes * kKBox, kVBox = 64 * 128, kVStage = 2 * kVBox;
+constexpr uint32_t kPBox = kTileRows * 128, kPTile = 2 * kPBox;  // P: 128 rows x 64 keys of a pair, both pairs' (two tiles)
 constexpr int kVHalf = kVDim / 2;
-constexpr uint32_t kColO = 0, kColS = 256;     // tensor memory: O 256 columns, S two times 128
+constexpr int kQtBoxes = 6, kQsBoxes = kBoxes - kQtBoxes;  // query columns in tensor memory, in shared memory
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;    // tensor memory: O 256 columns, S 64, Q 192
+constexpr int kLag = 2;
+constexpr int kQWarp0 = 4, kAKeyWarp = 8, kAValueWarp = 9, kAMmaWarp = 10, kAPassWarp = 11, kAThreads = 384;
 constexpr float kRescaleLog2 = 8.0f;           // the reference maximum is raised when a score passes it by 2^8
 struct alignas(16) AttendCtl {
-    uint64_t q_full[kBoxes], q_free[kBoxes];   // query columns (full: in rank 0, the bytes of both CTAs)
-    uint64_t k_full[kKRing], k_free[kKRing];
-    uint64_t v_full[kVRing], v_free[kVRing];
-    uint64_t s_full[2];                        // scores of a block
-    uint64_t p_full[2];                        // P of a block (in rank 0, a warp of either CTA's softmax)
-    uint64_t pv_done[2];                       // O += P V of a block
-    uint64_t o_free;                           // an item's output has been read (in rank 0, a warp of either CTA)
-    uint64_t fin;                              // every product has completed
+    // "leader": the barrier of the pair's first CTA, which multiplies
+    uint64_t q_full, q_tm, q_free;             // queries in shared memory (leader, bytes of both CTAs), in tensor memory
+                                               // (leader, a warp of either CTA); the item's scores are done (both)
+    uint64_t k_full[kKRing], k_free[kKRing];   // key columns (leader, bytes of both; both)
+    uint64_t v_full[kVRing], v_free[kVRing];   // value stages
+    uint64_t s_full, s_free;                   // a block's scores are complete (both); have been read (leader, a warp of either)
+    uint64_t m_full[2];                        // the other pair's maxima of a block have arrived (512 bytes)
+    uint64_t x_full[2];                        // the other pair's half of a P tile has arrived (16 KB)
+    uint64_t p_full[2];                        // a P tile is complete (leader: a warp of either CTA, and either's pass warp)
+    uint64_t pv_done[2][2];                    // [pair][tile]: O += P V of a block has completed (all four CTAs)
+    uint64_t l_full;                           // the other pair's shares of the sums have arrived (1024 bytes)
+    uint64_t o_free;                           // an item's output has been read (leader, a warp of either CTA)
+    uint64_t fin;                              // every product of the pair has completed
+    float mx[2][kTileRows], lx[kTileRows], rx[kTileRows];  // the other pair's maxima and sums
     uint32_t tmem_base, abort;
 };
-constexpr uint32_t kAOffK = kBoxes * kTileBox, kAOffV = kAOffK + kKRing * kKBox, kAOffCtl = kAOffV + kVRing * kVStage,
-                   kASmem = kAOffCtl + sizeof(AttendCtl);
-static_assert(kASmem <= kSmemLimit, "shared memory of attend_prefix_kernel");
+constexpr uint32_t kAOffP = kQsBoxes * kTileBox, kAOffK = kAOffP + 2 * kPTile, kAOffV = kAOffK + kKRing * kKStage,
+                   kAOffCtl = kAOffV + kVRing * kVStage, kASmem = kAOffCtl + sizeof(AttendCtl);
+static_assert(kASmem <= kSmemLimit && kAOffV % 1024 == 0, "shared memory of attend_prefix_kernel");
+static_assert(kColQ + kQtBoxes * 32 <= 512, "tensor memory of attend_prefix_kernel");
 
 struct AttendPlan {
     int pairs;            // of query tiles, a layer
     int direct, rest;     // items that clusters do whole, and those that are split
     int splits, blocks;   // of one of the latter; key blocks a split
     int all_blocks;       // key blocks of the prefix
-    float* o;             // results of the splits: [rest * splits * 2][256 / 4][128 rows][4], normalised
-    float* lse;           // [rest * splits * 2][128], log2
+    float* o;             // results of the splits: [rest * splits * 4 CTAs][256 / 4][128 rows][4], normalised
+    float* lse;           // [rest * splits * 2 tiles][128], log2
     __host__ __device__ int pieces() const { return direct + rest * splits; }
     // Pieces: the whole items, then the first splits of the others, then their second ones (so that neighbours read the same keys).
     __device__ int item(int piece) const { return piece < direct ? piece : direct + (piece - direct) % rest; }
@@ -442,24 +445,24 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi)
     return r;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
-    attend_prefix_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap q_map, PrefixShape p,
-                         AttendPlan plan, uint16_t* out, float* lse, float scale_log2, uint32_t* err, int withhold)
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
+    attend_prefix_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap value_map,
+                         const __grid_constant__ CUtensorMap q_map, PrefixShape p, AttendPlan plan, const uint16_t* q,
+                         uint16_t* out, float* lse, float scale_log2, uint32_t* err, int withhold)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     AttendCtl& c = *reinterpret_cast<AttendCtl*>(smem + kAOffCtl);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
-    const uint32_t rank = blockIdx.x & 1u;
+    const int cl = blockIdx.x >> 2, ncl = gridDim.x >> 2;
+    const uint32_t rank = blockIdx.x & 3u, half = rank >> 1, r = rank & 1u, leader = rank & 2u, peer = rank ^ 2u;
     const int per = entries_a_tile(p.heads), pieces = plan.pieces();
     volatile uint32_t* abort = &c.abort;
 
     chain_next();
     if (tid == 0) {
-        for (int i = 0; i < kBoxes; ++i) {
-            tc::mbar_init(&c.q_full[i], 1);
-            tc::mbar_init(&c.q_free[i], 1);
-        }
+        tc::mbar_init(&c.q_full, 1);
+        tc::mbar_init(&c.q_tm, 8);
+        tc::mbar_init(&c.q_free, 1);
         for (int i = 0; i < kKRing; ++i) {
             tc::mbar_init(&c.k_full[i], 1);
             tc::mbar_init(&c.k_free[i], 1);
@@ -468,72 +471,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
             tc::mbar_init(&c.v_full[i], 1);
             tc::mbar_init(&c.v_free[i], 1);
         }
+        tc::mbar_init(&c.s_full, 1);
+        tc::mbar_init(&c.s_free, 8);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&c.s_full[i], 1);
-            tc::mbar_init(&c.p_full[i], 8);
-            tc::mbar_init(&c.pv_done[i], 1);
+            tc::mbar_init(&c.m_full[i], 1);
+            tc::mbar_init(&c.x_full[i], 1);
+            tc::mbar_init(&c.p_full[i], 10);
+            tc::mbar_init(&c.pv_done[0][i], 1);
+            tc::mbar_init(&c.pv_done[1][i], 1);
         }
+        tc::mbar_init(&c.l_full, 1);
         tc::mbar_init(&c.o_free, 8);
         tc::mbar_init(&c.fin, 1);
         c.abort = 0u;
     }
     if (per * p.heads < kTileRows) {  // query rows behind the last of a tile are zeros for good (a copy writes whole entries only)
-        for (uint32_t i = tid; i < kBoxes * kTileBox / 16; i += kAThreads)
+        for (uint32_t i = tid; i < kQsBoxes * kTileBox / 16; i += kAThreads)
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
         tc::fence_smem_async();
     }
     if (warp == kAMmaWarp) tc::tmem2_alloc(&c.tmem_base, 512);
     tc::fence_before_sync();
-    tc::cluster_sync();  // both CTAs' barriers exist
+    tc::cluster_sync();  // all CTAs' barriers exist
     tc::fence_after_sync();
     const uint32_t tbase = c.tmem_base;
     chain_wait();
 
-    // a piece of the work: layer, pair of query tiles, half of the value dims, key blocks [b0, b1)
+    // a piece of the work: layer, pair of query tiles, key blocks [b0, b1)
     struct Piece {
-        int l, pair, half, b0, b1;
+        int l, pair, b0, b1;
     };
     auto piece_of = [&](int i) {
-        const int item = plan.item(i), rest = item >> 1;
+        const int item = plan.item(i);
         Piece w;
-        w.half = item & 1;
-        w.l = rest / plan.pairs;
-        w.pair = rest - w.l * plan.pairs;
+        w.l = item / plan.pairs;
+        w.pair = item - w.l * plan.pairs;
         w.b0 = i < plan.direct ? 0 : plan.split(i) * plan.blocks;
         w.b1 = i < plan.direct ? plan.all_blocks : min(plan.all_blocks, w.b0 + plan.blocks);
         return w;
     };
+    auto at_leader = [&](uint64_t* bar) { return tc::map_to_rank(tc::smem_u32(bar), leader); };
 
     if (warp == kAKeyWarp) {
         if (lane == 0 && !withhold) {
-            // rank 0's barriers count the bytes of both CTAs
-            const uint32_t qf = tc::map_to_rank(tc::smem_u32(&c.q_full[0]), 0), kf = tc::map_to_rank(tc::smem_u32(&c.k_full[0]), 0);
-            const uint32_t q_bytes = (uint32_t)(per * p.heads) * 128u;
+            const uint32_t qf = at_leader(&c.q_full), kf = at_leader(&c.k_full[0]), q_bytes = (uint32_t)(per * p.heads) * 128u;
             bool ok = true;
-            int g = 0, n = 0;  // key columns, pieces
+            int g = 0, n = 0;  // blocks, pieces
             for (int i = cl; ok && i < pieces; i += ncl, ++n) {
                 const Piece w = piece_of(i);
-                for (int b = w.b0; ok && b < w.b1; ++b)
-                    for (int x = 0; x < kBoxes; ++x, ++g) {
-                        if (b == w.b0) {
-                            if (n > 0 && !(ok = wait_phase(&c.q_free[x], (n - 1) & 1, abort))) break;
-                            if (rank == 0) tc::mbar_arrive_expect_tx(&c.q_full[x], 2 * q_bytes);
-                            tc::tma2_load4(tc::smem_u32(smem) + x * kTileBox, &q_map, 64 * x, 0, w.l, (2 * w.pair + (int)rank) * per,
-                                           qf + 8 * x);
-                        }
-                        const int st = g % kKRing;
-                        if (g >= kKRing && !(ok = wait_phase(&c.k_free[st], ((g / kKRing) - 1) & 1, abort))) break;
-                        if (rank == 0) tc::mbar_arrive_expect_tx(&c.k_full[st], 2 * kKBox);
-                        tc::tma2_load3(tc::smem_u32(smem) + kAOffK + st * kKBox, &key_map, 64 * x, kBlk * b + 64 * (int)rank,
-                                       p.layer0 + w.l, kf + 8 * st);
+                for (int b = w.b0; b < w.b1; ++b, ++g) {
+                    const int st = g % kKRing;
+                    if (g >= kKRing && !(ok = wait_phase(&c.k_free[st], ((g / kKRing) - 1) & 1, abort))) break;
+                    if (r == 0) tc::mbar_arrive_expect_tx(&c.k_full[st], 2 * kKStage);
+#pragma unroll
+                    for (int x = 0; x < kBoxes; ++x)
+                        tc::tma2_load3(tc::smem_u32(smem) + kAOffK + st * kKStage + x * kKBox, &key_map, 64 * x,
+                                       kBlk * b + kHalfBlk * (int)half + 32 * (int)r, p.layer0 + w.l, kf + 8 * st);
+                    if (b == w.b0) {
+                        if (n > 0 && !(ok = wait_phase(&c.q_free, (n - 1) & 1, abort))) break;
+                        if (r == 0) tc::mbar_arrive_expect_tx(&c.q_full, 2 * kQsBoxes * q_bytes);
+                        for (int y = 0; y < kQsBoxes; ++y)
+                            tc::tma2_load4(tc::smem_u32(smem) + y * kTileBox, &q_map, 64 * (kQtBoxes + y), 0, w.l,
+                                           (2 * w.pair + (int)r) * per, qf);
                     }
+                }
             }
             if (!ok) give_up(&c.abort, err);
         }
         __syncwarp();
     } else if (warp == kAValueWarp) {
         if (lane == 0 && !withhold) {
-            const uint32_t vf = tc::map_to_rank(tc::smem_u32(&c.v_full[0]), 0);
+            const uint32_t vf = at_leader(&c.v_full[0]);
             bool ok = true;
             int g = 0;  // value stages
             for (int i = cl; ok && i < pieces; i += ncl) {
@@ -541,97 +549,177 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
                 for (int b = 2 * w.b0; b < 2 * w.b1; ++b, ++g) {
                     const int st = g % kVRing;
                     if (g >= kVRing && !(ok = wait_phase(&c.v_free[st], ((g / kVRing) - 1) & 1, abort))) break;
-                    if (rank == 0) tc::mbar_arrive_expect_tx(&c.v_full[st], 2 * kVStage);
+                    if (r == 0) tc::mbar_arrive_expect_tx(&c.v_full[st], 2 * kVStage);
                     for (int x = 0; x < 2; ++x)
-                        tc::tma2_load3(tc::smem_u32(smem) + kAOffV + st * kVStage + x * kKBox, &key_map,
-                                       kVHalf * w.half + 128 * (int)rank + 64 * x, 64 * b, p.layer0 + w.l, vf + 8 * st);
+                        tc::tma2_load3(tc::smem_u32(smem) + kAOffV + st * kVStage + x * kVBox, &value_map,
+                                       kVHalf * (int)half + 128 * (int)r + 64 * x, 64 * b, p.layer0 + w.l, vf + 8 * st);
                 }
             }
             if (!ok) give_up(&c.abort, err);
         }
         __syncwarp();
     } else if (warp == kAMmaWarp) {
-        if (rank == 0) {
-            const uint32_t idesc_s = tc::idesc_bf16_f32(256, kBlk, 0), idesc_o = tc::idesc_bf16_f32(256, kVHalf, 1);
+        if (r == 0) {
+            const uint32_t idesc_s = tc::idesc_bf16_f32(256, kHalfBlk, 0), idesc_o = tc::idesc_bf16_f32(256, kVHalf, 1);
             const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), base = tc::smem_u32(smem);
-            const uint64_t dq = tc::sw128_kmajor_desc(base), dk = tc::sw128_kmajor_desc(base + kAOffK),
-                           dv = tc::sw128_mnmajor_desc(base + kAOffV, kKBox);
+            const uint32_t mine = 3u << __shfl_sync(0xFFFFFFFFu, leader, 0);  // the CTAs of this pair
+            const uint32_t hp = __shfl_sync(0xFFFFFFFFu, half, 0);
+            const uint64_t dq = tc::sw128_kmajor_desc(base), dp = tc::sw128_kmajor_desc(base + kAOffP),
+                           dk = tc::sw128_kmajor_desc(base + kAOffK), dv = tc::sw128_mnmajor_desc(base + kAOffV, kVBox);
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, abort)); };
-            auto wait_both = [&](uint64_t* bar, uint32_t parity) -> bool {
-                return __all_sync(0xFFFFFFFFu, wait_phase_cluster(bar, parity, abort));
-            };
             bool ok = true;
-            int gk = 0, gv = 0, n = 0, g = 0;  // key columns, value stages, pieces, blocks
+            int gv = 0, n = 0, g = 0;  // value stages, pieces, blocks
             // O += P V of block j of the call (the piece's first: O = P V, once the piece before has read its O)
             auto values = [&](int j, bool first) -> bool {
-                if (!wait_both(&c.p_full[j & 1], (j >> 1) & 1)) return false;
-                if (first && n > 0 && !wait_both(&c.o_free, (n - 1) & 1)) return false;
+                if (!wait(&c.p_full[j & 1], (j >> 1) & 1)) return false;
+                if (first && n > 0 && !wait(&c.o_free, (n - 1) & 1)) return false;
                 for (int h = 0; h < 2; ++h, ++gv) {
                     const int st = gv % kVRing;
                     if (!wait(&c.v_full[st], (gv / kVRing) & 1)) return false;
                     tc::fence_after_sync();
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        tc::mma2_bf16_ta_warp(tb + kColO, tb + kColS + kBlk * (j & 1) + 32 * h + 8 * k,
-                                              dv + ((st * kVStage + 2048 * k) >> 4), idesc_o, !first || h > 0 || k > 0 ? 1u : 0u);
-                    tc::mma2_commit_warp(&c.v_free[st]);
+                        tc::mma2_bf16_warp(tb + kColO, dp + (((j & 1) * kPTile + h * kPBox + 32 * k) >> 4),
+                                           dv + ((st * kVStage + 2048 * k) >> 4), idesc_o, !first || h > 0 || k > 0 ? 1u : 0u);
+                    tc::mma2_commit_warp(&c.v_free[st], mine);
                 }
-                tc::mma2_commit_warp(&c.pv_done[j & 1]);
+                tc::mma2_commit_warp(&c.pv_done[hp][j & 1], 15);
                 return true;
             };
             for (int i = cl; ok && i < pieces; i += ncl, ++n) {
                 const Piece w = piece_of(i);
-                for (int b = w.b0; ok && b < w.b1; ++b, ++g) {
-                    // S into the buffer whose P the product before the last one read
-                    for (int x = 0; x < kBoxes; ++x, ++gk) {
-                        const int st = gk % kKRing;
-                        if (b == w.b0 && !(ok = wait(&c.q_full[x], n & 1))) break;
-                        if (!(ok = wait(&c.k_full[st], (gk / kKRing) & 1))) break;
-                        tc::fence_after_sync();
+                const int blocks = w.b1 - w.b0, g0 = g;
+                if (!(ok = wait(&c.q_tm, n & 1))) break;
+                for (int b = 0; ok && b < blocks; ++b, ++g) {
+                    if (g > 0 && !(ok = wait(&c.s_free, (g - 1) & 1))) break;
+                    const int st = g % kKRing;
+                    if (b == 0 && !(ok = wait(&c.q_full, n & 1))) break;
+                    if (!(ok = wait(&c.k_full[st], (g / kKRing) & 1))) break;
+                    tc::fence_after_sync();
+                    // unrolled, so that each descriptor is the stage's plus a constant (32 cycles a product are left to issue it)
+                    const uint64_t ds = dk + ((st * kKStage) >> 4);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc::mma2_bf16_warp(tb + kColS + kBlk * (g & 1), dq + ((x * kTileBox + 32 * k) >> 4),
-                                               dk + ((st * kKBox + 32 * k) >> 4), idesc_s, x > 0 || k > 0 ? 1u : 0u);
-                        tc::mma2_commit_warp(&c.k_free[st]);
-                        if (b + 1 == w.b1) tc::mma2_commit_warp(&c.q_free[x]);
-                    }
-                    if (!ok) break;
-                    tc::mma2_commit_warp(&c.s_full[g & 1]);
-                    if (b > w.b0) ok = values(g - 1, b == w.b0 + 1);
+                    for (int x = 0; x < kBoxes; ++x)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (x < kQtBoxes)
+                                tc::mma2_bf16_ta_warp(tb + kColS, tb + kColQ + 32 * x + 8 * k, ds + ((x * kKBox + 32 * k) >> 4), idesc_s,
+                                                      x > 0 || k > 0 ? 1u : 0u);
+                            else
+                                tc::mma2_bf16_warp(tb + kColS, dq + (((x - kQtBoxes) * kTileBox + 32 * k) >> 4),
+                                                   ds + ((x * kKBox + 32 * k) >> 4), idesc_s, 1u);
+                        }
+                    tc::mma2_commit_warp(&c.k_free[st], mine);
+                    if (b + 1 == blocks) tc::mma2_commit_warp(&c.q_free, mine);
+                    tc::mma2_commit_warp(&c.s_full, mine);
+                    if (b >= kLag) ok = values(g - kLag, b == kLag);
                 }
-                if (ok) ok = values(g - 1, w.b1 == w.b0 + 1);
+                for (int j = max(g0, g - kLag); ok && j < g; ++j) ok = values(j, j == g0);
             }
             if (!ok && lane == 0) give_up(&c.abort, err);
-            tc::mma2_commit_warp(&c.fin);
+            tc::mma2_commit_warp(&c.fin, mine);
         }
+    } else if (warp == kAPassWarp) {
+        // tells the pair's first CTA that the other pair's half of P has arrived here
+        if (lane == 0) {
+            const uint32_t pf = at_leader(&c.p_full[0]);
+            bool ok = true;
+            int g = 0;
+            for (int i = cl; ok && i < pieces; i += ncl) {
+                const Piece w = piece_of(i);
+                for (int b = w.b0; b < w.b1; ++b, ++g) {
+                    tc::mbar_arrive_expect_tx(&c.x_full[g & 1], kPBox);
+                    if (!(ok = wait_phase(&c.x_full[g & 1], (g >> 1) & 1, abort))) break;
+                    tc::fence_smem_async();
+                    tc::mbar_arrive_at(pf + 8 * (g & 1));
+                }
+            }
+            if (!ok) give_up(&c.abort, err);
+        }
+        __syncwarp();
+    } else if (warp >= kQWarp0) {
+        // the first 384 dims of the item's queries into tensor memory, a row a thread
+        const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16) + kColQ, qt = at_leader(&c.q_tm);
+        const uint4* rows = reinterpret_cast<const uint4*>(behind_wait(q));
+        bool ok = true;
+        int n = 0;
+        for (int i = cl; i < pieces; i += ncl, ++n) {
+            const Piece w = piece_of(i);
+            const int64_t row = tile_row(p, w.l, 2 * w.pair + (int)r, tid - 32 * kQWarp0);
+            if (n > 0 && !(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.q_free, (n - 1) & 1, abort)))) break;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int x = 0; x < kQtBoxes; x += 2) {
+                uint4 v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = row >= 0 ? rows[row * (kRowBytes / 16) + 8 * x + j] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    const uint32_t a[8] = {v[j].x, v[j].y, v[j].z, v[j].w, v[j + 1].x, v[j + 1].y, v[j + 1].z, v[j + 1].w};
+                    tc::tmem_st8_async(tl + 32 * x + 4 * j, a);
+                }
+            }
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_at(qt);
+        }
+        if (!ok) give_up(&c.abort, err);
     } else {
         const uint32_t tl = tbase + ((uint32_t)(warp * 32) << 16);
-        const uint32_t pf = tc::map_to_rank(tc::smem_u32(&c.p_full[0]), 0), of = tc::map_to_rank(tc::smem_u32(&c.o_free), 0);
+        const uint32_t sf = at_leader(&c.s_free), pf = at_leader(&c.p_full[0]), of = at_leader(&c.o_free);
+        const uint32_t mx_peer = tc::map_to_rank(tc::smem_u32(&c.mx[0][tid]), peer), mf_peer = tc::map_to_rank(tc::smem_u32(&c.m_full[0]), peer);
+        const uint32_t lx_peer = tc::map_to_rank(tc::smem_u32(&c.lx[tid]), peer), rx_peer = tc::map_to_rank(tc::smem_u32(&c.rx[tid]), peer);
+        const uint32_t lf_peer = tc::map_to_rank(tc::smem_u32(&c.l_full), peer), xf_peer = tc::map_to_rank(tc::smem_u32(&c.x_full[0]), peer);
+        // this warp's rows of this pair's half of P tile 0, here and at the other pair's CTA of the same rows
+        const uint32_t p_at = kAOffP + half * kPBox + (uint32_t)warp * 4096u;
+        const uint32_t p_mine = tc::smem_u32(smem) + p_at, p_peer = tc::map_to_rank(p_mine, peer);
         bool ok = true;
-        int g = 0;
-        for (int i = cl; ok && i < pieces; i += ncl) {
+        int g = 0, n = 0;
+        auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, abort)); };
+        for (int i = cl; ok && i < pieces; i += ncl, ++n) {
             const Piece w = piece_of(i);
-            float m_ref = -INFINITY;  // reference maximum (log2) that the exponentials use
-            float l_run = 0.0f;       // the sum of P
+            float m_ref = -INFINITY;  // reference maximum (log2) that the exponentials use; the same in both pairs
+            float l_run = 0.0f;       // the sum of P over this pair's keys
             float r_run = 0.0f;       // of P as rounded to bf16, which the output is divided by
             for (int b = w.b0; b < w.b1; ++b, ++g) {
-                const uint32_t ts = tl + kColS + kBlk * (g & 1);
-                const int left = p.n - kBlk * b;  // keys of the block that exist
-                if (!(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.s_full[g & 1], (g >> 1) & 1, abort)))) break;
+                const int bb = g & 1, left = p.n - kBlk * b - kHalfBlk * (int)half;  // keys of this pair's half that exist
+                if (!(ok = wait(&c.s_full, g & 1))) break;
                 tc::fence_after_sync();
+                float v[kHalfBlk];
+                tc::tmem_ld32(tl + kColS, *reinterpret_cast<float(*)[32]>(v));
+                tc::tmem_ld32(tl + kColS + 32, *reinterpret_cast<float(*)[32]>(v + 32));
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_at(sf);
+                if (left < kHalfBlk) {
+#pragma unroll
+                    for (int j = 0; j < kHalfBlk; ++j) v[j] = j < left ? v[j] : -INFINITY;
+                }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c0 = 0; c0 < kBlk; c0 += 32) {
-                    float v[32];
-                    tc::tmem_ld32(ts + c0, v);
-                    if (left < kBlk) {
+                for (int j = 0; j < kHalfBlk; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+                const float mloc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (tid == 0) tc::mbar_arrive_expect_tx(&c.m_full[bb], kTileRows * 4);
+                tc::st_async4(mx_peer + bb * kTileRows * 4, mloc, mf_peer + 8 * bb);
+                uint32_t pk[kHalfBlk / 2];
+                float ls[2], rs[2];
+                auto exponentials = [&]() {
+                    const float neg_m = m_ref == -INFINITY ? 0.0f : -m_ref;  // (only keys that are masked, or NaN)
+                    ls[0] = ls[1] = rs[0] = rs[1] = 0.0f;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = c0 + j < left ? v[j] : -INFINITY;
+                    for (int j = 0; j < kHalfBlk / 2; ++j) {
+                        const float p0 = ex2(fmaf(v[2 * j], scale_log2, neg_m)), p1 = ex2(fmaf(v[2 * j + 1], scale_log2, neg_m));
+                        pk[j] = bf2(p0, p1);
+                        ls[0] += p0;
+                        ls[1] += p1;
+                        rs[0] += __uint_as_float(pk[j] << 16);
+                        rs[1] += __uint_as_float(pk[j] & 0xFFFF0000u);
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-                }
-                const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
+                };
+                if (b > w.b0) exponentials();
+                if (!(ok = wait(&c.m_full[bb], (g >> 1) & 1))) break;
+                const float mb = fmaxf(mloc, c.mx[bb][tid]) * scale_log2;
                 float factor = 1.0f;
                 if (mb > m_ref + kRescaleLog2) {
                     factor = ex2(m_ref - mb);  // (0 from -inf)
@@ -639,8 +727,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
                     l_run *= factor;
                     r_run *= factor;
                 }
-                if (b > w.b0 && __any_sync(0xFFFFFFFFu, factor != 1.0f)) {  // rescale this warp's rows of O
-                    if (!(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort)))) break;
+                if (b == w.b0) {
+                    exponentials();
+                } else if (__any_sync(0xFFFFFFFFu, factor != 1.0f)) {
+                    exponentials();
+                    // rescale this warp's rows of O
+                    if (!(ok = wait(&c.pv_done[half][bb ^ 1], ((g - 1) >> 1) & 1))) break;
                     tc::fence_after_sync();
 #pragma unroll 1
                     for (int c0 = 0; c0 < kVHalf; c0 += 32) {
@@ -650,49 +742,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
                         for (int j = 0; j < 32; ++j) ov[j] *= factor;
                         tc::tmem_st32(tl + kColO + c0, ov);
                     }
-                }
-                const float neg_m = m_ref == -INFINITY ? 0.0f : -m_ref;  // (only keys that are masked, or NaN)
-                float ls[2] = {0.0f, 0.0f}, rs[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int c0 = 0; c0 < kBlk; c0 += 32) {
-                    float v[32];
-                    tc::tmem_ld32(ts + c0, v);
-                    if (left < kBlk) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = c0 + j < left ? v[j] : -INFINITY;
-                    }
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float p0 = ex2(fmaf(v[2 * j], scale_log2, neg_m)), p1 = ex2(fmaf(v[2 * j + 1], scale_log2, neg_m));
-                        pk[j] = bf2(p0, p1);
-                        ls[0] += p0;
-                        ls[1] += p1;
-                        rs[0] += __uint_as_float(pk[j] << 16);
-                        rs[1] += __uint_as_float(pk[j] & 0xFFFF0000u);
-                    }
-                    // P of keys c0.. into columns c0 / 2.., whose scores have been read
-                    tc::tmem_st8_async(ts + c0 / 2, pk);
-                    tc::tmem_st8_async(ts + c0 / 2 + 8, pk + 8);
+                    tc::fence_before_sync();
                 }
                 l_run += ls[0] + ls[1];
                 r_run += rs[0] + rs[1];
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
+                // P tile bb is free, here and there, once both pairs have multiplied block g - 2 by it
+                if (g >= 2 && !(ok = wait(&c.pv_done[0][bb], ((g >> 1) - 1) & 1) && wait(&c.pv_done[1][bb], ((g >> 1) - 1) & 1))) break;
+                uint8_t* row = smem + p_at + bb * kPTile + lane * 128;
+#pragma unroll
+                for (int j = 0; j < kHalfBlk / 8; ++j)  // 16-byte pieces where the swizzle puts them
+                    *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+                tc::fence_smem_async();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(pf + 8 * (g & 1));
+                if (lane == 0) {
+                    tc::bulk_to_peer(p_peer + bb * kPTile, p_mine + bb * kPTile, 4096, xf_peer + 8 * bb);
+                    tc::mbar_arrive_at(pf + 8 * bb);
+                }
             }
-            if (!ok || !(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort)))) break;
+            if (!ok) break;
+            // the sums: pair 0's share + pair 1's, in that order in both
+            if (tid == 0) tc::mbar_arrive_expect_tx(&c.l_full, kTileRows * 8);
+            tc::st_async4(lx_peer, l_run, lf_peer);
+            tc::st_async4(rx_peer, r_run, lf_peer);
+            if (!(ok = wait(&c.pv_done[half][(g - 1) & 1], ((g - 1) >> 1) & 1) && wait(&c.l_full, n & 1))) break;
             tc::fence_after_sync();
-            const float inv = r_run == 0.0f ? 0.0f : 1.0f / r_run, lse2 = m_ref + log2f(l_run);  // (0: scores of -inf alone)
+            const float l_all = half == 0 ? l_run + c.lx[tid] : c.lx[tid] + l_run;
+            const float r_all = half == 0 ? r_run + c.rx[tid] : c.rx[tid] + r_run;
+            const float inv = r_all == 0.0f ? 0.0f : 1.0f / r_all, lse2 = m_ref + log2f(l_all);  // (0: scores of -inf alone)
             if (i < plan.direct) {
-                const int64_t row = tile_row(p, w.l, 2 * w.pair + (int)rank, tid);
-                uint16_t* o = out + row * kVDim + kVHalf * w.half;
+                const int64_t at = tile_row(p, w.l, 2 * w.pair + (int)r, tid);
+                uint16_t* o = out + at * kVDim + kVHalf * (int)half;
 #pragma unroll 1
                 for (int c0 = 0; c0 < kVHalf; c0 += 32) {
                     float ov[32];
                     tc::tmem_ld32(tl + kColO + c0, ov);
-                    if (row >= 0) {
+                    if (at >= 0) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 8)
                             *reinterpret_cast<uint4*>(o + c0 + j) =
@@ -700,10 +784,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
                                            bf2(ov[j + 4] * inv, ov[j + 5] * inv), bf2(ov[j + 6] * inv, ov[j + 7] * inv));
                     }
                 }
-                if (w.half == 0 && lse && row >= 0) lse[row] = lse2 * kLn2;
+                if (half == 0 && lse && at >= 0) lse[at] = lse2 * kLn2;
             } else {
-                const int64_t slot = ((int64_t)(plan.item(i) - plan.direct) * plan.splits + plan.split(i)) * 2 + rank;
-                float4* o = reinterpret_cast<float4*>(plan.o) + slot * (kVHalf / 4) * kTileRows + tid;
+                const int64_t slot = (int64_t)(plan.item(i) - plan.direct) * plan.splits + plan.split(i);
+                float4* o = reinterpret_cast<float4*>(plan.o) + (4 * slot + rank) * (kVHalf / 4) * kTileRows + tid;
 #pragma unroll 1
                 for (int c0 = 0; c0 < kVHalf; c0 += 32) {
                     float ov[32];
@@ -712,11 +796,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAThreads, 1)
                     for (int j = 0; j < 32; j += 4)
                         o[(c0 + j) / 4 * kTileRows] = make_float4(ov[j] * inv, ov[j + 1] * inv, ov[j + 2] * inv, ov[j + 3] * inv);
                 }
-                plan.lse[slot * kTileRows + tid] = lse2;
+                if (half == 0) plan.lse[(2 * slot + r) * kTileRows + tid] = lse2;
             }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(of);
+            if (lane == 0) tc::mbar_arrive_at(of);
         }
         if (!ok) give_up(&c.abort, err);
     }
@@ -729,13 +813,13 @@ __global__ void __launch_bounds__(512) combine_prefix_kernel(PrefixShape p, Atte
 {
     chain_next();
     chain_wait();
-    const int r = threadIdx.x % kTileRows, col4 = blockIdx.x * 4 + threadIdx.x / kTileRows, rank = blockIdx.y & 1;
-    const int item = plan.direct + (int)(blockIdx.y >> 1), half = item & 1, l = (item >> 1) / plan.pairs, pair = (item >> 1) % plan.pairs;
-    const int64_t row = tile_row(p, l, 2 * pair + rank, r);
-    if (row < 0) return;
-    const int64_t slot0 = (int64_t)(item - plan.direct) * plan.splits * 2 + rank;
-    const float* ls = behind_wait(plan.lse) + slot0 * kTileRows + r;
-    const float4* po = reinterpret_cast<const float4*>(behind_wait(plan.o)) + (slot0 * (kVHalf / 4) + col4) * kTileRows + r;
+    const int row = threadIdx.x % kTileRows, col4 = blockIdx.x * 4 + threadIdx.x / kTileRows;
+    const int rank = blockIdx.y & 3, half = rank >> 1, r = rank & 1, item = plan.direct + (int)(blockIdx.y >> 2);
+    const int l = item / plan.pairs, pair = item - l * plan.pairs;
+    const int64_t at = tile_row(p, l, 2 * pair + r, row), slot0 = (int64_t)(item - plan.direct) * plan.splits;
+    if (at < 0) return;
+    const float* ls = behind_wait(plan.lse) + (2 * slot0 + r) * kTileRows + row;
+    const float4* po = reinterpret_cast<const float4*>(behind_wait(plan.o)) + ((4 * slot0 + rank) * (kVHalf / 4) + col4) * kTileRows + row;
     float m = -INFINITY;
 #pragma unroll 8
     for (int i = 0; i < plan.splits; ++i) m = fmaxf(m, ls[(int64_t)i * 2 * kTileRows]);
@@ -744,7 +828,7 @@ __global__ void __launch_bounds__(512) combine_prefix_kernel(PrefixShape p, Atte
 #pragma unroll 8
     for (int i = 0; i < plan.splits; ++i) {
         const float w = ex2(ls[(int64_t)i * 2 * kTileRows] - base);
-        const float4 o = po[(int64_t)i * 2 * (kVHalf / 4) * kTileRows];
+        const float4 o = po[(int64_t)i * kVHalf * kTileRows];
         total += w;
         acc[0] = fmaf(w, o.x, acc[0]);
         acc[1] = fmaf(w, o.y, acc[1]);
@@ -752,9 +836,9 @@ __global__ void __launch_bounds__(512) combine_prefix_kernel(PrefixShape p, Atte
         acc[3] = fmaf(w, o.w, acc[3]);
     }
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    *reinterpret_cast<uint2*>(out + row * kVDim + kVHalf * half + 4 * col4) =
+    *reinterpret_cast<uint2*>(out + at * kVDim + kVHalf * half + 4 * col4) =
         make_uint2(bf2(acc[0] * inv, acc[1] * inv), bf2(acc[2] * inv, acc[3] * inv));
-    if (col4 == 0 && half == 0 && lse) lse[row] = (base + log2f(total)) * kLn2;
+    if (col4 == 0 && half == 0 && lse) lse[at] = (base + log2f(total)) * kLn2;
 }
 
 // What an attention over an empty prefix returns.
@@ -768,17 +852,17 @@ __global__ void __launch_bounds__(256) nothing_kernel(int64_t rows, uint4* out, 
 
 // Whole items for full rounds of the clusters; the rest in splits such that its rounds are short: rounds * (blocks + what
 // a piece costs besides, 1.5 blocks), and the joining of the parts.
-AttendPlan attend_plan(int64_t n, int B, int heads, int layers, int device_sms)
+AttendPlan attend_plan(int64_t n, int B, int heads, int layers, int ncl)
 {
-    const int ncl = std::max(1, device_sms / 2), nblk = (int)((n + kBlk - 1) / kBlk);
-    const int64_t tiles = ((int64_t)B + entries_a_tile(heads) - 1) / entries_a_tile(heads), pairs = (tiles + 1) / 2, items = pairs * layers * 2;
+    const int nblk = (int)((n + kBlk - 1) / kBlk);
+    const int64_t tiles = ((int64_t)B + entries_a_tile(heads) - 1) / entries_a_tile(heads), pairs = (tiles + 1) / 2, items = pairs * layers;
     AttendPlan a{(int)pairs, (int)(items / ncl * ncl), (int)(items % ncl), 1, nblk, nblk, nullptr, nullptr};
     if (a.rest == 0) return a;
     double least = 1e30;
     for (int k = 1; k <= std::min(nblk, 64); ++k) {
         const int blocks = (nblk + k - 1) / k;
         if ((nblk + blocks - 1) / blocks != k) continue;  // the last splits would be empty
-        const double cost = (double)((a.rest * (int64_t)k + ncl - 1) / ncl) * (blocks + 1.5) + (k > 1 ? 1.5 + 0.05 * k : 0.0);
+        const double cost = (double)((a.rest * (int64_t)k + ncl - 1) / ncl) * (blocks + 2.5) + (k > 1 ? 2.0 + 0.07 * k : 0.0);
         if (cost < least) {
             least = cost;
             a.splits = k;
@@ -791,28 +875,29 @@ AttendPlan attend_plan(int64_t n, int B, int heads, int layers, int device_sms)
     }
     return a;
 }
-int64_t attend_bytes(const AttendPlan& a) { return (int64_t)a.rest * a.splits * 2 * kTileRows * (kVHalf + 1) * 4; }
+int64_t attend_bytes(const AttendPlan& a) { return (int64_t)a.rest * a.splits * 2 * kTileRows * (kVDim + 1) * 4; }
 
 cudaError_t launch_attend_prefix(const PrefixShape& p, int all_layers, const void* q, void* out, float* lse, float sm_scale,
-                                 void* workspace, uint32_t* err, int device_sms, cudaStream_t st, bool withhold = false)
+                                 void* workspace, uint32_t* err, int clusters, cudaStream_t st, bool withhold = false)
 {
     if (p.n == 0) {
         const int64_t rows = (int64_t)p.B * p.layers * p.heads;
         nothing_kernel<<<(unsigned)std::min<int64_t>((rows * (kVDim / 8) + 255) / 256, 1 << 16), 256, 0, st>>>(rows, static_cast<uint4*>(out), lse);
         return cudaGetLastError();
     }
-    AttendPlan plan = attend_plan(p.n, p.B, p.heads, p.layers, device_sms);
+    AttendPlan plan = attend_plan(p.n, p.B, p.heads, p.layers, clusters);
     plan.o = static_cast<float*>(workspace);
-    plan.lse = plan.o + (int64_t)plan.rest * plan.splits * 2 * kTileRows * kVHalf;
-    CUtensorMap key_map, q_map;
-    cudaError_t e = encode_rows(p, all_layers, 64, &key_map);
+    plan.lse = plan.o + (int64_t)plan.rest * plan.splits * 2 * kTileRows * kVDim;
+    CUtensorMap key_map, value_map, q_map;
+    cudaError_t e = encode_rows(p, all_layers, 32, &key_map);
+    if (e == cudaSuccess) e = encode_rows(p, all_layers, 64, &value_map);
     if (e == cudaSuccess) e = encode_queries(p, q, &q_map);
     if (e != cudaSuccess) return e;
-    const unsigned grid = 2u * (unsigned)std::min(plan.pieces(), std::max(1, device_sms / 2));
-    e = launch_chained(attend_prefix_kernel, dim3(grid), kAThreads, kASmem, st, key_map, q_map, p, plan, static_cast<uint16_t*>(out), lse,
-                       sm_scale * kLog2e, err, withhold ? 1 : 0);
+    e = launch_chained(attend_prefix_kernel, dim3(4u * (unsigned)std::min(plan.pieces(), clusters)), kAThreads, kASmem, st, key_map, value_map,
+                       q_map, p, plan, static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), lse, sm_scale * kLog2e, err,
+                       withhold ? 1 : 0);
     if (e != cudaSuccess || plan.rest == 0) return e;
-    return launch_chained(combine_prefix_kernel, dim3(kVHalf / 16, 2u * (unsigned)plan.rest), 512, 0, st, p, plan,
+    return launch_chained(combine_prefix_kernel, dim3(kVHalf / 16, 4u * (unsigned)plan.rest), 512, 0, st, p, plan,
                           static_cast<uint16_t*>(out), lse);
 }
 
@@ -903,10 +988,24 @@ int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 }  // namespace
 
-cudaError_t prepare_prefix()
+cudaError_t prepare_prefix(int* clusters)
 {
     cudaError_t e = cudaFuncSetAttribute(attend_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kASmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(weigh_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWSmem);
+    if (e != cudaSuccess) return e;
+    // clusters of four that are on the chip at once (its processors come in groups that are no multiple of four)
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(4);
+    cfg.blockDim = dim3(kAThreads);
+    cfg.dynamicSmemBytes = kASmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 4;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(clusters, attend_prefix_kernel, &cfg);
+    if (*clusters < 1) *clusters = 1;
     return e;
 }
 
@@ -969,7 +1068,7 @@ skv_status skv_attend_prefix_workspace(skv_ctx* ctx, const skv_prefix* prefix, i
     if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !bytes) return SKV_ERR_INVALID_ARG;
     *bytes = 16;
     if (B > 0 && prefix->n > 0)
-        *bytes = std::max<int64_t>(16, skv::attend_bytes(skv::attend_plan(prefix->n, B, heads, layer < 0 ? ctx->cfg.num_layers : 1, ctx->device_sms)));
+        *bytes = std::max<int64_t>(16, skv::attend_bytes(skv::attend_plan(prefix->n, B, heads, layer < 0 ? ctx->cfg.num_layers : 1, ctx->prefix_clusters)));
     return SKV_OK;
 }
 
@@ -988,7 +1087,7 @@ skv_status skv_attend_prefix(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, 
     const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);
     return on_device(ctx, "skv_attend_prefix", [&] {
         return skv::launch_attend_prefix(p, ctx->cfg.num_layers, q_dev, out_dev, lse_dev, sm_scale, workspace_dev,
-                                         &ctx->d.ctl[skv::CTL_ERR], ctx->device_sms, stream);
+                                         &ctx->d.ctl[skv::CTL_ERR], ctx->prefix_clusters, stream);
     });
 }
 

@@ -465,7 +465,7 @@ skv_status skv_create(const skv_config* cfg, skv_ctx** out)
     SKV_TRY(skv::prepare_step_kernels(c.topk, c.hot_slots, &x->gather_grid));
     SKV_TRY(skv::prepare_attend(&x->device_sms));
     SKV_TRY(skv::prepare_select());
-    SKV_TRY(skv::prepare_prefix());
+    SKV_TRY(skv::prepare_prefix(&x->prefix_clusters));
     SKV_TRY(skv::noalloc_prepare(c.device));
     if (c.row_bytes == skv::q4::kRowBytes)  // skv_attend_q4 may be called on this context
         SKV_ALLOC(cudaMalloc(&x->q4_scratch, skv::attend_q4_scratch_bytes(x->device_sms)));

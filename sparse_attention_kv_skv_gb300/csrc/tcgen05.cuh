@@ -359,14 +359,14 @@ __device__ __forceinline__ void mma2_bf16_ta_warp(uint32_t d_tmem, uint32_t a_tm
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrive on `bar` of both CTAs once every such product issued so far has completed.
-__device__ __forceinline__ void mma2_commit_warp(uint64_t* bar)
+// Arrive on `bar` of the cluster's CTAs in `ctas` (a bit a rank) once every such product issued so far has completed.
+__device__ __forceinline__ void mma2_commit_warp(uint64_t* bar, uint32_t ctas)
 {
     asm volatile(
         "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
         " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)ctas)
         : "memory");
 }
 // Tensor memory of both CTAs, by one whole warp of each.
@@ -398,22 +398,21 @@ __device__ __forceinline__ void tma2_load4(uint32_t dst, const void* map, int x,
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
-// Arrive on a barrier of either CTA, whose waiters acquire at cluster scope.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+// `bytes` of this CTA's shared memory to another CTA of the cluster, completing on a barrier of that one
+// (addresses that map_to_rank gave; 16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void bulk_to_peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
-// mbar_test for arrivals of both CTAs.
-__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar_addr, uint32_t parity)
+// Arrive on a barrier of any CTA of the cluster (an address that map_to_rank gave).  No memory has to become visible to
+// the other CTA's threads: what such an arrival announces is tensor memory that has been read or written (tcgen05.wait
+// and tcgen05.fence before it), or this CTA's own shared memory as the tensor core will read it (a proxy fence before
+// it).  So the release is the CTA's; a cluster-scope one waits some 2000 cycles for everything in flight.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
 {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar_addr), "r"(parity), "n"(kSuspendNs)
-        : "memory");
-    return done != 0;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Bring the 128-byte line at `p` (global memory) into L2.
