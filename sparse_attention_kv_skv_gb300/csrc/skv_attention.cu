@@ -49,6 +49,7 @@
 #include <cmath>
 #include <string>
 
+#include "f32x2.cuh"
 #include "q4.cuh"
 #include "skv_ctx.cuh"
 #include "tcgen05.cuh"
@@ -221,22 +222,6 @@ __host__ __device__ inline AttnLayout attend_layout(uint32_t raw_bytes = 0)
     }
 }
 
-// Two floats to a bf16 pair (lo in the low half), round to nearest even.
-__device__ __forceinline__ uint32_t bf2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// 2^x on the special-function unit (approximate, denormal results flush to
-// zero; -inf gives 0).  The softmax feeds it x <= 8.
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 struct alignas(16) AttnCtl {
     uint64_t full[kMaxStages];   // key stage landed (TMA transaction bytes; one arrive per loader)
     uint64_t empty[kMaxStages];  // key stage consumed by its last product
@@ -294,27 +279,6 @@ __device__ __forceinline__ void issue_scores_q4(uint32_t tbase, uint64_t dk, uin
         tc::mma_bf16_ta_warp(tbase + kColS, tbase + kColQ + 8u * st,
                              st < kVHalf / 16 ? dk + (((st >> 2) * kBoxBytes + (st & 3) * 32u) >> 4) : dr + (st & 3) * 2u,
                              idesc, st > 0 ? 1u : 0u);
-}
-
-// Two fp32 numbers side by side, for one instruction on both.
-__device__ __forceinline__ uint64_t pair(float lo, float hi)
-{
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
-    return p;
-}
-__device__ __forceinline__ void split(uint64_t p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
 }
 
 // A partial score crosses the CTA pair as the upper 24 bits of its fp32

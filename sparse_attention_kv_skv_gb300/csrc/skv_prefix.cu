@@ -13,6 +13,7 @@
 #include <cmath>
 #include <string>
 
+#include "f32x2.cuh"
 #include "skv_ctx.cuh"
 #include "tcgen05.cuh"
 
@@ -50,6 +51,7 @@ __host__ __device__ __forceinline__ int entries_a_tile(int heads) { return kTile
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort)
 {
     const uint32_t a = tc::smem_u32(bar);
+#pragma unroll 1
     for (uint32_t i = 0; i < kMaxSleepPolls; ++i) {
         if (tc::mbar_test(a, parity)) return true;
         if ((i & 7u) == 7u && *abort) return false;
@@ -82,14 +84,6 @@ __device__ __forceinline__ void pair_exit(uint64_t* fin, uint32_t* abort, uint32
         tc::fence_after_sync();
         tc::tmem2_dealloc(tbase, cols);
     }
-}
-
-// 2^x on the special-function unit (approximate; -inf gives 0)
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // The query row that lies in row r of tile `tile`: its unit's first head's row plus its head, or -1.
@@ -135,7 +129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     WeighCtl& c = *reinterpret_cast<WeighCtl*>(smem + kWOffCtl);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;  // (the compiler sees that a warp stays together)
     const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
     const uint32_t rank = blockIdx.x & 1u;
     const int per = entries_a_tile(p.heads);
@@ -227,10 +221,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
                         if (pr == p0 && !(ok = wait(&c.a_full[x], n & 1))) break;
                         if (!(ok = wait(&c.b_full[st], (g / kWRing) & 1))) break;
                         tc::fence_after_sync();
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc::mma2_bf16_warp(tb + 256 * d, da + ((x * kTileBox + 32 * k) >> 4), db + ((st * kTileBox + 32 * k) >> 4),
-                                               idesc, x > 0 || k > 0 ? 1u : 0u);
+                        tc::mma2_bf16_x4_warp<2, 2>(tb + 256 * d, da + ((x * kTileBox) >> 4), db + ((st * kTileBox) >> 4), idesc,
+                                                    x > 0 ? 1u : 0u);
                         tc::mma2_commit_warp(&c.b_free[st], 3);
                         if (pr + 1 == p1) tc::mma2_commit_warp(&c.a_free[x], 3);
                     }
@@ -391,8 +383,7 @@ cudaError_t launch_weigh(const PrefixShape& p, int all_layers, const void* q, co
 // maximum) and their halves of P, and at an item's end their shares of the sums.
 // The softmax has a query row a thread (the row's tensor-memory lane).  It takes the exponentials with the
 // reference there is while the maxima travel, and again if it has risen.  P goes into shared memory, by
-// a bulk copy into the other pair's as well.  O += P V of a block is issued kLag scores later, which
-// hides the way from S to P.
+// a bulk copy into the other pair's as well.
 // Items that do not fill the clusters evenly are split along the keys; combine_prefix_kernel joins their parts.
 constexpr int kBlk = 128, kHalfBlk = 64;       // keys of a block, and those that a pair scores
 constexpr int kKRing = 2, kVRing = 2;          // key stages (32 keys, 36 KB), value stages (64 keys x 128 dims, 16 KB)
@@ -401,8 +392,7 @@ constexpr uint32_t kPBox = kTileRows * 128, kPTile = 2 * kPBox;  // P: 128 rows 
 constexpr int kVHalf = kVDim / 2;
 constexpr int kQtBoxes = 6, kQsBoxes = kBoxes - kQtBoxes;  // query columns in tensor memory, in shared memory
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;    // tensor memory: O 256 columns, S 64, Q 192
-constexpr int kLag = 2;
-constexpr int kQWarp0 = 4, kAKeyWarp = 8, kAValueWarp = 9, kAMmaWarp = 10, kAPassWarp = 11, kAThreads = 384;
+constexpr int kQWarp0 = 4, kAKeyWarp = 8, kAValueWarp = 9, kAScoreWarp = 10, kAValueMmaWarp = 11, kAThreads = 384;
 constexpr float kRescaleLog2 = 8.0f;           // the reference maximum is raised when a score passes it by 2^8
 struct alignas(16) AttendCtl {
     // "leader": the barrier of the pair's first CTA, which multiplies
@@ -413,11 +403,11 @@ struct alignas(16) AttendCtl {
     uint64_t s_full, s_free;                   // a block's scores are complete (both); have been read (leader, a warp of either)
     uint64_t m_full[2];                        // the other pair's maxima of a block have arrived (512 bytes)
     uint64_t x_full[2];                        // the other pair's half of a P tile has arrived (16 KB)
-    uint64_t p_full[2];                        // a P tile is complete (leader: a warp of either CTA, and either's pass warp)
-    uint64_t pv_done[2][2];                    // [pair][tile]: O += P V of a block has completed (all four CTAs)
+    uint64_t p_full[2];                        // a P tile is complete (leader: a warp of either CTA, and the second CTA once x_full)
+    uint64_t pv_done[2];                       // O += P V of a block has completed in both pairs (all four CTAs)
     uint64_t l_full;                           // the other pair's shares of the sums have arrived (1024 bytes)
     uint64_t o_free;                           // an item's output has been read (leader, a warp of either CTA)
-    uint64_t fin;                              // every product of the pair has completed
+    uint64_t fin;                              // every product of the pair has completed (both streams)
     float mx[2][kTileRows], lx[kTileRows], rx[kTileRows];  // the other pair's maxima and sums
     uint32_t tmem_base, abort;
 };
@@ -438,13 +428,6 @@ struct AttendPlan {
     __device__ int item(int piece) const { return piece < direct ? piece : direct + (piece - direct) % rest; }
     __device__ int split(int piece) const { return piece < direct ? 0 : (piece - direct) / rest; }
 };
-__device__ __forceinline__ uint32_t bf2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
     attend_prefix_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap value_map,
                          const __grid_constant__ CUtensorMap q_map, PrefixShape p, AttendPlan plan, const uint16_t* q,
@@ -452,7 +435,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     AttendCtl& c = *reinterpret_cast<AttendCtl*>(smem + kAOffCtl);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;  // (the compiler sees that a warp stays together)
     const int cl = blockIdx.x >> 2, ncl = gridDim.x >> 2;
     const uint32_t rank = blockIdx.x & 3u, half = rank >> 1, r = rank & 1u, leader = rank & 2u, peer = rank ^ 2u;
     const int per = entries_a_tile(p.heads), pieces = plan.pieces();
@@ -476,13 +459,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&c.m_full[i], 1);
             tc::mbar_init(&c.x_full[i], 1);
-            tc::mbar_init(&c.p_full[i], 10);
-            tc::mbar_init(&c.pv_done[0][i], 1);
-            tc::mbar_init(&c.pv_done[1][i], 1);
+            tc::mbar_init(&c.p_full[i], 9);
+            tc::mbar_init(&c.pv_done[i], 2);
         }
         tc::mbar_init(&c.l_full, 1);
         tc::mbar_init(&c.o_free, 8);
-        tc::mbar_init(&c.fin, 1);
+        tc::mbar_init(&c.fin, 2);
         c.abort = 0u;
     }
     if (per * p.heads < kTileRows) {  // query rows behind the last of a tile are zeros for good (a copy writes whole entries only)
@@ -490,7 +472,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
         tc::fence_smem_async();
     }
-    if (warp == kAMmaWarp) tc::tmem2_alloc(&c.tmem_base, 512);
+    if (warp == kAScoreWarp) tc::tmem2_alloc(&c.tmem_base, 512);
     tc::fence_before_sync();
     tc::cluster_sync();  // all CTAs' barriers exist
     tc::fence_after_sync();
@@ -523,7 +505,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
                     const int st = g % kKRing;
                     if (g >= kKRing && !(ok = wait_phase(&c.k_free[st], ((g / kKRing) - 1) & 1, abort))) break;
                     if (r == 0) tc::mbar_arrive_expect_tx(&c.k_full[st], 2 * kKStage);
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < kBoxes; ++x)
                         tc::tma2_load3(tc::smem_u32(smem) + kAOffK + st * kKStage + x * kKBox, &key_map, 64 * x,
                                        kBlk * b + kHalfBlk * (int)half + 32 * (int)r, p.layer0 + w.l, kf + 8 * st);
@@ -558,85 +540,79 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
             if (!ok) give_up(&c.abort, err);
         }
         __syncwarp();
-    } else if (warp == kAMmaWarp) {
+    } else if (warp == kAScoreWarp) {
+        // The two streams of products have a warp each: the tensor pipe takes few products ahead, and what a warp spends on
+        // its waits and commits the other's products fill.
         if (r == 0) {
-            const uint32_t idesc_s = tc::idesc_bf16_f32(256, kHalfBlk, 0), idesc_o = tc::idesc_bf16_f32(256, kVHalf, 1);
+            const uint32_t idesc = tc::idesc_bf16_f32(256, kHalfBlk, 0);
             const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), base = tc::smem_u32(smem);
             const uint32_t mine = 3u << __shfl_sync(0xFFFFFFFFu, leader, 0);  // the CTAs of this pair
-            const uint32_t hp = __shfl_sync(0xFFFFFFFFu, half, 0);
-            const uint64_t dq = tc::sw128_kmajor_desc(base), dp = tc::sw128_kmajor_desc(base + kAOffP),
-                           dk = tc::sw128_kmajor_desc(base + kAOffK), dv = tc::sw128_mnmajor_desc(base + kAOffV, kVBox);
+            const uint64_t dq = tc::sw128_kmajor_desc(base), dk = tc::sw128_kmajor_desc(base + kAOffK);
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, abort)); };
             bool ok = true;
-            int gv = 0, n = 0, g = 0;  // value stages, pieces, blocks
-            // O += P V of block j of the call (the piece's first: O = P V, once the piece before has read its O)
-            auto values = [&](int j, bool first) -> bool {
-                if (!wait(&c.p_full[j & 1], (j >> 1) & 1)) return false;
-                if (first && n > 0 && !wait(&c.o_free, (n - 1) & 1)) return false;
-                for (int h = 0; h < 2; ++h, ++gv) {
-                    const int st = gv % kVRing;
-                    if (!wait(&c.v_full[st], (gv / kVRing) & 1)) return false;
-                    tc::fence_after_sync();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc::mma2_bf16_warp(tb + kColO, dp + (((j & 1) * kPTile + h * kPBox + 32 * k) >> 4),
-                                           dv + ((st * kVStage + 2048 * k) >> 4), idesc_o, !first || h > 0 || k > 0 ? 1u : 0u);
-                    tc::mma2_commit_warp(&c.v_free[st], mine);
-                }
-                tc::mma2_commit_warp(&c.pv_done[hp][j & 1], 15);
-                return true;
-            };
+            int n = 0, g = 0;  // pieces, blocks
             for (int i = cl; ok && i < pieces; i += ncl, ++n) {
                 const Piece w = piece_of(i);
-                const int blocks = w.b1 - w.b0, g0 = g;
-                if (!(ok = wait(&c.q_tm, n & 1))) break;
-                for (int b = 0; ok && b < blocks; ++b, ++g) {
-                    if (g > 0 && !(ok = wait(&c.s_free, (g - 1) & 1))) break;
+                if (!(ok = wait(&c.q_tm, n & 1) && wait(&c.q_full, n & 1))) break;
+                for (int b = w.b0; b < w.b1; ++b, ++g) {
                     const int st = g % kKRing;
-                    if (b == 0 && !(ok = wait(&c.q_full, n & 1))) break;
                     if (!(ok = wait(&c.k_full[st], (g / kKRing) & 1))) break;
+                    if (g > 0 && !(ok = wait(&c.s_free, (g - 1) & 1))) break;
                     tc::fence_after_sync();
-                    // unrolled, so that each descriptor is the stage's plus a constant (32 cycles a product are left to issue it)
                     const uint64_t ds = dk + ((st * kKStage) >> 4);
-#pragma unroll
-                    for (int x = 0; x < kBoxes; ++x)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (x < kQtBoxes)
-                                tc::mma2_bf16_ta_warp(tb + kColS, tb + kColQ + 32 * x + 8 * k, ds + ((x * kKBox + 32 * k) >> 4), idesc_s,
-                                                      x > 0 || k > 0 ? 1u : 0u);
-                            else
-                                tc::mma2_bf16_warp(tb + kColS, dq + (((x - kQtBoxes) * kTileBox + 32 * k) >> 4),
-                                                   ds + ((x * kKBox + 32 * k) >> 4), idesc_s, 1u);
-                        }
-                    tc::mma2_commit_warp(&c.k_free[st], mine);
-                    if (b + 1 == blocks) tc::mma2_commit_warp(&c.q_free, mine);
+#pragma unroll 1
+                    for (int x = 0; x < kQtBoxes; ++x)
+                        tc::mma2_bf16_ta_x4_warp<8, 2>(tb + kColS, tb + kColQ + 32 * x, ds + ((x * kKBox) >> 4), idesc, x > 0 ? 1u : 0u);
+#pragma unroll 1
+                    for (int x = kQtBoxes; x < kBoxes; ++x)
+                        tc::mma2_bf16_x4_warp<2, 2>(tb + kColS, dq + (((x - kQtBoxes) * kTileBox) >> 4), ds + ((x * kKBox) >> 4), idesc, 1u);
                     tc::mma2_commit_warp(&c.s_full, mine);
-                    if (b >= kLag) ok = values(g - kLag, b == kLag);
+                    tc::mma2_commit_warp(&c.k_free[st], mine);
+                    if (b + 1 == w.b1) tc::mma2_commit_warp(&c.q_free, mine);
                 }
-                for (int j = max(g0, g - kLag); ok && j < g; ++j) ok = values(j, j == g0);
             }
             if (!ok && lane == 0) give_up(&c.abort, err);
             tc::mma2_commit_warp(&c.fin, mine);
         }
-    } else if (warp == kAPassWarp) {
-        // tells the pair's first CTA that the other pair's half of P has arrived here
-        if (lane == 0) {
-            const uint32_t pf = at_leader(&c.p_full[0]);
-            bool ok = true;
-            int g = 0;
-            for (int i = cl; ok && i < pieces; i += ncl) {
-                const Piece w = piece_of(i);
-                for (int b = w.b0; b < w.b1; ++b, ++g) {
-                    tc::mbar_arrive_expect_tx(&c.x_full[g & 1], kPBox);
-                    if (!(ok = wait_phase(&c.x_full[g & 1], (g >> 1) & 1, abort))) break;
-                    tc::fence_smem_async();
-                    tc::mbar_arrive_at(pf + 8 * (g & 1));
+    } else if (warp == kAValueMmaWarp) {
+        const uint32_t pf = at_leader(&c.p_full[0]);
+        const uint32_t idesc = tc::idesc_bf16_f32(256, kVHalf, 1);
+        const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), base = tc::smem_u32(smem);
+        const uint32_t mine = 3u << __shfl_sync(0xFFFFFFFFu, leader, 0);
+        const uint64_t dp = tc::sw128_kmajor_desc(base + kAOffP), dv = tc::sw128_mnmajor_desc(base + kAOffV, kVBox);
+        auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, abort)); };
+        bool ok = true;
+        int gv = 0, n = 0, g = 0;  // value stages, pieces, blocks
+        for (int i = cl; ok && i < pieces; i += ncl, ++n) {
+            const Piece w = piece_of(i);
+            for (int b = w.b0; b < w.b1; ++b, ++g) {
+                // the other pair's half of P
+                if (lane == 0) tc::mbar_arrive_expect_tx(&c.x_full[g & 1], kPBox);
+                __syncwarp();
+                if (!(ok = wait(&c.x_full[g & 1], (g >> 1) & 1))) break;
+                tc::fence_smem_async();
+                if (r == 1) {  // this CTA's part of it is there
+                    if (lane == 0) tc::mbar_arrive_at(pf + 8 * (g & 1));
+                    __syncwarp();
+                    continue;
                 }
+                if (!(ok = wait(&c.p_full[g & 1], (g >> 1) & 1))) break;
+                if (b == w.b0 && n > 0 && !(ok = wait(&c.o_free, (n - 1) & 1))) break;  // the item before has read its O
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h, ++gv) {
+                    const int st = gv % kVRing;
+                    if (!(ok = wait(&c.v_full[st], (gv / kVRing) & 1))) break;
+                    tc::fence_after_sync();
+                    tc::mma2_bf16_x4_warp<2, 128>(tb + kColO, dp + (((g & 1) * kPTile + h * kPBox) >> 4), dv + ((st * kVStage) >> 4),
+                                                  idesc, b > w.b0 || h > 0 ? 1u : 0u);
+                    tc::mma2_commit_warp(&c.v_free[st], mine);
+                }
+                if (!ok) break;
+                tc::mma2_commit_warp(&c.pv_done[g & 1], 15);
             }
-            if (!ok) give_up(&c.abort, err);
         }
-        __syncwarp();
+        if (!ok && lane == 0) give_up(&c.abort, err);
+        if (r == 0) tc::mma2_commit_warp(&c.fin, mine);
     } else if (warp >= kQWarp0) {
         // the first 384 dims of the item's queries into tensor memory, a row a thread
         const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16) + kColQ, qt = at_leader(&c.q_tm);
@@ -702,37 +678,41 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
                 const float mloc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if (tid == 0) tc::mbar_arrive_expect_tx(&c.m_full[bb], kTileRows * 4);
                 tc::st_async4(mx_peer + bb * kTileRows * 4, mloc, mf_peer + 8 * bb);
+                // P tile bb is free, here and there, once both pairs have multiplied block g - 2 by it
+                if (g >= 2 && !(ok = wait(&c.pv_done[bb], ((g >> 1) - 1) & 1))) break;
                 uint32_t pk[kHalfBlk / 2];
-                float ls[2], rs[2];
-                auto exponentials = [&]() {
+                uint64_t ls, rs;
+                float factor = 1.0f;
+                for (bool settled = false;; settled = true) {
                     const float neg_m = m_ref == -INFINITY ? 0.0f : -m_ref;  // (only keys that are masked, or NaN)
-                    ls[0] = ls[1] = rs[0] = rs[1] = 0.0f;
+                    const uint64_t scale2 = pair(scale_log2, scale_log2), neg2 = pair(neg_m, neg_m);
+                    uint64_t sums[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
                     for (int j = 0; j < kHalfBlk / 2; ++j) {
-                        const float p0 = ex2(fmaf(v[2 * j], scale_log2, neg_m)), p1 = ex2(fmaf(v[2 * j + 1], scale_log2, neg_m));
+                        float p0, p1;
+                        split(fma2(pair(v[2 * j], v[2 * j + 1]), scale2, neg2), p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
                         pk[j] = bf2(p0, p1);
-                        ls[0] += p0;
-                        ls[1] += p1;
-                        rs[0] += __uint_as_float(pk[j] << 16);
-                        rs[1] += __uint_as_float(pk[j] & 0xFFFF0000u);
+                        sums[j & 1] = add2(sums[j & 1], pair(p0, p1));
+                        sums[2 + (j & 1)] = add2(sums[2 + (j & 1)], pair(__uint_as_float(pk[j] << 16), __uint_as_float(pk[j] & 0xFFFF0000u)));
                     }
-                };
-                if (b > w.b0) exponentials();
-                if (!(ok = wait(&c.m_full[bb], (g >> 1) & 1))) break;
-                const float mb = fmaxf(mloc, c.mx[bb][tid]) * scale_log2;
-                float factor = 1.0f;
-                if (mb > m_ref + kRescaleLog2) {
-                    factor = ex2(m_ref - mb);  // (0 from -inf)
-                    m_ref = mb;
-                    l_run *= factor;
-                    r_run *= factor;
+                    ls = add2(sums[0], sums[1]);
+                    rs = add2(sums[2], sums[3]);
+                    if (settled) break;
+                    if (!(ok = wait(&c.m_full[bb], (g >> 1) & 1))) break;
+                    const float mb = fmaxf(mloc, c.mx[bb][tid]) * scale_log2;
+                    if (mb > m_ref + kRescaleLog2) {
+                        factor = ex2(m_ref - mb);  // (0 from -inf)
+                        m_ref = mb;
+                        l_run *= factor;
+                        r_run *= factor;
+                    }
+                    if (!__any_sync(0xFFFFFFFFu, factor != 1.0f)) break;
                 }
-                if (b == w.b0) {
-                    exponentials();
-                } else if (__any_sync(0xFFFFFFFFu, factor != 1.0f)) {
-                    exponentials();
-                    // rescale this warp's rows of O
-                    if (!(ok = wait(&c.pv_done[half][bb ^ 1], ((g - 1) >> 1) & 1))) break;
+                if (!ok) break;
+                if (b > w.b0 && __any_sync(0xFFFFFFFFu, factor != 1.0f)) {  // rescale this warp's rows of O
+                    if (!(ok = wait(&c.pv_done[bb ^ 1], ((g - 1) >> 1) & 1))) break;
                     tc::fence_after_sync();
 #pragma unroll 1
                     for (int c0 = 0; c0 < kVHalf; c0 += 32) {
@@ -744,10 +724,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
                     }
                     tc::fence_before_sync();
                 }
-                l_run += ls[0] + ls[1];
-                r_run += rs[0] + rs[1];
-                // P tile bb is free, here and there, once both pairs have multiplied block g - 2 by it
-                if (g >= 2 && !(ok = wait(&c.pv_done[0][bb], ((g >> 1) - 1) & 1) && wait(&c.pv_done[1][bb], ((g >> 1) - 1) & 1))) break;
+                float s0, s1;
+                split(ls, s0, s1);
+                l_run += s0 + s1;
+                split(rs, s0, s1);
+                r_run += s0 + s1;
                 uint8_t* row = smem + p_at + bb * kPTile + lane * 128;
 #pragma unroll
                 for (int j = 0; j < kHalfBlk / 8; ++j)  // 16-byte pieces where the swizzle puts them
@@ -764,7 +745,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
             if (tid == 0) tc::mbar_arrive_expect_tx(&c.l_full, kTileRows * 8);
             tc::st_async4(lx_peer, l_run, lf_peer);
             tc::st_async4(rx_peer, r_run, lf_peer);
-            if (!(ok = wait(&c.pv_done[half][(g - 1) & 1], ((g - 1) >> 1) & 1) && wait(&c.l_full, n & 1))) break;
+            if (!(ok = wait(&c.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1) && wait(&c.l_full, n & 1))) break;
             tc::fence_after_sync();
             const float l_all = half == 0 ? l_run + c.lx[tid] : c.lx[tid] + l_run;
             const float r_all = half == 0 ? r_run + c.rx[tid] : c.rx[tid] + r_run;
@@ -804,7 +785,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
         }
         if (!ok) give_up(&c.abort, err);
     }
-    pair_exit(&c.fin, &c.abort, err, tbase, warp == kAMmaWarp, 512);
+    pair_exit(&c.fin, &c.abort, err, tbase, warp == kAScoreWarp, 512);
 }
 
 // The splits of an item joined: with lse_i their log2 sums and M the largest, out = sum 2^(lse_i - M) o_i / sum 2^(lse_i - M).

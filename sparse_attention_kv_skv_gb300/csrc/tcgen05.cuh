@@ -341,22 +341,33 @@ __device__ __forceinline__ void st_async16u(uint32_t remote_addr, uint4 v, uint3
 // so do the first and the second half of B's N; both ranks at the offsets that the descriptors and addresses
 // give.  Rank 0 issues; each SM multiplies its own rows of A with all of B, which is held once for the two.
 // Called by a whole converged warp of rank 0, as mma_bf16_warp.
-__device__ __forceinline__ void mma2_bf16_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate)
-{
-    asm volatile(
-        "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void mma2_bf16_ta_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// Four of them, K steps of 16 whose operands lie kA and kB 16-byte units (A in tensor memory: columns) apart; the first
+// one adds to D if `accumulate`.  One statement, so that there is one election and the steps are constants: each product by
+// itself is some 30 instructions, and a loop of many of them does not stay in the instruction caches.
+template <int kA, int kB>
+__device__ __forceinline__ void mma2_bf16_x4_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                   uint32_t accumulate)
 {
     asm volatile(
-        "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p, q, t;\n .reg .b64 a, b;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        " add.s64 a, %1, %5;\n add.s64 b, %2, %6;\n @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
+        " add.s64 a, a, %5;\n add.s64 b, b, %6;\n @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
+        " add.s64 a, a, %5;\n add.s64 b, b, %6;\n @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kB)
+        : "memory");
+}
+template <int kA, int kB>
+__device__ __forceinline__ void mma2_bf16_ta_x4_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                     uint32_t accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, q, t;\n .reg .b32 a;\n .reg .b64 b;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " setp.eq.b32 t, 0, 0;\n @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n"
+        " add.s32 a, %1, %5;\n add.s64 b, %2, %6;\n @q tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, t;\n"
+        " add.s32 a, a, %5;\n add.s64 b, b, %6;\n @q tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, t;\n"
+        " add.s32 a, a, %5;\n add.s64 b, b, %6;\n @q tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, t;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kB)
         : "memory");
 }
 // Arrive on `bar` of the cluster's CTAs in `ctas` (a bit a rank) once every such product issued so far has completed.
