@@ -67,11 +67,6 @@ int64_t select_stride(int64_t max_context, int block);
 cudaError_t prepare_select();  // once per context, on its device
 cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_ids, int B, const void* q, const float* w,
                           int32_t* topk, void* workspace, int device_sms, cudaStream_t st, bool withhold_keys = false);
-// The `keep` heaviest of each row of weights [units][n] (rows weights_stride floats apart), its first `first` and last
-// `last` always taken, ascending in kept [units][keep], -1 behind them.  workspace: units * select_stride(n, 1) words
-// and a length a unit.
-cudaError_t launch_heaviest(const Dev& d, const float* weights, int64_t weights_stride, int units, int n, int keep,
-                            int first, int last, int32_t* kept, void* workspace, int device_sms, cudaStream_t st);
 // Kernels around a shared prefix (skv_prefix.cu): once per context, on its device.
 cudaError_t prepare_prefix(int* clusters);  // *clusters: those of skv_attend_prefix that are on the chip at once
 // Loads skv_assemble_noalloc's static work list on `device` (current) and

@@ -936,15 +936,379 @@ __global__ void __launch_bounds__(256) join_kernel(JoinParts parts, int64_t rows
 }
 
 // ---------------------------------------------------------------------------
+// Eviction.  Weights are compared as unsigned words of the same order; tokens
+// that always stay have the largest word, which no weight has.  The threshold tv is
+// the word of the last token that stays: what is above it stays, and of those equal to it the
+// first `ties`.  With the threshold known a scan gives every token that stays its place, so
+// nothing is sorted, and ties go to the lower token.
+struct Heaviest {
+    const float* weights;
+    int64_t stride;           // floats between layers
+    int n, keep, first, last;
+    const uint32_t* err;      // the error word
+    // of token j, whose weight is x
+    __device__ __forceinline__ uint32_t word(float x, int j) const
+    {
+        const uint32_t u = __float_as_uint(x + 0.0f);  // -0 as +0
+        const uint32_t v = x != x ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;  // a NaN below everything
+        return j < first || j >= n - last ? 0xFFFFFFFFu : v;
+    }
+    // kEach weights, `step` tokens apart: all reads in flight together
+    template <int kEach>
+    __device__ __forceinline__ void read(const float* w, int j0, int step, float (&x)[kEach]) const
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) x[i] = j0 + i * step < n ? w[j0 + i * step] : 0.0f;
+    }
+};
+constexpr uint32_t kNoWord = 0xFFFFFFFEu;  // above every weight, below the tokens that always stay
+
+// Inclusive sum over a CTA of kWarps warps, in thread order; *all receives the total.  (a __syncthreads inside)
+template <int kWarps>
+__device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* warp_sum, uint32_t* all)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += x;
+    }
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    const uint32_t w = lane < kWarps ? warp_sum[lane] : 0u;
+    *all = __reduce_add_sync(0xFFFFFFFFu, w);
+    return v + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u);
+}
+
+// Everything stays (or, with the error word set, nothing is said to).
+__global__ void __launch_bounds__(256) keep_all_kernel(Heaviest h, int32_t* kept)
+{
+    chain_next();
+    chain_wait();
+    const bool none = *behind_wait(h.err) != 0u;
+    kept += (int64_t)blockIdx.y * h.keep;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < h.keep; i += (int64_t)gridDim.x * 256) kept[i] = !none && i < h.n ? (int32_t)i : -1;
+}
+
+// Short rows: a CTA a layer, its words in shared memory.  The range of the words is narrowed by histograms of 2048
+// equal parts until the part that holds the threshold has few enough to be ranked directly; the first range is that of the
+// words themselves, so mostly the first histogram is the only one.  Bound by latency: some ten barriers.
+constexpr int kShort = 32768, kShortThreads = 1024, kBins = 2048, kFew = 256;
+__global__ void __launch_bounds__(kShortThreads) heaviest_short_kernel(Heaviest h, int32_t* kept)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint32_t* words = reinterpret_cast<uint32_t*>(smem);
+    __shared__ uint32_t hist[kBins], few[kFew], above[kShort / 32], equal[kShort / 32], warp_sum[32];
+    __shared__ uint32_t s_lo, s_hi, s_bin, s_before, s_count, s_few, s_tv, s_ties;
+    const int tid = threadIdx.x, lane = tid & 31, n = h.n;
+    if (tid == 0) {
+        s_lo = 0xFFFFFFFFu;
+        s_hi = 0u;
+    }
+    chain_next();
+    chain_wait();
+    const float* w = behind_wait(h.weights) + blockIdx.x * h.stride;
+    kept += (int64_t)blockIdx.x * h.keep;
+    const bool stop = __syncthreads_or(tid == 0 && *behind_wait(h.err) != 0u);
+    if (stop) {
+        for (int i = tid; i < h.keep; i += kShortThreads) kept[i] = -1;
+        return;
+    }
+    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+    for (int j0 = tid; j0 < n; j0 += 8 * kShortThreads) {
+        float x[8];
+        h.read(w, j0, kShortThreads, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = j0 + i * kShortThreads;
+            const uint32_t v = h.word(x[i], j);
+            if (j < n) words[j] = v;
+            if (j < n && v != 0xFFFFFFFFu) {
+                lo = min(lo, v);
+                hi = max(hi, v);
+            }
+        }
+    }
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    if (lane == 0) {
+        atomicMin(&s_lo, lo);
+        atomicMax(&s_hi, hi);
+    }
+    __syncthreads();
+    lo = s_lo;
+    hi = s_hi;
+    uint32_t need = (uint32_t)(h.keep - h.first - h.last);  // to take from [lo, hi]; every word above hi stays
+    uint32_t tv = kNoWord, ties = 0u;
+    while (need > 0u) {
+        if (lo == hi) {
+            tv = lo;
+            ties = need;
+            break;
+        }
+        const uint32_t span = hi - lo;
+        const int bits = 32 - __clz(span), shift = bits > 11 ? bits - 11 : 0;
+        hist[tid] = hist[tid + kShortThreads] = 0u;
+        if (tid == 0) s_few = 0u;
+        __syncthreads();
+#pragma unroll 4
+        for (int j = tid; j < n; j += kShortThreads) {
+            const uint32_t x = words[j] - lo;
+            if (x <= span) atomicAdd(&hist[x >> shift], 1u);
+        }
+        __syncthreads();
+        const int top = kBins - 1 - 2 * tid;
+        const uint32_t h1 = hist[top], h0 = hist[top - 1];
+        uint32_t all;
+        const uint32_t before = cta_scan<32>(h1 + h0, warp_sum, &all) - h1 - h0;
+        if (before < need && need <= before + h1 + h0) {
+            const bool first = need <= before + h1;
+            s_bin = first ? top : top - 1;
+            s_before = first ? before : before + h1;
+            s_count = first ? h1 : h0;
+        }
+        __syncthreads();
+        lo += s_bin << shift;
+        hi = min(hi - lo, (1u << shift) - 1u) + lo;
+        need -= s_before;
+        const uint32_t in = s_count;
+        if (in == need) {  // all of it
+            tv = lo;
+            ties = 0xFFFFFFFFu;
+            break;
+        }
+        if (in <= kFew) {
+            const uint32_t range = hi - lo;
+#pragma unroll 4
+            for (int j = tid; j < n; j += kShortThreads)
+                if (words[j] - lo <= range) few[atomicAdd(&s_few, 1u)] = words[j];
+            __syncthreads();
+            if (tid < in) {
+                const uint32_t mine = few[tid];
+                uint32_t more = 0, same = 0;
+                for (uint32_t i = 0; i < in; ++i) {
+                    more += few[i] > mine;
+                    same += few[i] == mine;
+                }
+                if (more < need && need <= more + same) {  // (equal words write the same)
+                    s_tv = mine;
+                    s_ties = need - more;
+                }
+            }
+            __syncthreads();
+            tv = s_tv;
+            ties = s_ties;
+            break;
+        }
+    }
+    // a bit a token, a word of bits a thread
+    for (int j0 = tid - lane; j0 < n; j0 += kShortThreads) {
+        const uint32_t v = j0 + lane < n ? words[j0 + lane] : 0u;
+        const uint32_t a = __ballot_sync(0xFFFFFFFFu, j0 + lane < n && v > tv), e = __ballot_sync(0xFFFFFFFFu, j0 + lane < n && v == tv);
+        if (lane == 0) {
+            above[j0 / 32] = a;
+            equal[j0 / 32] = e;
+        }
+    }
+    __syncthreads();
+    const uint32_t a = 32 * tid < n ? above[tid] : 0u, e = 32 * tid < n ? equal[tid] : 0u;
+    uint32_t all;
+    const uint32_t upto = cta_scan<32>(__popc(a) | (uint32_t)__popc(e) << 16, warp_sum, &all);  // (at most 2^15 each)
+    // what a word keeps: all above, and of the equal ones the first that are left; the word's first place beside it
+    const uint32_t ab = (upto & 0xFFFFu) - __popc(a), eb = (upto >> 16) - __popc(e);
+    uint32_t stay = a | e;
+    if (eb + __popc(e) > ties) {
+        uint32_t some = 0u, left = e;
+        for (uint32_t i = eb; i < ties; ++i) {
+            some |= left & (0u - left);
+            left &= left - 1u;
+        }
+        stay = a | some;
+    }
+    above[tid] = stay;
+    equal[tid] = ab + min(eb, ties);
+    __syncthreads();
+    for (int i = tid >> 5; 32 * i < n; i += kShortThreads / 32) {  // a word a warp, so that the writes are together
+        const uint32_t m = above[i];
+        if (m >> lane & 1u) kept[equal[i] + __popc(m & ((1u << lane) - 1u))] = 32 * i + lane;
+    }
+}
+
+// Long rows: chunks of 8192 tokens, a CTA each, over the whole GPU.  Three passes find the threshold's digits (11, 11 and
+// 10 bits, from the top) by histograms of the words that share the digits found so far; the last CTA of a layer to finish a pass
+// picks the digit.  A fourth pass counts, a fifth writes.  Each pass reads the weights once, from L2 after the first.
+constexpr int kChunk = 8192, kLongThreads = 512;
+struct LongState {  // of a layer; zeros before the first pass
+    uint32_t hist[3][kBins];
+    uint32_t done[3];
+    uint32_t digits;  // found so far; at last tv
+    uint32_t need;    // to take from the words that share them; at last ties
+    uint32_t err;     // the error word as the first pass saw it
+    uint32_t pad[2];
+};
+static_assert(sizeof(LongState) % 16 == 0, "a layer's state");
+
+template <int kPass>
+__global__ void __launch_bounds__(kLongThreads) digit_kernel(Heaviest h, LongState* states)
+{
+    constexpr int kDigitBits = kPass < 2 ? 11 : 10, kShift = kPass == 0 ? 21 : kPass == 1 ? 10 : 0, kDigits = 1 << kDigitBits;
+    __shared__ uint32_t hist[kBins], warp_sum[32], s_last, s_digit, s_before;
+    const int tid = threadIdx.x;
+    for (int i = tid; i < kBins; i += kLongThreads) hist[i] = 0u;
+    chain_next();
+    chain_wait();
+    LongState& st = behind_wait(states)[blockIdx.y];
+    const float* w = behind_wait(h.weights) + blockIdx.y * h.stride;
+    const uint32_t digits = kPass ? __ldcg(&st.digits) : 0u;
+    __syncthreads();
+    float x[kChunk / kLongThreads];
+    const int j0 = blockIdx.x * kChunk + tid;
+    h.read(w, j0, kLongThreads, x);
+#pragma unroll
+    for (int i = 0; i < kChunk / kLongThreads; ++i) {
+        const int j = j0 + i * kLongThreads;
+        if (j < h.n) {
+            const uint32_t v = h.word(x[i], j);
+            if (v != 0xFFFFFFFFu && (kPass == 0 || v >> ((kShift + kDigitBits) & 31) == digits)) atomicAdd(&hist[(v >> kShift) & (kDigits - 1)], 1u);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < kDigits; i += kLongThreads)
+        if (hist[i]) atomicAdd(&st.hist[kPass][i], hist[i]);
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(&st.done[kPass], 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    // the last CTA of the layer: kDigits / kLongThreads digits a thread, from the top
+    constexpr int kEach = kDigits / kLongThreads;
+    const uint32_t need = kPass ? __ldcg(&st.need) : (uint32_t)(h.keep - h.first - h.last);
+    uint32_t c[kEach], sum = 0, all;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        c[i] = __ldcg(&st.hist[kPass][kDigits - 1 - kEach * tid - i]);
+        sum += c[i];
+    }
+    uint32_t before = cta_scan<kLongThreads / 32>(sum, warp_sum, &all) - sum;
+    if (tid == 0) {  // none needed: the word above all weights
+        s_digit = (kNoWord >> kShift) & (kDigits - 1);
+        s_before = 0u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (before < need && need <= before + c[i]) {
+            s_digit = kDigits - 1 - kEach * tid - i;
+            s_before = before;
+        }
+        before += c[i];
+    }
+    __syncthreads();
+    if (tid == 0) {
+        st.digits = digits << kDigitBits | s_digit;
+        st.need = need - s_before;
+        if (kPass == 0) st.err = *behind_wait(h.err);
+    }
+}
+
+__device__ __forceinline__ void chunk_bits(const Heaviest& h, const float* w, uint32_t tv, uint32_t (&a)[16], uint32_t (&e)[16], uint32_t& na, uint32_t& ne)
+{
+    // a warp has 512 consecutive tokens of the chunk
+    const int lane = threadIdx.x & 31, j0 = blockIdx.x * kChunk + (threadIdx.x >> 5) * (kChunk / (kLongThreads / 32)) + lane;
+    float x[16];
+    h.read(w, j0, 32, x);
+    na = ne = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t v = h.word(x[i], j0 + 32 * i);
+        a[i] = __ballot_sync(0xFFFFFFFFu, j0 + 32 * i < h.n && v > tv);
+        e[i] = __ballot_sync(0xFFFFFFFFu, j0 + 32 * i < h.n && v == tv);
+        na += __popc(a[i]);
+        ne += __popc(e[i]);
+    }
+}
+
+__global__ void __launch_bounds__(kLongThreads) count_kernel(Heaviest h, const LongState* states, uint2* counts)
+{
+    __shared__ uint32_t sa, se;
+    if (threadIdx.x == 0) sa = se = 0u;
+    chain_next();
+    chain_wait();
+    const LongState& st = behind_wait(states)[blockIdx.y];
+    uint32_t a[16], e[16], na, ne;
+    chunk_bits(h, behind_wait(h.weights) + blockIdx.y * h.stride, st.digits, a, e, na, ne);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+        atomicAdd(&sa, na);
+        atomicAdd(&se, ne);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) counts[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = make_uint2(sa, se);
+}
+
+__global__ void __launch_bounds__(kLongThreads) place_kernel(Heaviest h, const LongState* states, const uint2* counts, int32_t* kept)
+{
+    __shared__ uint32_t wa[kLongThreads / 32], we[kLongThreads / 32], sa, se;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) sa = se = 0u;
+    chain_next();
+    chain_wait();
+    const LongState& st = behind_wait(states)[blockIdx.y];
+    counts = behind_wait(counts) + (int64_t)blockIdx.y * gridDim.x;
+    kept += (int64_t)blockIdx.y * h.keep;
+    const uint32_t tv = st.digits, ties = st.need;
+    if (st.err) {
+        for (int64_t i = (int64_t)blockIdx.x * kLongThreads + tid; i < h.keep; i += (int64_t)gridDim.x * kLongThreads) kept[i] = -1;
+        return;
+    }
+    uint32_t a[16], e[16], na, ne, ca = 0, ce = 0;
+    chunk_bits(h, behind_wait(h.weights) + blockIdx.y * h.stride, tv, a, e, na, ne);
+    if (lane == 0) {
+        wa[warp] = na;
+        we[warp] = ne;
+    }
+    for (int i = tid; i < (int)blockIdx.x; i += kLongThreads) {  // the chunks before this one
+        const uint2 c = counts[i];
+        ca += c.x;
+        ce += c.y;
+    }
+    ca = __reduce_add_sync(0xFFFFFFFFu, ca);
+    ce = __reduce_add_sync(0xFFFFFFFFu, ce);
+    __syncthreads();
+    if (lane == 0 && (ca | ce)) {
+        atomicAdd(&sa, ca);
+        atomicAdd(&se, ce);
+    }
+    __syncthreads();
+    uint32_t ab = sa, eb = se;  // before this warp's tokens
+    for (int i = 0; i < warp; ++i) {
+        ab += wa[i];
+        eb += we[i];
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    const int j0 = blockIdx.x * kChunk + warp * (kChunk / (kLongThreads / 32)) + lane;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t er = eb + __popc(e[i] & below), ar = ab + __popc(a[i] & below);
+        if (a[i] >> lane & 1u || (e[i] >> lane & 1u && er < ties)) kept[ar + min(er, ties)] = j0 + 32 * i;
+        ab += __popc(a[i]);
+        eb += __popc(e[i]);
+    }
+}
+
 // The tokens that stay (kept, ascending, -1 behind the last): their rows and weights moved together.  A warp
-// moves four rows, nine 16-byte pieces a lane.
+// moves four rows, nine 16-byte pieces a lane.  Bound by HBM: 191 us at 2 x 262144 rows (1.21 GB, 6.3 TB/s).
 __global__ void __launch_bounds__(256) keep_kernel(PrefixShape p, const float* weights, int64_t weights_stride, int keep,
                                                    const int32_t* kept, uint4* rows_out, float* weights_out)
 {
     constexpr int kPieces = kRowBytes / 16, kRowsAWarp = 4, kEach = kPieces * kRowsAWarp / 32;
+    chain_next();
+    chain_wait();
     const int l = blockIdx.y, lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * 8 * kRowsAWarp;
-    kept += (int64_t)l * keep;
+    kept = behind_wait(kept) + (int64_t)l * keep;
+    weights = behind_wait(weights);
     for (int64_t i0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kRowsAWarp; i0 < keep; i0 += step) {
         const int32_t token = lane < kRowsAWarp && i0 + lane < keep ? kept[i0 + lane] : -1;
         if (rows_out) {
@@ -965,6 +1329,37 @@ __global__ void __launch_bounds__(256) keep_kernel(PrefixShape p, const float* w
     }
 }
 
+// Workspace of an eviction: the layers' states and the chunks' counts (long rows only).
+int64_t evict_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
+int64_t evict_bytes(int64_t n, int layers) { return n <= kShort ? 16 : layers * ((int64_t)sizeof(LongState) + evict_chunks(n) * (int64_t)sizeof(uint2)); }
+
+cudaError_t launch_evict(const PrefixShape& p, const float* weights, int64_t weights_stride, int keep, int first, int last,
+                         int32_t* kept, void* rows_out, float* weights_out, void* workspace, const uint32_t* err, cudaStream_t st)
+{
+    const Heaviest h{p.n ? weights + p.layer0 * weights_stride : nullptr, weights_stride, p.n, keep, first, last, err};
+    const unsigned layers = (unsigned)p.layers;
+    cudaError_t e = cudaSuccess;
+    if (p.n <= keep) {
+        e = launch_chained(keep_all_kernel, dim3((unsigned)std::min(1 << 16, (keep + 255) / 256), layers), 256, 0, st, h, kept);
+    } else if (p.n <= kShort) {
+        e = launch_chained(heaviest_short_kernel, dim3(layers), kShortThreads, (size_t)(p.n + 31) / 32 * 128, st, h, kept);
+    } else {
+        LongState* states = static_cast<LongState*>(workspace);
+        uint2* counts = reinterpret_cast<uint2*>(states + layers);
+        const dim3 grid((unsigned)evict_chunks(p.n), layers);
+        e = cudaMemsetAsync(states, 0, layers * sizeof(LongState), st);
+        if (e == cudaSuccess) e = launch_chained(digit_kernel<0>, grid, kLongThreads, 0, st, h, states);
+        if (e == cudaSuccess) e = launch_chained(digit_kernel<1>, grid, kLongThreads, 0, st, h, states);
+        if (e == cudaSuccess) e = launch_chained(digit_kernel<2>, grid, kLongThreads, 0, st, h, states);
+        if (e == cudaSuccess) e = launch_chained(count_kernel, grid, kLongThreads, 0, st, h, static_cast<const LongState*>(states), counts);
+        if (e == cudaSuccess)
+            e = launch_chained(place_kernel, grid, kLongThreads, 0, st, h, static_cast<const LongState*>(states), static_cast<const uint2*>(counts), kept);
+    }
+    if (e != cudaSuccess || (!rows_out && !weights_out) || p.n == 0) return e;
+    return launch_chained(keep_kernel, dim3((unsigned)std::min<int64_t>(((int64_t)keep + 31) / 32, 1 << 20), layers), 256, 0, st, p, weights,
+                          weights_stride, keep, static_cast<const int32_t*>(kept), static_cast<uint4*>(rows_out), weights_out);
+}
+
 int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 }  // namespace
@@ -973,6 +1368,7 @@ cudaError_t prepare_prefix(int* clusters)
 {
     cudaError_t e = cudaFuncSetAttribute(attend_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kASmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(weigh_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(heaviest_short_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShort * 4);
     if (e != cudaSuccess) return e;
     // clusters of four that are on the chip at once (its processors come in groups that are no multiple of four)
     cudaLaunchConfig_t cfg{};
@@ -1032,12 +1428,6 @@ PrefixShape shape_of(const skv_ctx* ctx, const skv_prefix& x, int32_t B, int32_t
 {
     return PrefixShape{static_cast<const uint8_t*>(x.rows), x.layer_stride, x.row_stride, (int)x.n, B, heads,
                        layer < 0 ? ctx->cfg.num_layers : 1, layer < 0 ? 0 : layer};
-}
-int64_t evict_bytes(const skv_ctx* ctx, const skv_prefix& x, int32_t layer)
-{
-    // a word a token, and the lengths
-    const int64_t layers = layer < 0 ? ctx->cfg.num_layers : 1;
-    return layers * skv::select_stride(x.n, 1) * 4 + layers * 4;
 }
 }  // namespace
 
@@ -1131,7 +1521,7 @@ skv_status skv_weigh_prefix(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, i
 skv_status skv_evict_prefix_workspace(skv_ctx* ctx, const skv_prefix* prefix, int32_t layer, int64_t* bytes)
 {
     if (!shape_ok(ctx, prefix, layer) || !bytes) return SKV_ERR_INVALID_ARG;
-    *bytes = evict_bytes(ctx, *prefix, layer);
+    *bytes = skv::evict_bytes(prefix->n, layer < 0 ? ctx->cfg.num_layers : 1);
     return SKV_OK;
 }
 
@@ -1144,19 +1534,14 @@ skv_status skv_evict_prefix(skv_ctx* ctx, const skv_prefix* prefix, int32_t laye
         (int64_t)first + last > keep)
         return SKV_ERR_INVALID_ARG;
     if (!rows_ok(ctx, *prefix) || !kept_dev || !workspace_dev || (prefix->n > 0 && !weights_dev) ||
-        workspace_bytes < evict_bytes(ctx, *prefix, layer) || !aligned(workspace_dev, 16) || !aligned(rows_out_dev, 16) ||
+        workspace_bytes < skv::evict_bytes(prefix->n, layer < 0 ? ctx->cfg.num_layers : 1) || !aligned(workspace_dev, 16) || !aligned(rows_out_dev, 16) ||
         !aligned(kept_dev, 4) || !aligned(weights_dev, 4) || !aligned(weights_out_dev, 4) ||
         (ctx->cfg.num_layers > 1 && weights_stride < prefix->n) || weights_stride >= (int64_t)1 << 40)
         return SKV_ERR_INVALID_ARG;
     const PrefixShape p = shape_of(ctx, *prefix, 1, 1, layer);
     return on_device(ctx, "skv_evict_prefix", [&] {
-        cudaError_t e = skv::launch_heaviest(ctx->d, weights_dev + p.layer0 * weights_stride, weights_stride, p.layers, p.n,
-                                             keep, first, last, kept_dev, workspace_dev, ctx->device_sms, stream);
-        if (e != cudaSuccess || (!rows_out_dev && !weights_out_dev) || p.n == 0) return e;
-        const int64_t groups = ((int64_t)keep + 31) / 32;
-        skv::keep_kernel<<<dim3((unsigned)std::min<int64_t>(groups, 1 << 20), (unsigned)p.layers), 256, 0, stream>>>(
-            p, weights_dev, weights_stride, keep, kept_dev, static_cast<uint4*>(rows_out_dev), weights_out_dev);
-        return cudaGetLastError();
+        return skv::launch_evict(p, weights_dev, weights_stride, keep, first, last, kept_dev, rows_out_dev, weights_out_dev, workspace_dev,
+                                 &ctx->d.ctl[skv::CTL_ERR], stream);
     });
 }
 

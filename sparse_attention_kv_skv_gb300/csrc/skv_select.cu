@@ -902,35 +902,6 @@ cudaError_t prepare_select()
     return e;
 }
 
-namespace {
-// pick_kernel over `units` units of at most max_keys scores.
-cudaError_t launch_pick(const Dev& d, int64_t units, int64_t max_keys, const int32_t* lens, const SelectShape& sh,
-                        const uint32_t* scores, int32_t* topk, int device_sms, cudaStream_t st)
-{
-    // A unit's scores go to one CTA while they fit its shared memory and units fill the SMs; else a
-    // cluster shares them (never fewer than 8192 scores a CTA: the cluster's barriers cost more than they save).
-    int team = 1;
-    while (team < 8 && max_keys / (2 * team) >= 8192 && (max_keys / team > kStagedKeys || units * team * 2 <= device_sms)) team *= 2;
-    const int64_t chunk = ((max_keys + team - 1) / team + 127) & ~(int64_t)127;
-    const int staged = (int)std::min<int64_t>(chunk, kStagedKeys);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(units * team));
-    cfg.blockDim = dim3(kPickThreads);
-    cfg.dynamicSmemBytes = chunk <= staged ? (size_t)staged * 4 + staged / 8 : kPickSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = team;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // takes the SMs that score_kernel leaves, and waits
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    auto pick = team == 1 ? pick_kernel<1> : team == 2 ? pick_kernel<2> : team == 4 ? pick_kernel<4> : pick_kernel<8>;
-    return cudaLaunchKernelEx(&cfg, pick, d, lens, sh, scores, staged, topk);
-}
-}  // namespace
-
 cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_ids, int B, const void* q, const float* w,
                           int32_t* topk, void* workspace, int device_sms, cudaStream_t st, bool withhold_keys)
 {
@@ -983,44 +954,27 @@ cudaError_t launch_select(const Dev& d, const skv_index& ix, const int32_t* req_
     e = launch_chained(score, dim3(grid), kScoreThreads, lay.bytes, st, key_map, q_map, d, req_ids, w, sh, lay, scores, lens);
     if (e != cudaSuccess) return e;
 
-    return launch_pick(d, units, max_keys, lens, sh, scores, topk, device_sms, st);
-}
-
-// Weights as the words that pick_kernel takes, four tokens a thread.
-__global__ void __launch_bounds__(256) word_kernel(const float* weights, int64_t weights_stride, int n, int first, int last,
-                                                   int64_t stride, uint32_t* __restrict__ words, int32_t* __restrict__ lens)
-{
-    chain_next();
-    chain_wait();
-    weights = behind_wait(weights) + blockIdx.y * weights_stride;
-    words += blockIdx.y * stride;
-    if (blockIdx.x == 0 && threadIdx.x == 0) lens[blockIdx.y] = n;
-    const int j0 = (blockIdx.x * 256 + threadIdx.x) * 4;
-    uint32_t w[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        const int j = j0 + x;
-        w[x] = j >= n ? 0u : j < first || j >= n - last ? 0xFFFFFFFFu : order_word(weights[j]);
-    }
-    if (j0 < n) *reinterpret_cast<uint4*>(words + j0) = make_uint4(w[0], w[1], w[2], w[3]);  // a unit's room is a multiple of 128
-}
-
-cudaError_t launch_heaviest(const Dev& d, const float* weights, int64_t weights_stride, int units, int n, int keep,
-                            int first, int last, int32_t* kept, void* workspace, int device_sms, cudaStream_t st)
-{
-    SelectShape sh{};
-    sh.B = units;
-    sh.layers = 1;
-    sh.block = 1;
-    sh.stride = select_stride(n, 1);
-    uint32_t* words = static_cast<uint32_t*>(workspace);
-    int32_t* lens = reinterpret_cast<int32_t*>(words + units * sh.stride);
-    cudaError_t e = launch_chained(word_kernel, dim3((unsigned)std::max(1, (n + 1023) / 1024), (unsigned)units), 256, 0, st, weights,
-                                   weights_stride, n, first, last, sh.stride, words, lens);
-    if (e != cudaSuccess) return e;
-    Dev dk = d;
-    dk.k = keep;
-    return launch_pick(dk, units, std::max(1, n), lens, sh, words, kept, device_sms, st);
+    // A unit's scores go to one CTA while they fit its shared memory and units fill the SMs; else a
+    // cluster shares them (never fewer than 8192 scores a CTA: the cluster's barriers cost more than they save).
+    int team = 1;
+    while (team < 8 && max_keys / (2 * team) >= 8192 && (max_keys / team > kStagedKeys || units * team * 2 <= device_sms)) team *= 2;
+    const int64_t chunk = ((max_keys + team - 1) / team + 127) & ~(int64_t)127;
+    const int staged = (int)std::min<int64_t>(chunk, kStagedKeys);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(units * team));
+    cfg.blockDim = dim3(kPickThreads);
+    cfg.dynamicSmemBytes = chunk <= staged ? (size_t)staged * 4 + staged / 8 : kPickSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = team;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // takes the SMs that score_kernel leaves, and waits
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    auto pick = team == 1 ? pick_kernel<1> : team == 2 ? pick_kernel<2> : team == 4 ? pick_kernel<4> : pick_kernel<8>;
+    return cudaLaunchKernelEx(&cfg, pick, d, static_cast<const int32_t*>(lens), sh, static_cast<const uint32_t*>(scores), staged, topk);
 }
 
 }  // namespace skv
