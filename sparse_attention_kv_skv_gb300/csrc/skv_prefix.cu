@@ -390,6 +390,7 @@ constexpr int kKRing = 2, kVRing = 2;          // key stages (32 keys, 36 KB), v
 constexpr uint32_t kKBox = 32 * 128, kKStage = kBoxes * kKBox, kVBox = 64 * 128, kVStage = 2 * kVBox;
 constexpr uint32_t kPBox = kTileRows * 128, kPTile = 2 * kPBox;  // P: 128 rows x 64 keys of a pair, both pairs' (two tiles)
 constexpr int kVHalf = kVDim / 2;
+constexpr int kQAtOnce = 2;  // query columns a thread reads at once into tensor memory
 constexpr int kQtBoxes = 6, kQsBoxes = kBoxes - kQtBoxes;  // query columns in tensor memory, in shared memory
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;    // tensor memory: O 256 columns, S 64, Q 192
 constexpr int kQWarp0 = 4, kAKeyWarp = 8, kAValueWarp = 9, kAScoreWarp = 10, kAValueMmaWarp = 11, kAThreads = 384;
@@ -625,12 +626,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
             if (n > 0 && !(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.q_free, (n - 1) & 1, abort)))) break;
             tc::fence_after_sync();
 #pragma unroll 1
-            for (int x = 0; x < kQtBoxes; x += 2) {
-                uint4 v[16];
+            for (int x = 0; x < kQtBoxes; x += kQAtOnce) {
+                uint4 v[8 * kQAtOnce];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = row >= 0 ? rows[row * (kRowBytes / 16) + 8 * x + j] : make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < 8 * kQAtOnce; ++j) v[j] = row >= 0 ? rows[row * (kRowBytes / 16) + 8 * x + j] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
+                for (int j = 0; j < 8 * kQAtOnce; j += 2) {
                     const uint32_t a[8] = {v[j].x, v[j].y, v[j].z, v[j].w, v[j + 1].x, v[j + 1].y, v[j + 1].z, v[j + 1].w};
                     tc::tmem_st8_async(tl + 32 * x + 4 * j, a);
                 }
@@ -769,13 +770,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
             } else {
                 const int64_t slot = (int64_t)(plan.item(i) - plan.direct) * plan.splits + plan.split(i);
                 float4* o = reinterpret_cast<float4*>(plan.o) + (4 * slot + rank) * (kVHalf / 4) * kTileRows + tid;
+                const bool mine = tile_row(p, w.l, 2 * w.pair + (int)r, tid) >= 0;  // (nobody reads the others)
+                if (__any_sync(0xFFFFFFFFu, mine))
 #pragma unroll 1
                 for (int c0 = 0; c0 < kVHalf; c0 += 32) {
                     float ov[32];
                     tc::tmem_ld32(tl + kColO + c0, ov);
+                    if (mine) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        o[(c0 + j) / 4 * kTileRows] = make_float4(ov[j] * inv, ov[j + 1] * inv, ov[j + 2] * inv, ov[j + 3] * inv);
+                        for (int j = 0; j < 32; j += 4)
+                            o[(c0 + j) / 4 * kTileRows] = make_float4(ov[j] * inv, ov[j + 1] * inv, ov[j + 2] * inv, ov[j + 3] * inv);
+                    }
                 }
                 if (half == 0) plan.lse[(2 * slot + r) * kTileRows + tid] = lse2;
             }
@@ -789,7 +794,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
 }
 
 // The splits of an item joined: with lse_i their log2 sums and M the largest, out = sum 2^(lse_i - M) o_i / sum 2^(lse_i - M).
-// A thread a row and four columns.
+// A thread a row and four columns; kAtOnce splits' numbers are in flight together (19.2 us instead of 21.3 for a call of 10 splits).
+template <int kAtOnce>
 __global__ void __launch_bounds__(512) combine_prefix_kernel(PrefixShape p, AttendPlan plan, uint16_t* out, float* lse)
 {
     chain_next();
@@ -801,21 +807,34 @@ __global__ void __launch_bounds__(512) combine_prefix_kernel(PrefixShape p, Atte
     if (at < 0) return;
     const float* ls = behind_wait(plan.lse) + (2 * slot0 + r) * kTileRows + row;
     const float4* po = reinterpret_cast<const float4*>(behind_wait(plan.o)) + ((4 * slot0 + rank) * (kVHalf / 4) + col4) * kTileRows + row;
-    float m = -INFINITY;
-#pragma unroll 8
-    for (int i = 0; i < plan.splits; ++i) m = fmaxf(m, ls[(int64_t)i * 2 * kTileRows]);
-    const float base = m == -INFINITY ? 0.0f : m;  // (only NaN)
-    float acc[4] = {}, total = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < plan.splits; ++i) {
-        const float w = ex2(ls[(int64_t)i * 2 * kTileRows] - base);
-        const float4 o = po[(int64_t)i * kVHalf * kTileRows];
-        total += w;
-        acc[0] = fmaf(w, o.x, acc[0]);
-        acc[1] = fmaf(w, o.y, acc[1]);
-        acc[2] = fmaf(w, o.z, acc[2]);
-        acc[3] = fmaf(w, o.w, acc[3]);
+    float m = -INFINITY, acc[4] = {}, total = 0.0f;
+    for (int i0 = 0; i0 < plan.splits; i0 += kAtOnce) {
+        float li[kAtOnce], top = m;
+        float4 o[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const bool is = i0 + i < plan.splits;
+            li[i] = is ? ls[(int64_t)(i0 + i) * 2 * kTileRows] : -INFINITY;
+            o[i] = is ? po[(int64_t)(i0 + i) * kVHalf * kTileRows] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, li[i]);
+        const float base = top == -INFINITY ? 0.0f : top, fix = ex2(m - base);  // (only NaN, or scores of -inf)
+        total *= fix;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] *= fix;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const float w = ex2(li[i] - base);
+            total += w;
+            acc[0] = fmaf(w, o[i].x, acc[0]);
+            acc[1] = fmaf(w, o[i].y, acc[1]);
+            acc[2] = fmaf(w, o[i].z, acc[2]);
+            acc[3] = fmaf(w, o[i].w, acc[3]);
+        }
+        m = top;
     }
+    const float base = m == -INFINITY ? 0.0f : m;
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     *reinterpret_cast<uint2*>(out + at * kVDim + kVHalf * half + 4 * col4) =
         make_uint2(bf2(acc[0] * inv, acc[1] * inv), bf2(acc[2] * inv, acc[3] * inv));
@@ -878,8 +897,8 @@ cudaError_t launch_attend_prefix(const PrefixShape& p, int all_layers, const voi
                        q_map, p, plan, static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), lse, sm_scale * kLog2e, err,
                        withhold ? 1 : 0);
     if (e != cudaSuccess || plan.rest == 0) return e;
-    return launch_chained(combine_prefix_kernel, dim3(kVHalf / 16, 4u * (unsigned)plan.rest), 512, 0, st, p, plan,
-                          static_cast<uint16_t*>(out), lse);
+    return launch_chained(plan.splits <= 8 ? combine_prefix_kernel<8> : combine_prefix_kernel<12>, dim3(kVHalf / 16, 4u * (unsigned)plan.rest),
+                          512, 0, st, p, plan, static_cast<uint16_t*>(out), lse);
 }
 
 // ---------------------------------------------------------------------------

@@ -112,7 +112,7 @@ def _load():
         "skv_selftest_select_timeout": [vp, P(skv_index), vp, i32, vp, vp, vp, vp, i64, vp],
         "skv_attend_prefix_workspace": [vp, P(skv_prefix), i32, i32, i32, P(i64)],
         "skv_attend_prefix": [vp, P(skv_prefix), i32, i32, i32, vp, vp, vp, ctypes.c_float, vp, i64, vp],
-        "skv_join": [vp, i32, P(vp), P(vp), i64, vp, vp, vp],
+        "skv_join": [vp, i32, vp, vp, i64, vp, vp, vp],
         "skv_weigh_prefix_workspace": [vp, P(skv_prefix), i32, i32, i32, P(i64)],
         "skv_weigh_prefix": [vp, P(skv_prefix), i32, i32, i32, vp, vp, vp, i64, vp, i64, ctypes.c_float, ctypes.c_float, vp, i64, vp],
         "skv_evict_prefix_workspace": [vp, P(skv_prefix), i32, P(i64)],
@@ -311,17 +311,23 @@ class Prefix:
 
     def __setattr__(self, name, value):
         if name == "rows":
-            if value.dim() != 3 or value.shape[2] != 576 or value.stride(2) != 1 or not _is_type(value, "bf16"):
+            layers, n, dim = value.shape if value.dim() == 3 else (0, 0, 0)
+            if dim != 576 or value.stride(2) != 1 or not _is_type(value, "bf16"):
                 raise ValueError("Prefix: rows must be [layers][tokens][576] bf16 with adjacent values")
-            object.__setattr__(self, "_c", skv_prefix(value.data_ptr(), 2 * value.stride(0), 2 * value.stride(1), value.shape[1]))
+            # described once: a call of few tokens takes less time on the GPU than such look-ups take here
+            c = skv_prefix(value.data_ptr(), 2 * value.stride(0), 2 * value.stride(1), n)
+            object.__setattr__(self, "_made", (ctypes.byref(c), layers, n, value.get_device()))
         object.__setattr__(self, name, value)
 
     def c(self):
-        return ctypes.byref(self._c)
+        return self._made[0]
 
     @property
     def n(self) -> int:
-        return self.rows.shape[1]
+        return self._made[2]
+
+
+_pointers = [ctypes.c_void_p * (2 * i) for i in range(9)]  # a join's parts: their outs, then their lses
 
 
 class Context:
@@ -494,34 +500,36 @@ class Context:
             check(status, "skv_unpack_rows")
 
     # a prefix that the batch shares ------------------------------------------
-    def _prefix(self, prefix: Prefix, what: str) -> int:
-        """The context's device, which the prefix, with a row of every layer, is on."""
-        dev = self.cfg.device
-        if prefix.rows.shape[0] < self.cfg.num_layers:
+    def _prefix(self, prefix: Prefix, q, layer: int, B: int | None, what: str):
+        """What a call's description starts with: (the prefix, B, units, heads, tokens, the context's device)."""
+        c, layers, n, dev = prefix._made
+        if layers < self.cfg.num_layers:
             raise ValueError(f"{what}: the prefix has fewer layers than the context")
-        if prefix.rows.get_device() != dev:
-            _elsewhere(prefix.rows, dev, f"{what}: the prefix")
-        return dev
-
-    def _units(self, q, layer: int, B: int | None, what: str):
-        """(B, units, heads) of queries q [units][heads][576]."""
-        if q.dim() != 3 or q.shape[2] != 576:
-            raise ValueError(f"{what}: q must be [units][heads][576]")
+        if dev != self.cfg.device:
+            _elsewhere(prefix.rows, self.cfg.device, f"{what}: the prefix")
         layers = 1 if layer >= 0 else self.cfg.num_layers
+        if q is None:
+            return c, 0, layers, 0, n, self.cfg.device
+        shape = q.shape
+        if len(shape) != 3 or shape[2] != 576:
+            raise ValueError(f"{what}: q must be [units][heads][576]")
         if B is None:
-            B, rest = divmod(q.shape[0], layers)
+            B, rest = divmod(shape[0], layers)
             if rest:
                 raise ValueError(f"{what}: q must hold a unit of every layer for each entry of the batch")
-        return B, B * layers, q.shape[1]
+        return c, B, B * layers, shape[1], n, self.cfg.device
 
-    def _weights(self, t, prefix: Prefix, dev: int, what: str) -> int:
+    def _weights(self, t, n: int, dev: int, what: str) -> int:
         """The row stride of weights [L][n] fp32 with adjacent values."""
-        if t.dim() != 2 or t.shape[0] < self.cfg.num_layers or t.shape[1] < prefix.n or not _is_type(t, "fp32") or \
-                (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{what} must be [layers][tokens] fp32 with adjacent values")
+        shape = t.shape
+        if len(shape) != 2 or shape[0] < self.cfg.num_layers or shape[1] < n or not _is_type(t, "fp32"):
+            raise ValueError(f"{what} must be [layers][tokens] fp32")
+        step = t.stride()
+        if shape[1] > 1 and step[1] != 1:
+            raise ValueError(f"{what} must have adjacent values")
         if t.get_device() != dev:
             _elsewhere(t, dev, what)
-        return t.stride(0)
+        return step[0]
 
     def attend_prefix_workspace(self, prefix: Prefix, B: int, heads: int = 128, layer: int = -1) -> int:
         """Bytes of workspace an attend_prefix() of B entries needs."""
@@ -534,16 +542,15 @@ class Context:
         """MLA attention of a batch over a prefix that all of it shares (see skv_attend_prefix):
         q [units][heads][576] bf16 -> out [units][heads][512] bf16, lse [units][heads] (or None).
         workspace: attend_prefix_workspace() bytes."""
-        dev = self._prefix(prefix, "attend_prefix")
-        B, units, heads = self._units(q, layer, B, "attend_prefix")
-        scale = (1.0 / 576 ** 0.5) if sm_scale is None else sm_scale
-        _need(q, "bf16", units * heads * 1152, dev, "attend_prefix: q")
-        _need(out, "bf16", units * heads * 1024, dev, "attend_prefix: out")
+        c, B, units, heads, _, dev = self._prefix(prefix, q, layer, B, "attend_prefix")
+        rows = units * heads
+        _need(q, "bf16", rows * 1152, dev, "attend_prefix: q")
+        _need(out, "bf16", rows * 1024, dev, "attend_prefix: out")
         if lse is not None:
-            _need(lse, "fp32", units * heads * 4, dev, "attend_prefix: lse")
+            _need(lse, "fp32", rows * 4, dev, "attend_prefix: lse")
         _need(workspace, None, 0, dev, "attend_prefix: workspace")
-        status = skv_attend_prefix(self.h, prefix.c(), B, heads, layer, q.data_ptr(), _ptr(out), _ptr(lse), scale,
-                                   workspace.data_ptr(), workspace.nbytes,
+        status = skv_attend_prefix(self.h, c, B, heads, layer, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                   1.0 / 24.0 if sm_scale is None else sm_scale, workspace.data_ptr(), workspace.nbytes,
                                    _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
         if status:
             check(status, "skv_attend_prefix")
@@ -551,23 +558,24 @@ class Context:
     def join(self, outs, lses, out, lse=None, stream=None) -> None:
         """Join attention results over disjoint sets of tokens (see skv_join): outs, up to 8 of
         [...][512] bf16, and lses [...] fp32 -> out, lse, which may take a part's place."""
-        parts, dev = len(outs), self.cfg.device
+        parts, dev, size = len(outs), self.cfg.device, out.numel()
         if len(lses) != parts or not 1 <= parts <= 8:
             raise ValueError("join: 1 to 8 parts, each with its lse")
         if out.shape[-1] != 512:
             raise ValueError("join: out must be [...][512]")
-        rows = out.numel() // 512
+        rows = size // 512
         for o, e in zip(outs, lses):
-            if o.shape != out.shape or e.numel() != rows:
-                raise ValueError("join: the parts and the result differ in shape")
+            if o.numel() != size or e.numel() != rows:
+                raise ValueError("join: the parts and the result differ in size")
             _need(o, "bf16", rows * 1024, dev, "join: outs")
             _need(e, "fp32", rows * 4, dev, "join: lses")
         _need(out, "bf16", rows * 1024, dev, "join: out")
         if lse is not None:
             _need(lse, "fp32", rows * 4, dev, "join: lse")
-        pointers = ctypes.c_void_p * parts
-        status = skv_join(self.h, parts, pointers(*[o.data_ptr() for o in outs]), pointers(*[e.data_ptr() for e in lses]), rows,
-                          out.data_ptr(), _ptr(lse), _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
+        both = _pointers[parts](*[o.data_ptr() for o in outs], *[e.data_ptr() for e in lses])
+        status = skv_join(self.h, parts, both, ctypes.byref(both, 8 * parts), rows,
+                          out.data_ptr(), None if lse is None else lse.data_ptr(),
+                          _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
         if status:
             check(status, "skv_join")
 
@@ -582,16 +590,16 @@ class Context:
         """out = weights (or 0 for None) + gain times the attention weight that each of the prefix's
         tokens receives from the batch (see skv_weigh_prefix): q [units][heads][576] bf16, lse
         [units][heads], weights and out [L][n] fp32 (may be the same)."""
-        dev = self._prefix(prefix, "weigh_prefix")
-        B, units, heads = self._units(q, layer, B, "weigh_prefix")
-        scale = (1.0 / 576 ** 0.5) if sm_scale is None else sm_scale
-        _need(q, "bf16", units * heads * 1152, dev, "weigh_prefix: q")
-        _need(lse, "fp32", units * heads * 4, dev, "weigh_prefix: lse")
-        w_stride = 0 if weights is None else self._weights(weights, prefix, dev, "weigh_prefix: weights")
-        o_stride = self._weights(out, prefix, dev, "weigh_prefix: out")
+        c, B, units, heads, n, dev = self._prefix(prefix, q, layer, B, "weigh_prefix")
+        rows = units * heads
+        _need(q, "bf16", rows * 1152, dev, "weigh_prefix: q")
+        _need(lse, "fp32", rows * 4, dev, "weigh_prefix: lse")
+        w_stride = 0 if weights is None else self._weights(weights, n, dev, "weigh_prefix: weights")
+        o_stride = self._weights(out, n, dev, "weigh_prefix: out")
         _need(workspace, None, 0, dev, "weigh_prefix: workspace")
-        status = skv_weigh_prefix(self.h, prefix.c(), B, heads, layer, q.data_ptr(), _ptr(lse), _ptr(weights), w_stride,
-                                  out.data_ptr(), o_stride, scale, gain, workspace.data_ptr(), workspace.nbytes,
+        status = skv_weigh_prefix(self.h, c, B, heads, layer, q.data_ptr(), lse.data_ptr(), None if weights is None else weights.data_ptr(),
+                                  w_stride, out.data_ptr(), o_stride, 1.0 / 24.0 if sm_scale is None else sm_scale, gain,
+                                  workspace.data_ptr(), workspace.nbytes,
                                   _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
         if status:
             check(status, "skv_weigh_prefix")
@@ -607,17 +615,18 @@ class Context:
         """Keep a prefix's heaviest tokens (see skv_evict_prefix): weights [L][n] fp32 -> kept
         [layers of the call][keep] int32, ascending, their rows [..][keep][576] bf16 and weights [..][keep] (either may be
         None).  Prefix(rows) takes the old one's place."""
-        dev = self._prefix(prefix, "evict_prefix")
-        layers, keep = 1 if layer >= 0 else self.cfg.num_layers, kept.shape[-1]
-        stride = self._weights(weights, prefix, dev, "evict_prefix: weights")
+        c, _, layers, _, n, dev = self._prefix(prefix, None, layer, None, "evict_prefix")
+        keep = kept.shape[-1]
+        stride = self._weights(weights, n, dev, "evict_prefix: weights")
         _need(kept, "int32", 4 * layers * keep, dev, "evict_prefix: kept")
         if rows is not None:
             _need(rows, "bf16", 1152 * layers * keep, dev, "evict_prefix: rows")
         if kept_weights is not None:
             _need(kept_weights, "fp32", 4 * layers * keep, dev, "evict_prefix: kept_weights")
         _need(workspace, None, 0, dev, "evict_prefix: workspace")
-        status = skv_evict_prefix(self.h, prefix.c(), layer, weights.data_ptr(), stride, keep, first, last, kept.data_ptr(),
-                                  _ptr(rows), _ptr(kept_weights), workspace.data_ptr(), workspace.nbytes,
+        status = skv_evict_prefix(self.h, c, layer, weights.data_ptr(), stride, keep, first, last, kept.data_ptr(),
+                                  None if rows is None else rows.data_ptr(), None if kept_weights is None else kept_weights.data_ptr(),
+                                  workspace.data_ptr(), workspace.nbytes,
                                   _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
         if status:
             check(status, "skv_evict_prefix")
