@@ -467,7 +467,8 @@ typedef struct {
     int64_t n;             /* tokens, 0 <= n <= 2^30 */
 } skv_prefix;
 
-/* Bytes of workspace that an skv_attend_prefix of this shape needs.  Host code only. */
+/* Bytes of workspace that an skv_attend_prefix of this shape needs, under the SM budget that skv_set_attend_sms has
+ * set.  Host code only. */
 SKV_API skv_status skv_attend_prefix_workspace(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads,
                                                int32_t layer, int64_t *bytes);
 
@@ -486,7 +487,7 @@ SKV_API skv_status skv_attend_prefix_workspace(skv_ctx *ctx, const skv_prefix *p
  * The context gives the device, L and max_batch (B <= max_batch) and the error word
  * (SKV_DEVERR_TIMEOUT); its requests and its row_bytes do not matter.  The workspace is the caller's and
  * holds nothing between calls: two calls, or two captured graphs, that may run at the same time need
- * one each.  Few units are split along the prefix, so results may differ in rounding with B,
+ * one each.  Few units are split along the prefix, so results may differ in rounding with B and the SM budget,
  * never from call to call.  B == 0 enqueues nothing.  Captures into a CUDA graph. */
 SKV_API skv_status skv_attend_prefix(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads, int32_t layer,
                                      const void *q_dev, void *out_dev, float *lse_dev, float sm_scale,
@@ -514,7 +515,7 @@ SKV_API skv_status skv_weigh_prefix_workspace(skv_ctx *ctx, const skv_prefix *pr
  * weights_dev (null: zeros) and out_dev (may be the same) hold row l at l*weights_stride and l*out_stride
  * floats, in calls on one layer too; nothing behind out[l][n - 1] is written.  gain finite (a gain
  * that grows from step to step lets older weights fade).  The rest as in skv_attend_prefix.
- * Sums are fp32 in a fixed order: the same call gives the same result. */
+ * B == 0: out is weights.  Sums are fp32 in a fixed order: the same call gives the same result. */
 SKV_API skv_status skv_weigh_prefix(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads, int32_t layer,
                                     const void *q_dev, const float *lse_dev, const float *weights_dev,
                                     int64_t weights_stride, float *out_dev, int64_t out_stride, float sm_scale, float gain,
@@ -624,7 +625,8 @@ SKV_API skv_status skv_set_gather_events(skv_ctx *ctx, skv_event_t before, skv_e
  * the same time on other streams -- e.g. the next layer's skv_assemble_layer,
  * which is bound by the host link and needs few SMs to keep it busy.  0 (the
  * default) uses every SM.  Negative: SKV_ERR_INVALID_ARG.  Results do not
- * depend on it (those of skv_attend_q4, which it bounds as well, in their rounding only). */
+ * depend on it (those of skv_attend_q4 and skv_attend_prefix, which it bounds as well -- the latter in clusters of
+ * four, at least one --, in their rounding only). */
 SKV_API skv_status skv_set_attend_sms(skv_ctx *ctx, int32_t sms);
 
 /* Diagnostic: one 128 x n x k bf16 matrix product on the tensor cores through
@@ -664,6 +666,14 @@ SKV_API skv_status skv_selftest_attend_timeout(skv_ctx *ctx, const int32_t *req_
 SKV_API skv_status skv_selftest_select_timeout(skv_ctx *ctx, const skv_index *index, const int32_t *req_ids_dev, int32_t B,
                                                const void *q_dev, const float *w_dev, int32_t *topk_dev,
                                                void *workspace_dev, int64_t workspace_bytes, skv_stream_t stream);
+
+/* The same for skv_attend_prefix (out_dev not null, [units][heads][512] bf16) or skv_weigh_prefix (out_dev null,
+ * weights_dev and lse_dev as there): all layers, no load issued; the waits run out, SKV_DEVERR_TIMEOUT is set and the
+ * outputs are left unspecified. */
+SKV_API skv_status skv_selftest_prefix_timeout(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads,
+                                               const void *q_dev, const float *lse_dev, void *out_dev, float *weights_dev,
+                                               int64_t weights_stride, void *workspace_dev, int64_t workspace_bytes,
+                                               skv_stream_t stream);
 
 /* The message of the last failing CUDA call on this thread ("" if none). */
 SKV_API const char *skv_last_cuda_error(void);

@@ -359,6 +359,10 @@ cudaError_t launch_weigh(const PrefixShape& p, int all_layers, const void* q, co
                          int64_t weights_stride, float* out, int64_t out_stride, float sm_scale, float gain, float* part,
                          uint32_t* err, int device_sms, cudaStream_t st, bool withhold = false)
 {
+    const dim3 sum_grid((unsigned)((p.n + 255) / 256), (unsigned)p.layers);
+    if (p.B == 0)  // the weights as they are
+        return launch_chained(weigh_sum_kernel, sum_grid, 256, 0, st, p, 0, static_cast<const float*>(nullptr), weights, weights_stride,
+                              out, out_stride, gain);
     const WeighPlan plan = weigh_plan(p.n, p.B, p.heads, p.layers, device_sms);
     CUtensorMap key_map, q_map;
     cudaError_t e = encode_rows(p, all_layers, kTileRows, &key_map);
@@ -368,7 +372,7 @@ cudaError_t launch_weigh(const PrefixShape& p, int all_layers, const void* q, co
     e = launch_chained(weigh_kernel, dim3(grid), kWThreads, kWSmem, st, key_map, q_map, p, plan, lse, weights, weights_stride, out,
                        out_stride, part, sm_scale * kLog2e, gain, err, withhold ? 1 : 0);
     if (e != cudaSuccess || plan.shares == 1) return e;
-    return launch_chained(weigh_sum_kernel, dim3((unsigned)((p.n + 255) / 256), (unsigned)p.layers), 256, 0, st, p, plan.shares,
+    return launch_chained(weigh_sum_kernel, sum_grid, 256, 0, st, p, plan.shares,
                           static_cast<const float*>(part), weights, weights_stride, out, out_stride, gain);
 }
 
@@ -908,12 +912,20 @@ struct JoinParts {
 };
 
 // A warp a row, 16 columns a lane.  All of a row is read before any of it is written, so the result may
-// take a part's place.
+// take a part's place.  Bound by HBM: 91 us at two parts of 192 x 8 units of 128 heads (606 MB, 6.66 TB/s, a copy's
+// rate); at 21 units 2.4 us, a launch and a row's latency.
 template <int kParts>
 __global__ void __launch_bounds__(256) join_kernel(JoinParts parts, int64_t rows, uint4* out, float* lse)
 {
     const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * 8;
+    chain_next();
+    chain_wait();
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        parts.out[i] = behind_wait(parts.out[i]);
+        parts.lse[i] = behind_wait(parts.lse[i]);
+    }
     for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += step) {
         float e[kParts], top = -INFINITY;
         uint4 v[kParts][2];
@@ -1443,10 +1455,68 @@ bool rows_ok(const skv_ctx* ctx, const skv_prefix& x)
     return x.n == 0 || (x.rows && aligned(x.rows, 16) && stride_ok(x.row_stride, x.n) &&
                         (x.n == 1 || x.row_stride >= skv::kRowBytes) && stride_ok(x.layer_stride, ctx->cfg.num_layers));
 }
+// Clusters of skv_attend_prefix within skv_set_attend_sms's budget.
+int attend_clusters(const skv_ctx* ctx)
+{
+    return ctx->attend_sms > 0 ? std::max(1, std::min(ctx->prefix_clusters, ctx->attend_sms / 4)) : ctx->prefix_clusters;
+}
 PrefixShape shape_of(const skv_ctx* ctx, const skv_prefix& x, int32_t B, int32_t heads, int32_t layer)
 {
     return PrefixShape{static_cast<const uint8_t*>(x.rows), x.layer_stride, x.row_stride, (int)x.n, B, heads,
                        layer < 0 ? ctx->cfg.num_layers : 1, layer < 0 ? 0 : layer};
+}
+int call_layers(const skv_ctx* ctx, int32_t layer) { return layer < 0 ? ctx->cfg.num_layers : 1; }
+int64_t attend_workspace(const skv_ctx* ctx, const skv_prefix& x, int32_t B, int32_t heads, int32_t layer)
+{
+    if (B == 0 || x.n == 0) return 16;
+    return std::max<int64_t>(16, skv::attend_bytes(skv::attend_plan(x.n, B, heads, call_layers(ctx, layer), attend_clusters(ctx))));
+}
+int64_t weigh_workspace(const skv_ctx* ctx, const skv_prefix& x, int32_t B, int32_t heads, int32_t layer)
+{
+    if (B == 0 || x.n == 0) return 16;
+    const int layers = call_layers(ctx, layer), shares = skv::weigh_plan(x.n, B, heads, layers, ctx->device_sms).shares;
+    return shares > 1 ? skv::align16((int64_t)shares * layers * x.n * 4) : 16;
+}
+
+skv_status attend_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_t heads, int32_t layer,
+                             const void* q_dev, void* out_dev, float* lse_dev, float sm_scale, void* workspace_dev,
+                             int64_t workspace_bytes, skv_stream_t stream, bool withhold)
+{
+    if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale))
+        return SKV_ERR_INVALID_ARG;
+    if (B == 0) return SKV_OK;
+    if (!rows_ok(ctx, *prefix) || !q_dev || !out_dev || !workspace_dev || workspace_bytes < attend_workspace(ctx, *prefix, B, heads, layer) || !aligned(q_dev, 16) ||
+        !aligned(out_dev, 16) || !aligned(lse_dev, 4) || !aligned(workspace_dev, 16))
+        return SKV_ERR_INVALID_ARG;
+    const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);
+    return on_device(ctx, "skv_attend_prefix", [&] {
+        return skv::launch_attend_prefix(p, ctx->cfg.num_layers, q_dev, out_dev, lse_dev, sm_scale, workspace_dev,
+                                         &ctx->d.ctl[skv::CTL_ERR], attend_clusters(ctx), stream, withhold);
+    });
+}
+
+skv_status weigh_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_t heads, int32_t layer,
+                            const void* q_dev, const float* lse_dev, const float* weights_dev, int64_t weights_stride,
+                            float* out_dev, int64_t out_stride, float sm_scale, float gain, void* workspace_dev,
+                            int64_t workspace_bytes, skv_stream_t stream, bool withhold)
+{
+    if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale) ||
+        !std::isfinite(gain))
+        return SKV_ERR_INVALID_ARG;
+    if (prefix->n == 0) return SKV_OK;
+    const bool many = ctx->cfg.num_layers > 1;
+    if (!rows_ok(ctx, *prefix) || !out_dev || !aligned(weights_dev, 4) || !aligned(out_dev, 4) ||
+        (many && (out_stride < prefix->n || (weights_dev && weights_stride < prefix->n))) || out_stride >= (int64_t)1 << 40 ||
+        weights_stride >= (int64_t)1 << 40)
+        return SKV_ERR_INVALID_ARG;
+    if (B > 0 && (!q_dev || !lse_dev || !workspace_dev || workspace_bytes < weigh_workspace(ctx, *prefix, B, heads, layer) ||
+                  !aligned(q_dev, 16) || !aligned(workspace_dev, 16) || !aligned(lse_dev, 4)))
+        return SKV_ERR_INVALID_ARG;
+    const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);
+    return on_device(ctx, "skv_weigh_prefix", [&] {
+        return skv::launch_weigh(p, ctx->cfg.num_layers, q_dev, lse_dev, weights_dev, weights_stride, out_dev, out_stride, sm_scale,
+                                 gain, static_cast<float*>(workspace_dev), &ctx->d.ctl[skv::CTL_ERR], ctx->device_sms, stream, withhold);
+    });
 }
 }  // namespace
 
@@ -1456,9 +1526,7 @@ skv_status skv_attend_prefix_workspace(skv_ctx* ctx, const skv_prefix* prefix, i
                                        int64_t* bytes)
 {
     if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !bytes) return SKV_ERR_INVALID_ARG;
-    *bytes = 16;
-    if (B > 0 && prefix->n > 0)
-        *bytes = std::max<int64_t>(16, skv::attend_bytes(skv::attend_plan(prefix->n, B, heads, layer < 0 ? ctx->cfg.num_layers : 1, ctx->prefix_clusters)));
+    *bytes = attend_workspace(ctx, *prefix, B, heads, layer);
     return SKV_OK;
 }
 
@@ -1466,19 +1534,7 @@ skv_status skv_attend_prefix(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, 
                              const void* q_dev, void* out_dev, float* lse_dev, float sm_scale, void* workspace_dev,
                              int64_t workspace_bytes, skv_stream_t stream)
 {
-    if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale))
-        return SKV_ERR_INVALID_ARG;
-    if (B == 0) return SKV_OK;
-    int64_t need = 0;
-    skv_attend_prefix_workspace(ctx, prefix, B, heads, layer, &need);
-    if (!rows_ok(ctx, *prefix) || !q_dev || !out_dev || !workspace_dev || workspace_bytes < need || !aligned(q_dev, 16) ||
-        !aligned(out_dev, 16) || !aligned(lse_dev, 4) || !aligned(workspace_dev, 16))
-        return SKV_ERR_INVALID_ARG;
-    const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);
-    return on_device(ctx, "skv_attend_prefix", [&] {
-        return skv::launch_attend_prefix(p, ctx->cfg.num_layers, q_dev, out_dev, lse_dev, sm_scale, workspace_dev,
-                                         &ctx->d.ctl[skv::CTL_ERR], ctx->prefix_clusters, stream);
-    });
+    return attend_impl(ctx, prefix, B, heads, layer, q_dev, out_dev, lse_dev, sm_scale, workspace_dev, workspace_bytes, stream, false);
 }
 
 skv_status skv_join(skv_ctx* ctx, int32_t parts, const void* const* outs, const float* const* lses, int64_t rows,
@@ -1498,8 +1554,7 @@ skv_status skv_join(skv_ctx* ctx, int32_t parts, const void* const* outs, const 
             skv::join_kernel<1>, skv::join_kernel<2>, skv::join_kernel<3>, skv::join_kernel<4>,
             skv::join_kernel<5>, skv::join_kernel<6>, skv::join_kernel<7>, skv::join_kernel<8>};
         const unsigned grid = (unsigned)std::min<int64_t>((rows + 7) / 8, 1 << 20);
-        kernels[parts - 1]<<<grid, 256, 0, stream>>>(jp, rows, static_cast<uint4*>(out_dev), lse_dev);
-        return cudaGetLastError();
+        return skv::launch_chained(kernels[parts - 1], dim3(grid), 256, 0, stream, jp, rows, static_cast<uint4*>(out_dev), lse_dev);
     });
 }
 
@@ -1507,9 +1562,7 @@ skv_status skv_weigh_prefix_workspace(skv_ctx* ctx, const skv_prefix* prefix, in
                                       int64_t* bytes)
 {
     if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !bytes) return SKV_ERR_INVALID_ARG;
-    const int layers = layer < 0 ? ctx->cfg.num_layers : 1;
-    const int shares = B > 0 && prefix->n > 0 ? skv::weigh_plan(prefix->n, B, heads, layers, ctx->device_sms).shares : 1;
-    *bytes = shares > 1 ? skv::align16((int64_t)shares * layers * prefix->n * 4) : 16;
+    *bytes = weigh_workspace(ctx, *prefix, B, heads, layer);
     return SKV_OK;
 }
 
@@ -1518,29 +1571,23 @@ skv_status skv_weigh_prefix(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, i
                             float* out_dev, int64_t out_stride, float sm_scale, float gain, void* workspace_dev,
                             int64_t workspace_bytes, skv_stream_t stream)
 {
-    if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale) ||
-        !std::isfinite(gain))
-        return SKV_ERR_INVALID_ARG;
-    if (B == 0 || prefix->n == 0) return SKV_OK;
-    int64_t need = 0;
-    skv_weigh_prefix_workspace(ctx, prefix, B, heads, layer, &need);
-    const bool many = ctx->cfg.num_layers > 1;
-    if (!rows_ok(ctx, *prefix) || !q_dev || !lse_dev || !out_dev || !workspace_dev || workspace_bytes < need ||
-        !aligned(q_dev, 16) || !aligned(workspace_dev, 16) || !aligned(lse_dev, 4) || !aligned(weights_dev, 4) ||
-        !aligned(out_dev, 4) || (many && (out_stride < prefix->n || (weights_dev && weights_stride < prefix->n))) ||
-        out_stride >= (int64_t)1 << 40 || weights_stride >= (int64_t)1 << 40)
-        return SKV_ERR_INVALID_ARG;
-    const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);
-    return on_device(ctx, "skv_weigh_prefix", [&] {
-        return skv::launch_weigh(p, ctx->cfg.num_layers, q_dev, lse_dev, weights_dev, weights_stride, out_dev, out_stride, sm_scale,
-                                 gain, static_cast<float*>(workspace_dev), &ctx->d.ctl[skv::CTL_ERR], ctx->device_sms, stream);
-    });
+    return weigh_impl(ctx, prefix, B, heads, layer, q_dev, lse_dev, weights_dev, weights_stride, out_dev, out_stride, sm_scale, gain,
+                      workspace_dev, workspace_bytes, stream, false);
+}
+
+skv_status skv_selftest_prefix_timeout(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_t heads, const void* q_dev,
+                                       const float* lse_dev, void* out_dev, float* weights_dev, int64_t weights_stride,
+                                       void* workspace_dev, int64_t workspace_bytes, skv_stream_t stream)
+{
+    if (out_dev) return attend_impl(ctx, prefix, B, heads, -1, q_dev, out_dev, nullptr, 1.0f, workspace_dev, workspace_bytes, stream, true);
+    return weigh_impl(ctx, prefix, B, heads, -1, q_dev, lse_dev, nullptr, 0, weights_dev, weights_stride, 1.0f, 1.0f, workspace_dev,
+                      workspace_bytes, stream, true);
 }
 
 skv_status skv_evict_prefix_workspace(skv_ctx* ctx, const skv_prefix* prefix, int32_t layer, int64_t* bytes)
 {
     if (!shape_ok(ctx, prefix, layer) || !bytes) return SKV_ERR_INVALID_ARG;
-    *bytes = skv::evict_bytes(prefix->n, layer < 0 ? ctx->cfg.num_layers : 1);
+    *bytes = skv::evict_bytes(prefix->n, call_layers(ctx, layer));
     return SKV_OK;
 }
 
@@ -1553,7 +1600,7 @@ skv_status skv_evict_prefix(skv_ctx* ctx, const skv_prefix* prefix, int32_t laye
         (int64_t)first + last > keep)
         return SKV_ERR_INVALID_ARG;
     if (!rows_ok(ctx, *prefix) || !kept_dev || !workspace_dev || (prefix->n > 0 && !weights_dev) ||
-        workspace_bytes < skv::evict_bytes(prefix->n, layer < 0 ? ctx->cfg.num_layers : 1) || !aligned(workspace_dev, 16) || !aligned(rows_out_dev, 16) ||
+        workspace_bytes < skv::evict_bytes(prefix->n, call_layers(ctx, layer)) || !aligned(workspace_dev, 16) || !aligned(rows_out_dev, 16) ||
         !aligned(kept_dev, 4) || !aligned(weights_dev, 4) || !aligned(weights_out_dev, 4) ||
         (ctx->cfg.num_layers > 1 && weights_stride < prefix->n) || weights_stride >= (int64_t)1 << 40)
         return SKV_ERR_INVALID_ARG;

@@ -117,6 +117,7 @@ def _load():
         "skv_weigh_prefix": [vp, P(skv_prefix), i32, i32, i32, vp, vp, vp, i64, vp, i64, ctypes.c_float, ctypes.c_float, vp, i64, vp],
         "skv_evict_prefix_workspace": [vp, P(skv_prefix), i32, P(i64)],
         "skv_evict_prefix": [vp, P(skv_prefix), i32, vp, i64, i32, i32, i32, vp, vp, vp, vp, i64, vp],
+        "skv_selftest_prefix_timeout": [vp, P(skv_prefix), i32, i32, vp, vp, vp, vp, i64, vp, i64, vp],
         "skv_pool_placement": [vp, P(i32), P(i32), P(ctypes.c_float)],
         "skv_host_node_for_pci": [ctypes.c_char_p, ctypes.c_char_p, P(i32)],
     }
@@ -171,6 +172,7 @@ skv_weigh_prefix_workspace = lib.skv_weigh_prefix_workspace
 skv_weigh_prefix = lib.skv_weigh_prefix
 skv_evict_prefix_workspace = lib.skv_evict_prefix_workspace
 skv_evict_prefix = lib.skv_evict_prefix
+skv_selftest_prefix_timeout = lib.skv_selftest_prefix_timeout
 skv_pool_placement = lib.skv_pool_placement
 skv_host_node_for_pci = lib.skv_host_node_for_pci
 skv_last_cuda_error = lib.skv_last_cuda_error
@@ -644,6 +646,13 @@ class Context:
         check(skv_selftest_select_timeout(self.h, index.c(q.shape[-2]), _ptr(req_ids), B, _ptr(q), _ptr(w), _ptr(topk),
                                           _ptr(workspace), workspace.nbytes, _stream_handle(stream, self.cfg.device)),
               "skv_selftest_select_timeout")
+
+    def selftest_prefix_timeout(self, prefix: Prefix, q, lse, out, weights, workspace, B: int | None = None, stream=None) -> None:
+        """attend_prefix() (out given) or weigh_prefix() with its loads withheld (see skv_selftest_prefix_timeout)."""
+        c, B, _, heads, _, dev = self._prefix(prefix, q, -1, B, "selftest_prefix_timeout")
+        check(skv_selftest_prefix_timeout(self.h, c, B, heads, _ptr(q), _ptr(lse), _ptr(out), _ptr(weights),
+                                          0 if weights is None else weights.stride(0), _ptr(workspace), workspace.nbytes,
+                                          _stream_handle(stream, dev)), "skv_selftest_prefix_timeout")
 
     # inspection ------------------------------------------------------------
     def get_device_error(self, stream=None) -> int:
