@@ -479,7 +479,7 @@ SKV_API skv_status skv_attend_prefix_workspace(skv_ctx *ctx, const skv_prefix *p
  *   out[unit][h][0..512) = sum_j softmax_j(s_h)_j * row(l, j)[0..512)
  *   lse[unit][h] = log sum_j exp(s_hj)   (n == 0: -inf, and zero output)
  * q_dev [units][heads][576] bf16, out_dev [units][heads][512] bf16, lse_dev
- * [units][heads] fp32 (may be null); device memory, q, out and workspace 16-byte
+ * [units][heads] fp32 (may be null); device memory, q 32-byte, out and workspace 16-byte
  * aligned; sm_scale finite and > 0.  Products on the tensor cores in fp32, P
  * rounded to bf16; the output is divided by the sum of the rounded P, lse is that of the
  * unrounded ones.  A head with a NaN score has NaN results.  With skv_join the result
@@ -514,7 +514,7 @@ SKV_API skv_status skv_weigh_prefix_workspace(skv_ctx *ctx, const skv_prefix *pr
  * a request's whole attention, that of skv_attend_prefix for shares within the prefix.  A head whose lse is -inf adds nothing.
  * weights_dev (null: zeros) and out_dev (may be the same) hold row l at l*weights_stride and l*out_stride
  * floats, in calls on one layer too; nothing behind out[l][n - 1] is written.  gain finite (a gain
- * that grows from step to step lets older weights fade).  The rest as in skv_attend_prefix.
+ * that grows from step to step lets older weights fade).  q_dev 16-byte aligned; the rest as in skv_attend_prefix.
  * B == 0: out is weights.  Sums are fp32 in a fixed order: the same call gives the same result. */
 SKV_API skv_status skv_weigh_prefix(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads, int32_t layer,
                                     const void *q_dev, const float *lse_dev, const float *weights_dev,

@@ -629,14 +629,25 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
             const int64_t row = tile_row(p, w.l, 2 * w.pair + (int)r, tid - 32 * kQWarp0);
             if (n > 0 && !(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.q_free, (n - 1) & 1, abort)))) break;
             tc::fence_after_sync();
+            // (each lane reads a row of its own, so it is the number of sectors asked for that takes the time: 32 bytes at once)
 #pragma unroll 1
             for (int x = 0; x < kQtBoxes; x += kQAtOnce) {
-                uint4 v[8 * kQAtOnce];
-#pragma unroll
-                for (int j = 0; j < 8 * kQAtOnce; ++j) v[j] = row >= 0 ? rows[row * (kRowBytes / 16) + 8 * x + j] : make_uint4(0, 0, 0, 0);
+                uint32_t v[8 * kQAtOnce][4];
 #pragma unroll
                 for (int j = 0; j < 8 * kQAtOnce; j += 2) {
-                    const uint32_t a[8] = {v[j].x, v[j].y, v[j].z, v[j].w, v[j + 1].x, v[j + 1].y, v[j + 1].z, v[j + 1].w};
+                    const uint4* at = rows + row * (kRowBytes / 16) + 8 * x + j;
+                    if (row < 0) {
+                        v[j][0] = v[j][1] = v[j][2] = v[j][3] = v[j + 1][0] = v[j + 1][1] = v[j + 1][2] = v[j + 1][3] = 0u;
+                    } else {
+                        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                                     : "=r"(v[j][0]), "=r"(v[j][1]), "=r"(v[j][2]), "=r"(v[j][3]), "=r"(v[j + 1][0]), "=r"(v[j + 1][1]),
+                                       "=r"(v[j + 1][2]), "=r"(v[j + 1][3])
+                                     : "l"(at));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8 * kQAtOnce; j += 2) {
+                    const uint32_t a[8] = {v[j][0], v[j][1], v[j][2], v[j][3], v[j + 1][0], v[j + 1][1], v[j + 1][2], v[j + 1][3]};
                     tc::tmem_st8_async(tl + 32 * x + 4 * j, a);
                 }
             }
@@ -1485,7 +1496,7 @@ skv_status attend_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_
     if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale))
         return SKV_ERR_INVALID_ARG;
     if (B == 0) return SKV_OK;
-    if (!rows_ok(ctx, *prefix) || !q_dev || !out_dev || !workspace_dev || workspace_bytes < attend_workspace(ctx, *prefix, B, heads, layer) || !aligned(q_dev, 16) ||
+    if (!rows_ok(ctx, *prefix) || !q_dev || !out_dev || !workspace_dev || workspace_bytes < attend_workspace(ctx, *prefix, B, heads, layer) || !aligned(q_dev, 32) ||
         !aligned(out_dev, 16) || !aligned(lse_dev, 4) || !aligned(workspace_dev, 16))
         return SKV_ERR_INVALID_ARG;
     const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);

@@ -118,6 +118,17 @@ def test_attention_within_an_sm_budget(B, n, sms):
     c.check()
 
 
+def test_queries_that_lie_off_a_border_of_32_bytes_are_refused():
+    c = Case(2, 1, 300)
+    flat = torch.zeros(2 * 128 * 576 + 16, device="cuda", dtype=torch.bfloat16)
+    for off in (1, 4, 8):
+        with pytest.raises(skv.SkvError):
+            c.ctx.attend_prefix(c.prefix, flat[off:off + 2 * 128 * 576].view(2, 128, 576), c.out, c.lse, _bytes(1 << 24))
+    c.q = flat[16:].view(2, 128, 576).copy_(c.q)
+    c.attend()
+    c.check()
+
+
 def test_an_empty_batch():
     c = Case(2, 1, 300)
     none, w, out = c.q[:0], torch.rand((1, 300), device="cuda"), torch.full((1, 310), 5.0, device="cuda")
