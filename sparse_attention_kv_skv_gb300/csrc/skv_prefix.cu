@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "f32x2.cuh"
 #include "skv_ctx.cuh"
@@ -101,6 +102,12 @@ __device__ __forceinline__ int64_t tile_row(const PrefixShape& p, int l, int til
 // A piece of the work is 256 keys of a layer by a share of its query rows; the
 // keys stay in shared memory (147 KB a CTA) while the queries stream past them through a ring of
 // 64-dim columns.  Shares are summed in their order by a second kernel.
+// What bounds it: the products, 128 cycles each of 256 x 256 x 16, 4608 a pair of tiles; beside them go 32 bytes a cycle
+// from L2 and 96 of the 128 bytes a cycle that shared memory gives (with a CTA by itself, not a pair, 192 would), and an
+// epilogue of 256 exponentials a thread, 2048 cycles.
+// Measured: 443 us at 192 x 2 units of 128 heads over 16K tokens, 2.1 PFLOP/s, more than the 1.95 of a large library product; 9.1 us
+// at 4 units over 4096 tokens, 11.0 at 5 x 3 of 40 heads over 10007: launch, set-up, 147 KB of keys a CTA, one or two products.
+// (-lse log2 e and the scale in two floats each: 453 us and the same error, which is the tensor core's own.)
 constexpr int kWRing = 4;                      // query columns in flight (16 KB each)
 constexpr int kWEpilogue = 128, kWLoadWarp = 4, kWMmaWarp = 5, kWThreads = 192;
 constexpr uint32_t kWTmemCols = 512;           // two products of 256 columns
@@ -238,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
         auto neg_of = [&](int l, int tile) {
             const int64_t r = tile_row(p, l, tile, tid);
             const float e = r >= 0 ? lse[r] : -INFINITY;
-            return e == -INFINITY ? -INFINITY : -e * kLog2e;  // a row that is none, or attended to nothing, adds 2^-inf
+            return e == -INFINITY ? -INFINITY : -e * kLog2e;  // a row that is none, or attended to nothing, adds nothing
         };
         bool ok = true;
         int it = 0;
@@ -249,26 +256,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
             for (int pr = p0; pr < p1; ++pr, ++it) {
                 const int d = it & 1;
                 float* neg = c.neg[d];
-                neg[tid] = neg_of(l, 2 * pr);
-                neg[kTileRows + tid] = neg_of(l, 2 * pr + 1);
-                tc::named_sync(1, kWEpilogue);
+                const float n0 = neg_of(l, 2 * pr), n1 = neg_of(l, 2 * pr + 1);
+                neg[tid] = n0;
+                neg[kTileRows + tid] = n1;
+                const bool gaps = tc::named_sync_or(1, kWEpilogue, n0 == -INFINITY || n1 == -INFINITY);
                 // a give-up must not leave the other threads at a barrier
                 ok = ok && wait_phase(&c.d_full[d], (it >> 1) & 1, abort);
                 if (__all_sync(0xFFFFFFFFu, ok)) {
                     tc::fence_after_sync();
+                    // A row that adds nothing may have a NaN score (a key that holds an infinity, by a zero), so where there are
+                    // such rows they are left out one by one (443 us at 192 x 2 units over 16K tokens, 473 with it).
+                    auto sum_columns = [&](auto with_gaps) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < 2 * kTileRows; c0 += 32) {
-                        float v[32];
-                        tc::tmem_ld32(tl + 256 * d + c0, v);
+                        for (int c0 = 0; c0 < 2 * kTileRows; c0 += 32) {
+                            float v[32];
+                            tc::tmem_ld32(tl + 256 * d + c0, v);
 #pragma unroll
-                        for (int x = 0; x < 32; x += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(neg + c0 + x);
-                            acc[0] += ex2(fmaf(v[x], scale_log2, f.x));
-                            acc[1] += ex2(fmaf(v[x + 1], scale_log2, f.y));
-                            acc[2] += ex2(fmaf(v[x + 2], scale_log2, f.z));
-                            acc[3] += ex2(fmaf(v[x + 3], scale_log2, f.w));
+                            for (int x = 0; x < 32; x += 4) {
+                                const float4 f4 = *reinterpret_cast<const float4*>(neg + c0 + x);
+                                const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    const float e = ex2(fmaf(v[x + y], scale_log2, f[y]));
+                                    acc[y] += decltype(with_gaps)::value && f[y] == -INFINITY ? 0.0f : e;
+                                }
+                            }
                         }
-                    }
+                    };
+                    if (gaps)
+                        sum_columns(std::true_type{});
+                    else
+                        sum_columns(std::false_type{});
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive_at(df + 8 * d);
@@ -389,6 +407,16 @@ cudaError_t launch_weigh(const PrefixShape& p, int all_layers, const void* q, co
 // reference there is while the maxima travel, and again if it has risen.  P goes into shared memory, by
 // a bulk copy into the other pair's as well.
 // Items that do not fill the clusters evenly are split along the keys; combine_prefix_kernel joins their parts.
+// What bounds it: the products, 2176 cycles a block (36 of 256 x 64 x 16, 8 of 256 x 256 x 16), beside which shared memory
+// moves 265 KB (2070 cycles); from S to P there are an exchange of maxima, 64 exponentials a thread and the copy of P, some 2500 cycles, which
+// the products of the next scores cover.  Measured: 941 us at 192 x 2 units over 16K tokens, 1.86 PFLOP/s, 96 % of a
+// large library product's rate; 172 us at 8 units over 128K (1.70); 13.6 us at 2 over 1000, 18.6 at 7 x 3 of 16 heads over 5003, where a
+// launch, the queries' way into tensor memory (3 us), one block's chain, the parts' way out (2 us) and the joining kernel (3 us) are all there is.
+// On the way here, at 192 x 2 units: a pair for each half of the value dims, both taking all scores, 1539 us; this decomposition
+// with one warp for both streams of products 1075; waits and arrivals at cluster scope and the scores' columns in stages of their
+// own 2151.  The code has to stay small: with 112 KB of it instead of 60 the instruction caches, which GPCs share, were what
+// bounded it (1628 us; GPCs with three clusters were done in 249 us where those with five took 340).
+// Scores double-buffered, with more of Q in shared memory: 1118; P by st.async instead of bulk copies: 1079 (against 1050).
 constexpr int kBlk = 128, kHalfBlk = 64;       // keys of a block, and those that a pair scores
 constexpr int kKRing = 2, kVRing = 2;          // key stages (32 keys, 36 KB), value stages (64 keys x 128 dims, 16 KB)
 constexpr uint32_t kKBox = 32 * 128, kKStage = kBoxes * kKBox, kVBox = 64 * 128, kVStage = 2 * kVBox;
@@ -403,7 +431,7 @@ struct alignas(16) AttendCtl {
     // "leader": the barrier of the pair's first CTA, which multiplies
     uint64_t q_full, q_tm, q_free;             // queries in shared memory (leader, bytes of both CTAs), in tensor memory
                                                // (leader, a warp of either CTA); the item's scores are done (both)
-    uint64_t k_full[kKRing], k_free[kKRing];   // key columns (leader, bytes of both; both)
+    uint64_t k_full[kKRing], k_free[kKRing];   // key stages (leader, bytes of both CTAs; both)
     uint64_t v_full[kVRing], v_free[kVRing];   // value stages
     uint64_t s_full, s_free;                   // a block's scores are complete (both); have been read (leader, a warp of either)
     uint64_t m_full[2];                        // the other pair's maxima of a block have arrived (512 bytes)
@@ -433,6 +461,7 @@ struct AttendPlan {
     __device__ int item(int piece) const { return piece < direct ? piece : direct + (piece - direct) % rest; }
     __device__ int split(int piece) const { return piece < direct ? 0 : (piece - direct) / rest; }
 };
+
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
     attend_prefix_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap value_map,
                          const __grid_constant__ CUtensorMap q_map, PrefixShape p, AttendPlan plan, const uint16_t* q,
@@ -865,8 +894,11 @@ __global__ void __launch_bounds__(256) nothing_kernel(int64_t rows, uint4* out, 
     }
 }
 
-// Whole items for full rounds of the clusters; the rest in splits such that its rounds are short: rounds * (blocks + what
-// a piece costs besides, 1.5 blocks), and the joining of the parts.
+// Whole items for full rounds of the clusters; the rest in splits such that its rounds are short.  In units of a block's time
+// (1.25 us): rounds * (blocks + 2.5 for what a piece costs besides) and, for the joining of the parts, 2 and what their bytes
+// take (0.5 MB a split, written and read).  Swept over the splits, the choice was the fastest or within 0.2 us of it at 2 x 1000
+// (14.9 us with 8 splits, 16.8 with 2, 19.9 with one), 7 x 3 x 5003 of 16 heads (19.2 with 10, 24.9 with 4 and with 20),
+// 8 x 3000, 64 x 2000, 80 x 2000 (44.1 with 8, 57.3 with one) and 1 x 20000 tokens (23.5 with 40, 36 with 9).
 AttendPlan attend_plan(int64_t n, int B, int heads, int layers, int ncl)
 {
     const int nblk = (int)((n + kBlk - 1) / kBlk);
@@ -877,7 +909,7 @@ AttendPlan attend_plan(int64_t n, int B, int heads, int layers, int ncl)
     for (int k = 1; k <= std::min(nblk, 64); ++k) {
         const int blocks = (nblk + k - 1) / k;
         if ((nblk + blocks - 1) / blocks != k) continue;  // the last splits would be empty
-        const double cost = (double)((a.rest * (int64_t)k + ncl - 1) / ncl) * (blocks + 2.5) + (k > 1 ? 2.0 + 0.07 * k : 0.0);
+        const double cost = (double)((a.rest * (int64_t)k + ncl - 1) / ncl) * (blocks + 2.5) + (k > 1 ? 2.0 + 0.07 * k * a.rest : 0.0);
         if (cost < least) {
             least = cost;
             a.splits = k;
@@ -1034,7 +1066,8 @@ __global__ void __launch_bounds__(256) keep_all_kernel(Heaviest h, int32_t* kept
 
 // Short rows: a CTA a layer, its words in shared memory.  The range of the words is narrowed by histograms of 2048
 // equal parts until the part that holds the threshold has few enough to be ranked directly; the first range is that of the
-// words themselves, so mostly the first histogram is the only one.  Bound by latency: some ten barriers.
+// words themselves, so mostly the first histogram is the only one.  Bound by latency: some ten barriers; 5 us at 4096 tokens,
+// 13 at 8 x 16001.
 constexpr int kShort = 32768, kShortThreads = 1024, kBins = 2048, kFew = 256;
 __global__ void __launch_bounds__(kShortThreads) heaviest_short_kernel(Heaviest h, int32_t* kept)
 {
@@ -1178,7 +1211,8 @@ __global__ void __launch_bounds__(kShortThreads) heaviest_short_kernel(Heaviest 
 
 // Long rows: chunks of 8192 tokens, a CTA each, over the whole GPU.  Three passes find the threshold's digits (11, 11 and
 // 10 bits, from the top) by histograms of the words that share the digits found so far; the last CTA of a layer to finish a pass
-// picks the digit.  A fourth pass counts, a fifth writes.  Each pass reads the weights once, from L2 after the first.
+// picks the digit.  A fourth pass counts, a fifth writes.  Each pass reads the weights once, from L2 after the first: 34 us in all at
+// 2 x 1M tokens (one team of CTAs a layer took 96).
 constexpr int kChunk = 8192, kLongThreads = 512;
 struct LongState {  // of a layer; zeros before the first pass
     uint32_t hist[3][kBins];
@@ -1439,8 +1473,8 @@ skv_status on_device(const skv_ctx* ctx, const char* what, F f)
 {
     int prev = -1;
     if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    if (prev != ctx->cfg.device && cudaSetDevice(ctx->cfg.device) != cudaSuccess) return SKV_ERR_CUDA;
-    const cudaError_t e = f();
+    cudaError_t e = prev != ctx->cfg.device ? cudaSetDevice(ctx->cfg.device) : cudaSuccess;
+    if (e == cudaSuccess) e = f();
     if (prev >= 0 && prev != ctx->cfg.device) cudaSetDevice(prev);
     if (e == cudaSuccess) return SKV_OK;
     skv::set_last_error_message((std::string(what) + ": " + cudaGetErrorString(e)).c_str());
@@ -1490,8 +1524,8 @@ int64_t weigh_workspace(const skv_ctx* ctx, const skv_prefix& x, int32_t B, int3
 }
 
 skv_status attend_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_t heads, int32_t layer,
-                             const void* q_dev, void* out_dev, float* lse_dev, float sm_scale, void* workspace_dev,
-                             int64_t workspace_bytes, skv_stream_t stream, bool withhold)
+                       const void* q_dev, void* out_dev, float* lse_dev, float sm_scale, void* workspace_dev,
+                       int64_t workspace_bytes, skv_stream_t stream, bool withhold)
 {
     if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale))
         return SKV_ERR_INVALID_ARG;
@@ -1507,9 +1541,9 @@ skv_status attend_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_
 }
 
 skv_status weigh_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_t heads, int32_t layer,
-                            const void* q_dev, const float* lse_dev, const float* weights_dev, int64_t weights_stride,
-                            float* out_dev, int64_t out_stride, float sm_scale, float gain, void* workspace_dev,
-                            int64_t workspace_bytes, skv_stream_t stream, bool withhold)
+                      const void* q_dev, const float* lse_dev, const float* weights_dev, int64_t weights_stride,
+                      float* out_dev, int64_t out_stride, float sm_scale, float gain, void* workspace_dev,
+                      int64_t workspace_bytes, skv_stream_t stream, bool withhold)
 {
     if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale) ||
         !std::isfinite(gain))

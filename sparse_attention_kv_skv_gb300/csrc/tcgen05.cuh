@@ -453,6 +453,17 @@ __device__ __forceinline__ void named_sync(uint32_t id, uint32_t nthreads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// The same, and whether `value` holds in any of the threads.
+__device__ __forceinline__ bool named_sync_or(uint32_t id, uint32_t nthreads, bool value)
+{
+    uint32_t any;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(any)
+        : "r"((uint32_t)value), "r"(id), "r"(nthreads)
+        : "memory");
+    return any != 0u;
+}
 // Per-thread register budget of the executing warpgroup (all four warps execute it).
 template <int N>
 __device__ __forceinline__ void regs_grow()

@@ -332,7 +332,149 @@ class Prefix:
 _pointers = [ctypes.c_void_p * (2 * i) for i in range(9)]  # a join's parts: their outs, then their lses
 
 
-class Context:
+class PrefixCalls:
+    """The calls of a Context around a prefix that a whole batch shares."""
+
+    def _prefix(self, prefix: Prefix, q, layer: int, B: int | None, what: str):
+        """What a call's description starts with: (the prefix, B, units, heads, tokens, the context's device)."""
+        c, layers, n, dev = prefix._made
+        if layers < self.cfg.num_layers:
+            raise ValueError(f"{what}: the prefix has fewer layers than the context")
+        if dev != self.cfg.device:
+            _elsewhere(prefix.rows, self.cfg.device, f"{what}: the prefix")
+        layers = 1 if layer >= 0 else self.cfg.num_layers
+        if q is None:
+            return c, 0, layers, 0, n, self.cfg.device
+        shape = q.shape
+        if len(shape) != 3 or shape[2] != 576:
+            raise ValueError(f"{what}: q must be [units][heads][576]")
+        if B is None:
+            B, rest = divmod(shape[0], layers)
+            if rest:
+                raise ValueError(f"{what}: q must hold a unit of every layer for each entry of the batch")
+        return c, B, B * layers, shape[1], n, self.cfg.device
+
+    def _weights(self, t, n: int, dev: int, what: str) -> int:
+        """The row stride of weights [L][n] fp32 with adjacent values."""
+        shape = t.shape
+        if len(shape) != 2 or shape[0] < self.cfg.num_layers or shape[1] < n or not _is_type(t, "fp32"):
+            raise ValueError(f"{what} must be [layers][tokens] fp32")
+        step = t.stride()
+        if shape[1] > 1 and step[1] != 1:
+            raise ValueError(f"{what} must have adjacent values")
+        if t.get_device() != dev:
+            _elsewhere(t, dev, what)
+        return step[0]
+
+    def attend_prefix_workspace(self, prefix: Prefix, B: int, heads: int = 128, layer: int = -1) -> int:
+        """Bytes of workspace an attend_prefix() of B entries needs."""
+        n = ctypes.c_int64()
+        check(skv_attend_prefix_workspace(self.h, prefix.c(), B, heads, layer, ctypes.byref(n)), "skv_attend_prefix_workspace")
+        return n.value
+
+    def attend_prefix(self, prefix: Prefix, q, out, lse, workspace, layer: int = -1, sm_scale: float | None = None,
+                      B: int | None = None, stream=None) -> None:
+        """MLA attention of a batch over a prefix that all of it shares (see skv_attend_prefix):
+        q [units][heads][576] bf16 -> out [units][heads][512] bf16, lse [units][heads] (or None).
+        workspace: attend_prefix_workspace() bytes."""
+        c, B, units, heads, _, dev = self._prefix(prefix, q, layer, B, "attend_prefix")
+        rows = units * heads
+        _need(q, "bf16", rows * 1152, dev, "attend_prefix: q")
+        _need(out, "bf16", rows * 1024, dev, "attend_prefix: out")
+        if lse is not None:
+            _need(lse, "fp32", rows * 4, dev, "attend_prefix: lse")
+        _need(workspace, None, 0, dev, "attend_prefix: workspace")
+        status = skv_attend_prefix(self.h, c, B, heads, layer, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                   1.0 / 24.0 if sm_scale is None else sm_scale, workspace.data_ptr(), workspace.nbytes,
+                                   _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
+        if status:
+            check(status, "skv_attend_prefix")
+
+    def join(self, outs, lses, out, lse=None, stream=None) -> None:
+        """Join attention results over disjoint sets of tokens (see skv_join): outs, up to 8 of
+        [...][512] bf16, and lses [...] fp32 -> out, lse, which may take a part's place."""
+        parts, dev, size = len(outs), self.cfg.device, out.numel()
+        if len(lses) != parts or not 1 <= parts <= 8:
+            raise ValueError("join: 1 to 8 parts, each with its lse")
+        if out.shape[-1] != 512:
+            raise ValueError("join: out must be [...][512]")
+        rows = size // 512
+        for o, e in zip(outs, lses):
+            if o.numel() != size or e.numel() != rows:
+                raise ValueError("join: the parts and the result differ in size")
+            _need(o, "bf16", rows * 1024, dev, "join: outs")
+            _need(e, "fp32", rows * 4, dev, "join: lses")
+        _need(out, "bf16", rows * 1024, dev, "join: out")
+        if lse is not None:
+            _need(lse, "fp32", rows * 4, dev, "join: lse")
+        both = _pointers[parts](*[o.data_ptr() for o in outs], *[e.data_ptr() for e in lses])
+        status = skv_join(self.h, parts, both, ctypes.byref(both, 8 * parts), rows,
+                          out.data_ptr(), None if lse is None else lse.data_ptr(),
+                          _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
+        if status:
+            check(status, "skv_join")
+
+    def weigh_prefix_workspace(self, prefix: Prefix, B: int, heads: int = 128, layer: int = -1) -> int:
+        """Bytes of workspace a weigh_prefix() of B entries needs."""
+        n = ctypes.c_int64()
+        check(skv_weigh_prefix_workspace(self.h, prefix.c(), B, heads, layer, ctypes.byref(n)), "skv_weigh_prefix_workspace")
+        return n.value
+
+    def weigh_prefix(self, prefix: Prefix, q, lse, weights, out, workspace, layer: int = -1, sm_scale: float | None = None,
+                     gain: float = 1.0, B: int | None = None, stream=None) -> None:
+        """out = weights (or 0 for None) + gain times the attention weight that each of the prefix's
+        tokens receives from the batch (see skv_weigh_prefix): q [units][heads][576] bf16, lse
+        [units][heads], weights and out [L][n] fp32 (may be the same)."""
+        c, B, units, heads, n, dev = self._prefix(prefix, q, layer, B, "weigh_prefix")
+        rows = units * heads
+        _need(q, "bf16", rows * 1152, dev, "weigh_prefix: q")
+        _need(lse, "fp32", rows * 4, dev, "weigh_prefix: lse")
+        w_stride = 0 if weights is None else self._weights(weights, n, dev, "weigh_prefix: weights")
+        o_stride = self._weights(out, n, dev, "weigh_prefix: out")
+        _need(workspace, None, 0, dev, "weigh_prefix: workspace")
+        status = skv_weigh_prefix(self.h, c, B, heads, layer, q.data_ptr(), lse.data_ptr(), None if weights is None else weights.data_ptr(),
+                                  w_stride, out.data_ptr(), o_stride, 1.0 / 24.0 if sm_scale is None else sm_scale, gain,
+                                  workspace.data_ptr(), workspace.nbytes,
+                                  _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
+        if status:
+            check(status, "skv_weigh_prefix")
+
+    def evict_prefix_workspace(self, prefix: Prefix, layer: int = -1) -> int:
+        """Bytes of workspace an evict_prefix() needs."""
+        n = ctypes.c_int64()
+        check(skv_evict_prefix_workspace(self.h, prefix.c(), layer, ctypes.byref(n)), "skv_evict_prefix_workspace")
+        return n.value
+
+    def evict_prefix(self, prefix: Prefix, weights, kept, rows, kept_weights, workspace, first: int = 0, last: int = 0,
+                     layer: int = -1, stream=None) -> None:
+        """Keep a prefix's heaviest tokens (see skv_evict_prefix): weights [L][n] fp32 -> kept
+        [layers of the call][keep] int32, ascending, their rows [..][keep][576] bf16 and weights [..][keep] (either may be
+        None).  Prefix(rows) takes the old one's place."""
+        c, _, layers, _, n, dev = self._prefix(prefix, None, layer, None, "evict_prefix")
+        keep = kept.shape[-1]
+        stride = self._weights(weights, n, dev, "evict_prefix: weights")
+        _need(kept, "int32", 4 * layers * keep, dev, "evict_prefix: kept")
+        if rows is not None:
+            _need(rows, "bf16", 1152 * layers * keep, dev, "evict_prefix: rows")
+        if kept_weights is not None:
+            _need(kept_weights, "fp32", 4 * layers * keep, dev, "evict_prefix: kept_weights")
+        _need(workspace, None, 0, dev, "evict_prefix: workspace")
+        status = skv_evict_prefix(self.h, c, layer, weights.data_ptr(), stride, keep, first, last, kept.data_ptr(),
+                                  None if rows is None else rows.data_ptr(), None if kept_weights is None else kept_weights.data_ptr(),
+                                  workspace.data_ptr(), workspace.nbytes,
+                                  _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
+        if status:
+            check(status, "skv_evict_prefix")
+
+    def selftest_prefix_timeout(self, prefix: Prefix, q, lse, out, weights, workspace, B: int | None = None, stream=None) -> None:
+        """attend_prefix() (out given) or weigh_prefix() with its loads withheld (see skv_selftest_prefix_timeout)."""
+        c, B, _, heads, _, dev = self._prefix(prefix, q, -1, B, "selftest_prefix_timeout")
+        check(skv_selftest_prefix_timeout(self.h, c, B, heads, _ptr(q), _ptr(lse), _ptr(out), _ptr(weights),
+                                          0 if weights is None else weights.stride(0), _ptr(workspace), workspace.nbytes,
+                                          _stream_handle(stream, dev)), "skv_selftest_prefix_timeout")
+
+
+class Context(PrefixCalls):
     """One library context (pool, hot buffer, maps) on one GPU."""
 
     def __init__(self, cfg: Config):
@@ -501,138 +643,6 @@ class Context:
         if status:
             check(status, "skv_unpack_rows")
 
-    # a prefix that the batch shares ------------------------------------------
-    def _prefix(self, prefix: Prefix, q, layer: int, B: int | None, what: str):
-        """What a call's description starts with: (the prefix, B, units, heads, tokens, the context's device)."""
-        c, layers, n, dev = prefix._made
-        if layers < self.cfg.num_layers:
-            raise ValueError(f"{what}: the prefix has fewer layers than the context")
-        if dev != self.cfg.device:
-            _elsewhere(prefix.rows, self.cfg.device, f"{what}: the prefix")
-        layers = 1 if layer >= 0 else self.cfg.num_layers
-        if q is None:
-            return c, 0, layers, 0, n, self.cfg.device
-        shape = q.shape
-        if len(shape) != 3 or shape[2] != 576:
-            raise ValueError(f"{what}: q must be [units][heads][576]")
-        if B is None:
-            B, rest = divmod(shape[0], layers)
-            if rest:
-                raise ValueError(f"{what}: q must hold a unit of every layer for each entry of the batch")
-        return c, B, B * layers, shape[1], n, self.cfg.device
-
-    def _weights(self, t, n: int, dev: int, what: str) -> int:
-        """The row stride of weights [L][n] fp32 with adjacent values."""
-        shape = t.shape
-        if len(shape) != 2 or shape[0] < self.cfg.num_layers or shape[1] < n or not _is_type(t, "fp32"):
-            raise ValueError(f"{what} must be [layers][tokens] fp32")
-        step = t.stride()
-        if shape[1] > 1 and step[1] != 1:
-            raise ValueError(f"{what} must have adjacent values")
-        if t.get_device() != dev:
-            _elsewhere(t, dev, what)
-        return step[0]
-
-    def attend_prefix_workspace(self, prefix: Prefix, B: int, heads: int = 128, layer: int = -1) -> int:
-        """Bytes of workspace an attend_prefix() of B entries needs."""
-        n = ctypes.c_int64()
-        check(skv_attend_prefix_workspace(self.h, prefix.c(), B, heads, layer, ctypes.byref(n)), "skv_attend_prefix_workspace")
-        return n.value
-
-    def attend_prefix(self, prefix: Prefix, q, out, lse, workspace, layer: int = -1, sm_scale: float | None = None,
-                      B: int | None = None, stream=None) -> None:
-        """MLA attention of a batch over a prefix that all of it shares (see skv_attend_prefix):
-        q [units][heads][576] bf16 -> out [units][heads][512] bf16, lse [units][heads] (or None).
-        workspace: attend_prefix_workspace() bytes."""
-        c, B, units, heads, _, dev = self._prefix(prefix, q, layer, B, "attend_prefix")
-        rows = units * heads
-        _need(q, "bf16", rows * 1152, dev, "attend_prefix: q")
-        _need(out, "bf16", rows * 1024, dev, "attend_prefix: out")
-        if lse is not None:
-            _need(lse, "fp32", rows * 4, dev, "attend_prefix: lse")
-        _need(workspace, None, 0, dev, "attend_prefix: workspace")
-        status = skv_attend_prefix(self.h, c, B, heads, layer, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                   1.0 / 24.0 if sm_scale is None else sm_scale, workspace.data_ptr(), workspace.nbytes,
-                                   _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
-        if status:
-            check(status, "skv_attend_prefix")
-
-    def join(self, outs, lses, out, lse=None, stream=None) -> None:
-        """Join attention results over disjoint sets of tokens (see skv_join): outs, up to 8 of
-        [...][512] bf16, and lses [...] fp32 -> out, lse, which may take a part's place."""
-        parts, dev, size = len(outs), self.cfg.device, out.numel()
-        if len(lses) != parts or not 1 <= parts <= 8:
-            raise ValueError("join: 1 to 8 parts, each with its lse")
-        if out.shape[-1] != 512:
-            raise ValueError("join: out must be [...][512]")
-        rows = size // 512
-        for o, e in zip(outs, lses):
-            if o.numel() != size or e.numel() != rows:
-                raise ValueError("join: the parts and the result differ in size")
-            _need(o, "bf16", rows * 1024, dev, "join: outs")
-            _need(e, "fp32", rows * 4, dev, "join: lses")
-        _need(out, "bf16", rows * 1024, dev, "join: out")
-        if lse is not None:
-            _need(lse, "fp32", rows * 4, dev, "join: lse")
-        both = _pointers[parts](*[o.data_ptr() for o in outs], *[e.data_ptr() for e in lses])
-        status = skv_join(self.h, parts, both, ctypes.byref(both, 8 * parts), rows,
-                          out.data_ptr(), None if lse is None else lse.data_ptr(),
-                          _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
-        if status:
-            check(status, "skv_join")
-
-    def weigh_prefix_workspace(self, prefix: Prefix, B: int, heads: int = 128, layer: int = -1) -> int:
-        """Bytes of workspace a weigh_prefix() of B entries needs."""
-        n = ctypes.c_int64()
-        check(skv_weigh_prefix_workspace(self.h, prefix.c(), B, heads, layer, ctypes.byref(n)), "skv_weigh_prefix_workspace")
-        return n.value
-
-    def weigh_prefix(self, prefix: Prefix, q, lse, weights, out, workspace, layer: int = -1, sm_scale: float | None = None,
-                     gain: float = 1.0, B: int | None = None, stream=None) -> None:
-        """out = weights (or 0 for None) + gain times the attention weight that each of the prefix's
-        tokens receives from the batch (see skv_weigh_prefix): q [units][heads][576] bf16, lse
-        [units][heads], weights and out [L][n] fp32 (may be the same)."""
-        c, B, units, heads, n, dev = self._prefix(prefix, q, layer, B, "weigh_prefix")
-        rows = units * heads
-        _need(q, "bf16", rows * 1152, dev, "weigh_prefix: q")
-        _need(lse, "fp32", rows * 4, dev, "weigh_prefix: lse")
-        w_stride = 0 if weights is None else self._weights(weights, n, dev, "weigh_prefix: weights")
-        o_stride = self._weights(out, n, dev, "weigh_prefix: out")
-        _need(workspace, None, 0, dev, "weigh_prefix: workspace")
-        status = skv_weigh_prefix(self.h, c, B, heads, layer, q.data_ptr(), lse.data_ptr(), None if weights is None else weights.data_ptr(),
-                                  w_stride, out.data_ptr(), o_stride, 1.0 / 24.0 if sm_scale is None else sm_scale, gain,
-                                  workspace.data_ptr(), workspace.nbytes,
-                                  _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
-        if status:
-            check(status, "skv_weigh_prefix")
-
-    def evict_prefix_workspace(self, prefix: Prefix, layer: int = -1) -> int:
-        """Bytes of workspace an evict_prefix() needs."""
-        n = ctypes.c_int64()
-        check(skv_evict_prefix_workspace(self.h, prefix.c(), layer, ctypes.byref(n)), "skv_evict_prefix_workspace")
-        return n.value
-
-    def evict_prefix(self, prefix: Prefix, weights, kept, rows, kept_weights, workspace, first: int = 0, last: int = 0,
-                     layer: int = -1, stream=None) -> None:
-        """Keep a prefix's heaviest tokens (see skv_evict_prefix): weights [L][n] fp32 -> kept
-        [layers of the call][keep] int32, ascending, their rows [..][keep][576] bf16 and weights [..][keep] (either may be
-        None).  Prefix(rows) takes the old one's place."""
-        c, _, layers, _, n, dev = self._prefix(prefix, None, layer, None, "evict_prefix")
-        keep = kept.shape[-1]
-        stride = self._weights(weights, n, dev, "evict_prefix: weights")
-        _need(kept, "int32", 4 * layers * keep, dev, "evict_prefix: kept")
-        if rows is not None:
-            _need(rows, "bf16", 1152 * layers * keep, dev, "evict_prefix: rows")
-        if kept_weights is not None:
-            _need(kept_weights, "fp32", 4 * layers * keep, dev, "evict_prefix: kept_weights")
-        _need(workspace, None, 0, dev, "evict_prefix: workspace")
-        status = skv_evict_prefix(self.h, c, layer, weights.data_ptr(), stride, keep, first, last, kept.data_ptr(),
-                                  None if rows is None else rows.data_ptr(), None if kept_weights is None else kept_weights.data_ptr(),
-                                  workspace.data_ptr(), workspace.nbytes,
-                                  _raw_stream(dev) if stream is None else _stream_handle(stream, dev))
-        if status:
-            check(status, "skv_evict_prefix")
-
     def selftest_attend_timeout(self, req_ids, q, slots, out, B: int | None = None, stream=None) -> None:
         """The attention kernel with its key loads withheld: its waits run out
         and it reports SKV_DEVERR_TIMEOUT (see skv_selftest_attend_timeout)."""
@@ -646,13 +656,6 @@ class Context:
         check(skv_selftest_select_timeout(self.h, index.c(q.shape[-2]), _ptr(req_ids), B, _ptr(q), _ptr(w), _ptr(topk),
                                           _ptr(workspace), workspace.nbytes, _stream_handle(stream, self.cfg.device)),
               "skv_selftest_select_timeout")
-
-    def selftest_prefix_timeout(self, prefix: Prefix, q, lse, out, weights, workspace, B: int | None = None, stream=None) -> None:
-        """attend_prefix() (out given) or weigh_prefix() with its loads withheld (see skv_selftest_prefix_timeout)."""
-        c, B, _, heads, _, dev = self._prefix(prefix, q, -1, B, "selftest_prefix_timeout")
-        check(skv_selftest_prefix_timeout(self.h, c, B, heads, _ptr(q), _ptr(lse), _ptr(out), _ptr(weights),
-                                          0 if weights is None else weights.stride(0), _ptr(workspace), workspace.nbytes,
-                                          _stream_handle(stream, dev)), "skv_selftest_prefix_timeout")
 
     # inspection ------------------------------------------------------------
     def get_device_error(self, stream=None) -> int:

@@ -295,6 +295,19 @@ def test_heads_that_attended_to_nothing_add_nothing():
     assert not bool(c.weigh(lse, before).any())
 
 
+@pytest.mark.parametrize("B,heads", [(4, 40), (1, 128), (3, 37)])
+def test_an_infinite_key_that_no_head_attends_to_weighs_nothing(B, heads):
+    """Tiles that are not full, and heads that attended to nothing, meet it with zeros."""
+    c = Case(B, 1, 300, heads)
+    lse = c.shares()
+    c.q[..., 3] = -1.0
+    c.rows[0, 17, 3] = math.inf
+    lse[0, 2] = -math.inf
+    c.q[0, 2] = 0.0
+    got = c.weigh(lse, torch.zeros((1, 300), device="cuda"))
+    assert got[0, 17] == 0 and not bool(torch.isnan(got).any())
+
+
 def test_weights_twice_are_the_same():
     c = Case(50, 1, 900)
     lse, before = c.shares(), torch.rand((1, 900), device="cuda")

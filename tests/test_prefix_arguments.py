@@ -110,3 +110,35 @@ def test_a_prefix_that_is_changed_is_described_anew():
     with pytest.raises(ValueError):
         p.rows = p.rows.half()
     assert p.n == N + 2
+
+
+STREAM_CALLS = {
+    "attend_prefix": lambda c, **k: c.attend_prefix(_prefix(), torch.zeros((L, H, 576), dtype=BF16), torch.zeros((L, H, 512), dtype=BF16), None,
+                                                    torch.zeros(64, dtype=torch.uint8), **k),
+    "join": lambda c, **k: c.join([torch.zeros((1, 512), dtype=BF16)], [torch.zeros(1)], torch.zeros((1, 512), dtype=BF16), **k),
+    "weigh_prefix": lambda c, **k: c.weigh_prefix(_prefix(), torch.zeros((L, H, 576), dtype=BF16), torch.zeros((L, H)), None,
+                                                  torch.zeros((L, N)), torch.zeros(64, dtype=torch.uint8), **k),
+    "evict_prefix": lambda c, **k: c.evict_prefix(_prefix(), torch.zeros((L, N)), torch.zeros((L, 4), dtype=torch.int32), None, None,
+                                                  torch.zeros(64, dtype=torch.uint8), **k),
+    "selftest_prefix_timeout": lambda c, **k: c.selftest_prefix_timeout(_prefix(), torch.zeros((L, H, 576), dtype=BF16), None,
+                                                                        torch.zeros((L, H, 512), dtype=BF16), None,
+                                                                        torch.zeros(64, dtype=torch.uint8), **k),
+}
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_a_call_goes_to_the_stream_given_or_to_the_devices_current_one(ctx, monkeypatch, name):
+    asked = []
+    monkeypatch.setattr(skv, "_raw_stream", lambda device: asked.append(device) or 0)
+    with pytest.raises(SkvError):
+        STREAM_CALLS[name](ctx)
+    assert asked == [-1]
+    with pytest.raises(SkvError):
+        STREAM_CALLS[name](ctx, stream=0)
+    assert asked == [-1]
+
+
+def test_every_call_around_a_prefix_that_takes_a_stream_is_covered():
+    import inspect
+    takes = {n for n, f in vars(skv.PrefixCalls).items() if callable(f) and "stream" in inspect.signature(f).parameters}
+    assert takes == set(STREAM_CALLS)
