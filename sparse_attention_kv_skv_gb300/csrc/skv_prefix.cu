@@ -1209,11 +1209,11 @@ __global__ void __launch_bounds__(kShortThreads) heaviest_short_kernel(Heaviest 
     }
 }
 
-// Long rows: chunks of 8192 tokens, a CTA each, over the whole GPU.  Three passes find the threshold's digits (11, 11 and
+// Long rows: chunks of 4096 tokens, a CTA each, over the whole GPU.  Three passes find the threshold's digits (11, 11 and
 // 10 bits, from the top) by histograms of the words that share the digits found so far; the last CTA of a layer to finish a pass
-// picks the digit.  A fourth pass counts, a fifth writes.  Each pass reads the weights once, from L2 after the first: 34 us in all at
-// 2 x 1M tokens (one team of CTAs a layer took 96).
-constexpr int kChunk = 8192, kLongThreads = 512;
+// picks the digit.  A fourth pass counts, a fifth writes.  Each pass reads the weights once, from L2 after the first: 29 us in all at
+// 2 x 1M tokens (chunks of 8192 32, of 2048 38; one team of CTAs a layer 96).
+constexpr int kChunk = 4096, kLongThreads = 512, kEachLong = kChunk / kLongThreads;
 struct LongState {  // of a layer; zeros before the first pass
     uint32_t hist[3][kBins];
     uint32_t done[3];
@@ -1288,15 +1288,15 @@ __global__ void __launch_bounds__(kLongThreads) digit_kernel(Heaviest h, LongSta
     }
 }
 
-__device__ __forceinline__ void chunk_bits(const Heaviest& h, const float* w, uint32_t tv, uint32_t (&a)[16], uint32_t (&e)[16], uint32_t& na, uint32_t& ne)
+__device__ __forceinline__ void chunk_bits(const Heaviest& h, const float* w, uint32_t tv, uint32_t (&a)[kEachLong], uint32_t (&e)[kEachLong], uint32_t& na, uint32_t& ne)
 {
-    // a warp has 512 consecutive tokens of the chunk
+    // a warp has consecutive tokens of the chunk
     const int lane = threadIdx.x & 31, j0 = blockIdx.x * kChunk + (threadIdx.x >> 5) * (kChunk / (kLongThreads / 32)) + lane;
-    float x[16];
+    float x[kEachLong];
     h.read(w, j0, 32, x);
     na = ne = 0u;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kEachLong; ++i) {
         const uint32_t v = h.word(x[i], j0 + 32 * i);
         a[i] = __ballot_sync(0xFFFFFFFFu, j0 + 32 * i < h.n && v > tv);
         e[i] = __ballot_sync(0xFFFFFFFFu, j0 + 32 * i < h.n && v == tv);
@@ -1312,7 +1312,7 @@ __global__ void __launch_bounds__(kLongThreads) count_kernel(Heaviest h, const L
     chain_next();
     chain_wait();
     const LongState& st = behind_wait(states)[blockIdx.y];
-    uint32_t a[16], e[16], na, ne;
+    uint32_t a[kEachLong], e[kEachLong], na, ne;
     chunk_bits(h, behind_wait(h.weights) + blockIdx.y * h.stride, st.digits, a, e, na, ne);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) {
@@ -1338,7 +1338,7 @@ __global__ void __launch_bounds__(kLongThreads) place_kernel(Heaviest h, const L
         for (int64_t i = (int64_t)blockIdx.x * kLongThreads + tid; i < h.keep; i += (int64_t)gridDim.x * kLongThreads) kept[i] = -1;
         return;
     }
-    uint32_t a[16], e[16], na, ne, ca = 0, ce = 0;
+    uint32_t a[kEachLong], e[kEachLong], na, ne, ca = 0, ce = 0;
     chunk_bits(h, behind_wait(h.weights) + blockIdx.y * h.stride, tv, a, e, na, ne);
     if (lane == 0) {
         wa[warp] = na;
@@ -1365,7 +1365,7 @@ __global__ void __launch_bounds__(kLongThreads) place_kernel(Heaviest h, const L
     const uint32_t below = (1u << lane) - 1u;
     const int j0 = blockIdx.x * kChunk + warp * (kChunk / (kLongThreads / 32)) + lane;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kEachLong; ++i) {
         const uint32_t er = eb + __popc(e[i] & below), ar = ab + __popc(a[i] & below);
         if (a[i] >> lane & 1u || (e[i] >> lane & 1u && er < ties)) kept[ar + min(er, ties)] = j0 + 32 * i;
         ab += __popc(a[i]);
@@ -1374,7 +1374,9 @@ __global__ void __launch_bounds__(kLongThreads) place_kernel(Heaviest h, const L
 }
 
 // The tokens that stay (kept, ascending, -1 behind the last): their rows and weights moved together.  A warp
-// moves four rows, nine 16-byte pieces a lane.  Bound by HBM: 191 us at 2 x 262144 rows (1.21 GB, 6.3 TB/s).
+// moves four rows, nine 16-byte pieces a lane.  Bound by HBM: 181 us at 2 x 262144 rows (1.21 GB, 6.7 TB/s, a copy's rate; 192 with
+// a CTA for every 32 rows, 224 with streaming stores or loads that pass L1 by, 200 in pieces of 32 bytes).
+constexpr int kKeepGrid = 152 * 24;  // CTAs a layer, at most
 __global__ void __launch_bounds__(256) keep_kernel(PrefixShape p, const float* weights, int64_t weights_stride, int keep,
                                                    const int32_t* kept, uint4* rows_out, float* weights_out)
 {
@@ -1432,7 +1434,7 @@ cudaError_t launch_evict(const PrefixShape& p, const float* weights, int64_t wei
             e = launch_chained(place_kernel, grid, kLongThreads, 0, st, h, static_cast<const LongState*>(states), static_cast<const uint2*>(counts), kept);
     }
     if (e != cudaSuccess || (!rows_out && !weights_out) || p.n == 0) return e;
-    return launch_chained(keep_kernel, dim3((unsigned)std::min<int64_t>(((int64_t)keep + 31) / 32, 1 << 20), layers), 256, 0, st, p, weights,
+    return launch_chained(keep_kernel, dim3((unsigned)std::min<int64_t>(((int64_t)keep + 31) / 32, kKeepGrid), layers), 256, 0, st, p, weights,
                           weights_stride, keep, static_cast<const int32_t*>(kept), static_cast<uint4*>(rows_out), weights_out);
 }
 

@@ -172,7 +172,7 @@ def test_a_prefix_whose_rows_lie_beyond_four_gigabytes():
     assert torch.equal(kept[0].long(), at) and torch.equal(small[0], rows[0][at]) and torch.equal(kw[0], w[0][at])
 
 
-@pytest.mark.parametrize("n,keep", [(32768, 30000), (32769, 1), (8192 * 5, 8192 * 4), (8192 * 5 + 1, 16), (300000, 299999)])
+@pytest.mark.parametrize("n,keep", [(32768, 30000), (32769, 1), (8192 * 5, 8192 * 4), (8192 * 5 + 1, 16), (4096 * 9 - 1, 5000), (300000, 299999)])
 def test_eviction_at_the_borders_of_its_kernels(n, keep):
     rows, w = _rows(2, n, 0), torch.randn((2, n), device="cuda").exp()
     with context(L=2) as ctx:
