@@ -118,6 +118,52 @@ def test_attention_within_an_sm_budget(B, n, sms):
     c.check()
 
 
+def test_a_workspace_for_another_sm_budget_is_refused_where_it_is_too_small():
+    c = Case(37, 1, 3000)
+    need = {}
+    for sms in (0, 4, 8, 100):
+        c.ctx.set_attend_sms(sms)
+        need[sms] = c.ctx.attend_prefix_workspace(c.prefix, 37)
+    small, large = min(need, key=need.get), max(need, key=need.get)
+    assert need[small] < need[large]
+    c.ctx.set_attend_sms(large)
+    with pytest.raises(skv.SkvError):
+        c.ctx.attend_prefix(c.prefix, c.q, c.out, c.lse, _bytes(need[small]), sm_scale=SCALE)
+    work = _bytes(need[large] + 4096)
+    work[need[large]:] = 99
+    c.ctx.attend_prefix(c.prefix, c.q, c.out, c.lse, work[:need[large]], sm_scale=SCALE)
+    c.check()
+    assert bool((work[need[large]:] == 99).all())  # nothing is written behind it
+
+
+@pytest.mark.parametrize("B,L,n,heads", [(3, 2, 4000, 128), (9, 1, 70000, 40)])
+def test_nothing_is_written_behind_a_workspace(B, L, n, heads):
+    c = Case(B, L, n, heads)
+    lse, w, out = c.shares(), torch.rand((L, n), device="cuda"), torch.empty((L, n), device="cuda")
+    sizes = [c.ctx.attend_prefix_workspace(c.prefix, B, heads), c.ctx.weigh_prefix_workspace(c.prefix, B, heads),
+             c.ctx.evict_prefix_workspace(c.prefix)]
+    works = [torch.full((b + 4096,), 99, dtype=torch.uint8, device="cuda") for b in sizes]
+    kept = torch.empty((L, n // 3), dtype=torch.int32, device="cuda")
+    c.ctx.attend_prefix(c.prefix, c.q, c.out, c.lse, works[0][:sizes[0]], sm_scale=SCALE)
+    c.ctx.weigh_prefix(c.prefix, c.q, lse, w, out, works[1][:sizes[1]], sm_scale=SCALE)
+    c.ctx.evict_prefix(c.prefix, w, kept, None, None, works[2][:sizes[2]])
+    for b, t in zip(sizes, works):
+        assert bool((t[b:] == 99).all())
+    assert c.ctx.get_device_error() == 0
+
+
+def test_join_without_lse():
+    outs = [torch.randn((70, 512), device="cuda").bfloat16() for _ in range(3)]
+    lses = [torch.randn(70, device="cuda") for _ in range(3)]
+    a, b, lse = torch.empty_like(outs[0]), torch.empty_like(outs[0]), torch.empty_like(lses[0])
+    with context() as ctx:
+        ctx.join(outs, lses, a, lse)
+        ctx.join(outs, lses, b)
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+        ctx.join(outs, lses, outs[0], lses[2])  # in two parts' places
+        assert torch.equal(a.view(torch.int16), outs[0].view(torch.int16)) and torch.equal(lse, lses[2])
+
+
 def test_queries_that_lie_off_a_border_of_32_bytes_are_refused():
     c = Case(2, 1, 300)
     flat = torch.zeros(2 * 128 * 576 + 16, device="cuda", dtype=torch.bfloat16)
