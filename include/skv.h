@@ -479,7 +479,7 @@ SKV_API skv_status skv_attend_prefix_workspace(skv_ctx *ctx, const skv_prefix *p
  *   out[unit][h][0..512) = sum_j softmax_j(s_h)_j * row(l, j)[0..512)
  *   lse[unit][h] = log sum_j exp(s_hj)   (n == 0: -inf, and zero output)
  * q_dev [units][heads][576] bf16, out_dev [units][heads][512] bf16, lse_dev
- * [units][heads] fp32 (may be null); device memory, q 32-byte, out and workspace 16-byte
+ * [units][heads] fp32 (may be null); device memory, q, out and workspace 16-byte
  * aligned; sm_scale finite and > 0.  Products on the tensor cores in fp32, P
  * rounded to bf16; the output is divided by the sum of the rounded P, lse is that of the
  * unrounded ones.  A head with a NaN score has NaN results.  With skv_join the result

@@ -407,22 +407,26 @@ cudaError_t launch_weigh(const PrefixShape& p, int all_layers, const void* q, co
 // reference there is while the maxima travel, and again if it has risen.  P goes into shared memory, by
 // a bulk copy into the other pair's as well.
 // Items that do not fill the clusters evenly are split along the keys; combine_prefix_kernel joins their parts.
+// An item's queries are its products' first operand, 384 of their 576 dims in tensor memory; those come by way of the P and V tiles,
+// which nothing has used yet (or has finished with: item_done), and the values are loaded once they have been taken.
+// PV(g) is issued once S(g + 1) is (s_issued), so that the two streams of products take turns and the softmax of g + 1 starts early.
 // What bounds it: the products, 2176 cycles a block (36 of 256 x 64 x 16, 8 of 256 x 256 x 16), beside which shared memory
 // moves 265 KB (2070 cycles); from S to P there are an exchange of maxima, 64 exponentials a thread and the copy of P, some 2500 cycles, which
-// the products of the next scores cover.  Measured: 941 us at 192 x 2 units over 16K tokens, 1.86 PFLOP/s, 96 % of a
-// large library product's rate; 172 us at 8 units over 128K (1.70); 13.6 us at 2 over 1000, 18.6 at 7 x 3 of 16 heads over 5003, where a
-// launch, the queries' way into tensor memory (3 us), one block's chain, the parts' way out (2 us) and the joining kernel (3 us) are all there is.
+// the products of the next scores cover.  Measured: 920 us at 192 x 2 units over 16K tokens, 1.90 PFLOP/s, 98 % of a
+// large library product's rate; 173 us at 8 units over 128K (1.69); 12.8 us at 2 over 1000, 18.1 at 7 x 3 of 16 heads over 5003, where a
+// launch, the queries' way into tensor memory (2 us), one block's chain, the parts' way out (2 us) and the joining kernel (3 us) are all there is.
 // On the way here, at 192 x 2 units: a pair for each half of the value dims, both taking all scores, 1539 us; this decomposition
 // with one warp for both streams of products 1075; waits and arrivals at cluster scope and the scores' columns in stages of their
 // own 2151.  The code has to stay small: with 112 KB of it instead of 60 the instruction caches, which GPCs share, were what
 // bounded it (1628 us; GPCs with three clusters were done in 249 us where those with five took 340).
+// With the queries read into tensor memory by plain loads and the products in the order they come: 932, 171, 13.6 and 18.5; waiting for the
+// next P tile as soon as one is sent, ahead of the next scores, 994.
 // Scores double-buffered, with more of Q in shared memory: 1118; P by st.async instead of bulk copies: 1079 (against 1050).
 constexpr int kBlk = 128, kHalfBlk = 64;       // keys of a block, and those that a pair scores
 constexpr int kKRing = 2, kVRing = 2;          // key stages (32 keys, 36 KB), value stages (64 keys x 128 dims, 16 KB)
 constexpr uint32_t kKBox = 32 * 128, kKStage = kBoxes * kKBox, kVBox = 64 * 128, kVStage = 2 * kVBox;
 constexpr uint32_t kPBox = kTileRows * 128, kPTile = 2 * kPBox;  // P: 128 rows x 64 keys of a pair, both pairs' (two tiles)
 constexpr int kVHalf = kVDim / 2;
-constexpr int kQAtOnce = 2;  // query columns a thread reads at once into tensor memory
 constexpr int kQtBoxes = 6, kQsBoxes = kBoxes - kQtBoxes;  // query columns in tensor memory, in shared memory
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;    // tensor memory: O 256 columns, S 64, Q 192
 constexpr int kQWarp0 = 4, kAKeyWarp = 8, kAValueWarp = 9, kAScoreWarp = 10, kAValueMmaWarp = 11, kAThreads = 384;
@@ -431,13 +435,16 @@ struct alignas(16) AttendCtl {
     // "leader": the barrier of the pair's first CTA, which multiplies
     uint64_t q_full, q_tm, q_free;             // queries in shared memory (leader, bytes of both CTAs), in tensor memory
                                                // (leader, a warp of either CTA); the item's scores are done (both)
+    uint64_t q_way, way_free;                  // queries on their way to tensor memory have arrived; have been taken (a warp each)
     uint64_t k_full[kKRing], k_free[kKRing];   // key stages (leader, bytes of both CTAs; both)
     uint64_t v_full[kVRing], v_free[kVRing];   // value stages
     uint64_t s_full, s_free;                   // a block's scores are complete (both); have been read (leader, a warp of either)
+    uint64_t s_issued[4];                      // a block's scores are on their way (in the first CTA; they may be three blocks ahead)
     uint64_t m_full[2];                        // the other pair's maxima of a block have arrived (512 bytes)
     uint64_t x_full[2];                        // the other pair's half of a P tile has arrived (16 KB)
     uint64_t p_full[2];                        // a P tile is complete (leader: a warp of either CTA, and the second CTA once x_full)
     uint64_t pv_done[2];                       // O += P V of a block has completed in both pairs (all four CTAs)
+    uint64_t item_done;                        // the last of an item's, as well (a waiter that does not follow the blocks)
     uint64_t l_full;                           // the other pair's shares of the sums have arrived (1024 bytes)
     uint64_t o_free;                           // an item's output has been read (leader, a warp of either CTA)
     uint64_t fin;                              // every product of the pair has completed (both streams)
@@ -447,6 +454,7 @@ struct alignas(16) AttendCtl {
 constexpr uint32_t kAOffP = kQsBoxes * kTileBox, kAOffK = kAOffP + 2 * kPTile, kAOffV = kAOffK + kKRing * kKStage,
                    kAOffCtl = kAOffV + kVRing * kVStage, kASmem = kAOffCtl + sizeof(AttendCtl);
 static_assert(kASmem <= kSmemLimit && kAOffV % 1024 == 0, "shared memory of attend_prefix_kernel");
+static_assert(2 * kPTile == 4 * kTileBox && kVRing * kVStage == 2 * kTileBox && kQtBoxes == 6, "the queries' way");
 static_assert(kColQ + kQtBoxes * 32 <= 512, "tensor memory of attend_prefix_kernel");
 
 struct AttendPlan {
@@ -464,7 +472,7 @@ struct AttendPlan {
 
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
     attend_prefix_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap value_map,
-                         const __grid_constant__ CUtensorMap q_map, PrefixShape p, AttendPlan plan, const uint16_t* q,
+                         const __grid_constant__ CUtensorMap q_map, PrefixShape p, AttendPlan plan,
                          uint16_t* out, float* lse, float scale_log2, uint32_t* err, int withhold)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -480,6 +488,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
         tc::mbar_init(&c.q_full, 1);
         tc::mbar_init(&c.q_tm, 8);
         tc::mbar_init(&c.q_free, 1);
+        tc::mbar_init(&c.q_way, 1);
+        tc::mbar_init(&c.way_free, 4);
         for (int i = 0; i < kKRing; ++i) {
             tc::mbar_init(&c.k_full[i], 1);
             tc::mbar_init(&c.k_free[i], 1);
@@ -489,6 +499,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
             tc::mbar_init(&c.v_free[i], 1);
         }
         tc::mbar_init(&c.s_full, 1);
+        for (int i = 0; i < 4; ++i) tc::mbar_init(&c.s_issued[i], 1);
         tc::mbar_init(&c.s_free, 8);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&c.m_full[i], 1);
@@ -496,6 +507,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
             tc::mbar_init(&c.p_full[i], 9);
             tc::mbar_init(&c.pv_done[i], 2);
         }
+        tc::mbar_init(&c.item_done, 2);
         tc::mbar_init(&c.l_full, 1);
         tc::mbar_init(&c.o_free, 8);
         tc::mbar_init(&c.fin, 2);
@@ -526,11 +538,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
         w.b1 = i < plan.direct ? plan.all_blocks : min(plan.all_blocks, w.b0 + plan.blocks);
         return w;
     };
+    // where column x of the queries passes on its way to tensor memory
+    auto way_of = [&](int x) -> uint32_t { return x < 4 ? kAOffP + x * kTileBox : kAOffV + (x - 4) * kTileBox; };
     auto at_leader = [&](uint64_t* bar) { return tc::map_to_rank(tc::smem_u32(bar), leader); };
 
     if (warp == kAKeyWarp) {
         if (lane == 0 && !withhold) {
-            const uint32_t qf = at_leader(&c.q_full), kf = at_leader(&c.k_full[0]), q_bytes = (uint32_t)(per * p.heads) * 128u;
+            const uint32_t qf = at_leader(&c.q_full), qw = tc::map_to_rank(tc::smem_u32(&c.q_way), rank);
+            const uint32_t kf = at_leader(&c.k_full[0]), q_bytes = (uint32_t)(per * p.heads) * 128u;
             bool ok = true;
             int g = 0, n = 0;  // blocks, pieces
             for (int i = cl; ok && i < pieces; i += ncl, ++n) {
@@ -543,12 +558,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
                     for (int x = 0; x < kBoxes; ++x)
                         tc::tma2_load3(tc::smem_u32(smem) + kAOffK + st * kKStage + x * kKBox, &key_map, 64 * x,
                                        kBlk * b + kHalfBlk * (int)half + 32 * (int)r, p.layer0 + w.l, kf + 8 * st);
-                    if (b == w.b0) {
-                        if (n > 0 && !(ok = wait_phase(&c.q_free, (n - 1) & 1, abort))) break;
+                    if (b == w.b0) {  // the item's queries: most of them by way of the P and V tiles, once those are free
+                        if (n > 0 && !(ok = wait_phase(&c.q_free, (n - 1) & 1, abort) &&
+                                            wait_phase(&c.item_done, (n - 1) & 1, abort)))
+                            break;
+                        tc::mbar_arrive_expect_tx(&c.q_way, kQtBoxes * q_bytes);
                         if (r == 0) tc::mbar_arrive_expect_tx(&c.q_full, 2 * kQsBoxes * q_bytes);
-                        for (int y = 0; y < kQsBoxes; ++y)
-                            tc::tma2_load4(tc::smem_u32(smem) + y * kTileBox, &q_map, 64 * (kQtBoxes + y), 0, w.l,
-                                           (2 * w.pair + (int)r) * per, qf);
+#pragma unroll 1
+                        for (int x = 0; x < kBoxes; ++x)
+                            tc::tma2_load4(tc::smem_u32(smem) + (x < kQtBoxes ? way_of(x) : (x - kQtBoxes) * kTileBox), &q_map, 64 * x,
+                                           0, w.l, (2 * w.pair + (int)r) * per, x < kQtBoxes ? qw : qf);
                     }
                 }
             }
@@ -559,13 +578,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
         if (lane == 0 && !withhold) {
             const uint32_t vf = at_leader(&c.v_full[0]);
             bool ok = true;
-            int g = 0;  // value stages
-            for (int i = cl; ok && i < pieces; i += ncl) {
+            int g = 0, n = 0;  // value stages, pieces
+            for (int i = cl; ok && i < pieces; i += ncl, ++n) {
                 const Piece w = piece_of(i);
+                if (!(ok = wait_phase(&c.way_free, n & 1, abort))) break;
                 for (int b = 2 * w.b0; b < 2 * w.b1; ++b, ++g) {
                     const int st = g % kVRing;
                     if (g >= kVRing && !(ok = wait_phase(&c.v_free[st], ((g / kVRing) - 1) & 1, abort))) break;
                     if (r == 0) tc::mbar_arrive_expect_tx(&c.v_full[st], 2 * kVStage);
+#pragma unroll 1
                     for (int x = 0; x < 2; ++x)
                         tc::tma2_load3(tc::smem_u32(smem) + kAOffV + st * kVStage + x * kVBox, &value_map,
                                        kVHalf * (int)half + 128 * (int)r + 64 * x, 64 * b, p.layer0 + w.l, vf + 8 * st);
@@ -600,6 +621,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
 #pragma unroll 1
                     for (int x = kQtBoxes; x < kBoxes; ++x)
                         tc::mma2_bf16_x4_warp<2, 2>(tb + kColS, dq + (((x - kQtBoxes) * kTileBox) >> 4), ds + ((x * kKBox) >> 4), idesc, 1u);
+                    if (lane == 0) tc::mbar_arrive(&c.s_issued[g & 3]);
+                    __syncwarp();
                     tc::mma2_commit_warp(&c.s_full, mine);
                     tc::mma2_commit_warp(&c.k_free[st], mine);
                     if (b + 1 == w.b1) tc::mma2_commit_warp(&c.q_free, mine);
@@ -632,6 +655,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
                 }
                 if (!(ok = wait(&c.p_full[g & 1], (g >> 1) & 1))) break;
                 if (b == w.b0 && n > 0 && !(ok = wait(&c.o_free, (n - 1) & 1))) break;  // the item before has read its O
+                // behind the next block's scores, which the softmax waits for
+                if (b + 1 < w.b1 && !(ok = wait(&c.s_issued[(g + 1) & 3], ((g + 1) >> 2) & 1))) break;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h, ++gv) {
                     const int st = gv % kVRing;
@@ -643,47 +668,40 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
                 }
                 if (!ok) break;
                 tc::mma2_commit_warp(&c.pv_done[g & 1], 15);
+                if (b + 1 == w.b1) tc::mma2_commit_warp(&c.item_done, 15);
             }
         }
         if (!ok && lane == 0) give_up(&c.abort, err);
         if (r == 0) tc::mma2_commit_warp(&c.fin, mine);
     } else if (warp >= kQWarp0) {
-        // the first 384 dims of the item's queries into tensor memory, a row a thread
+        // the first 384 dims of the item's queries into tensor memory, a row a thread (by plain loads of the rows, which lie 1152
+        // bytes apart, it took a microsecond more)
         const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16) + kColQ, qt = at_leader(&c.q_tm);
-        const uint4* rows = reinterpret_cast<const uint4*>(behind_wait(q));
+        const int row = tid - 32 * kQWarp0;
+        const bool is = row < per * p.heads;
         bool ok = true;
         int n = 0;
         for (int i = cl; i < pieces; i += ncl, ++n) {
-            const Piece w = piece_of(i);
-            const int64_t row = tile_row(p, w.l, 2 * w.pair + (int)r, tid - 32 * kQWarp0);
-            if (n > 0 && !(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.q_free, (n - 1) & 1, abort)))) break;
+            if (!(ok = __all_sync(0xFFFFFFFFu, wait_phase(&c.q_way, n & 1, abort)))) break;
             tc::fence_after_sync();
-            // (each lane reads a row of its own, so it is the number of sectors asked for that takes the time: 32 bytes at once)
 #pragma unroll 1
-            for (int x = 0; x < kQtBoxes; x += kQAtOnce) {
-                uint32_t v[8 * kQAtOnce][4];
+            for (int x = 0; x < kQtBoxes; ++x) {
+                const uint8_t* at = smem + way_of(x) + row * 128;
 #pragma unroll
-                for (int j = 0; j < 8 * kQAtOnce; j += 2) {
-                    const uint4* at = rows + row * (kRowBytes / 16) + 8 * x + j;
-                    if (row < 0) {
-                        v[j][0] = v[j][1] = v[j][2] = v[j][3] = v[j + 1][0] = v[j + 1][1] = v[j + 1][2] = v[j + 1][3] = 0u;
-                    } else {
-                        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                                     : "=r"(v[j][0]), "=r"(v[j][1]), "=r"(v[j][2]), "=r"(v[j][3]), "=r"(v[j + 1][0]), "=r"(v[j + 1][1]),
-                                       "=r"(v[j + 1][2]), "=r"(v[j + 1][3])
-                                     : "l"(at));
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 8 * kQAtOnce; j += 2) {
-                    const uint32_t a[8] = {v[j][0], v[j][1], v[j][2], v[j][3], v[j + 1][0], v[j + 1][1], v[j + 1][2], v[j + 1][3]};
+                for (int j = 0; j < 8; j += 2) {
+                    const uint4 lo = is ? *reinterpret_cast<const uint4*>(at + ((j ^ (row & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+                    const uint4 hi = is ? *reinterpret_cast<const uint4*>(at + (((j + 1) ^ (row & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+                    const uint32_t a[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                     tc::tmem_st8_async(tl + 32 * x + 4 * j, a);
                 }
             }
             tc::tmem_wait_st();
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_at(qt);
+            if (lane == 0) {
+                tc::mbar_arrive(&c.way_free);
+                tc::mbar_arrive_at(qt);
+            }
         }
         if (!ok) give_up(&c.abort, err);
     } else {
@@ -941,8 +959,7 @@ cudaError_t launch_attend_prefix(const PrefixShape& p, int all_layers, const voi
     if (e == cudaSuccess) e = encode_queries(p, q, &q_map);
     if (e != cudaSuccess) return e;
     e = launch_chained(attend_prefix_kernel, dim3(4u * (unsigned)std::min(plan.pieces(), clusters)), kAThreads, kASmem, st, key_map, value_map,
-                       q_map, p, plan, static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), lse, sm_scale * kLog2e, err,
-                       withhold ? 1 : 0);
+                       q_map, p, plan, static_cast<uint16_t*>(out), lse, sm_scale * kLog2e, err, withhold ? 1 : 0);
     if (e != cudaSuccess || plan.rest == 0) return e;
     return launch_chained(plan.splits <= 8 ? combine_prefix_kernel<8> : combine_prefix_kernel<12>, dim3(kVHalf / 16, 4u * (unsigned)plan.rest),
                           512, 0, st, p, plan, static_cast<uint16_t*>(out), lse);
@@ -1532,7 +1549,7 @@ skv_status attend_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_
     if (!shape_ok(ctx, prefix, layer) || !batch_ok(ctx, B, heads) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale))
         return SKV_ERR_INVALID_ARG;
     if (B == 0) return SKV_OK;
-    if (!rows_ok(ctx, *prefix) || !q_dev || !out_dev || !workspace_dev || workspace_bytes < attend_workspace(ctx, *prefix, B, heads, layer) || !aligned(q_dev, 32) ||
+    if (!rows_ok(ctx, *prefix) || !q_dev || !out_dev || !workspace_dev || workspace_bytes < attend_workspace(ctx, *prefix, B, heads, layer) || !aligned(q_dev, 16) ||
         !aligned(out_dev, 16) || !aligned(lse_dev, 4) || !aligned(workspace_dev, 16))
         return SKV_ERR_INVALID_ARG;
     const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);
