@@ -913,10 +913,11 @@ __global__ void __launch_bounds__(256) nothing_kernel(int64_t rows, uint4* out, 
 }
 
 // Whole items for full rounds of the clusters; the rest in splits such that its rounds are short.  In units of a block's time
-// (1.25 us): rounds * (blocks + 2.5 for what a piece costs besides) and, for the joining of the parts, 2 and what their bytes
-// take (0.5 MB a split, written and read).  Swept over the splits, the choice was the fastest or within 0.2 us of it at 2 x 1000
-// (14.9 us with 8 splits, 16.8 with 2, 19.9 with one), 7 x 3 x 5003 of 16 heads (19.2 with 10, 24.9 with 4 and with 20),
-// 8 x 3000, 64 x 2000, 80 x 2000 (44.1 with 8, 57.3 with one) and 1 x 20000 tokens (23.5 with 40, 36 with 9).
+// (1.25 us): rounds * (blocks + 2.5 for what a piece costs besides) and, for the joining of the parts, 2, what their bytes
+// take (0.5 MB a split, written and read) and 0.8 for every 12 splits after the first 12.  Swept over the splits, the choice was
+// the fastest or within 0.2 us of it at 2 x 1000 (12.9 us with 8 splits, 18.5 with one), 1 x 3000 (14.1 with 12, 15.7 with 24),
+// 1 x 10000, 1 x 20000 (21.8 with 32, 23.3 with 23) and 1 x 100000, 2 x 2 x 3000 and 9000, 6 x 3000 and 20000, 2 x 8 x 2000 and 20000,
+// 7 x 3 x 5003 of 16 heads (18.1 with 10, 20.3 with 8), 64 x 2000 (31.6 with one, 47.8 with 2) and 80 x 2000 tokens (46.0 with 8, 55.2 with one).
 AttendPlan attend_plan(int64_t n, int B, int heads, int layers, int ncl)
 {
     const int nblk = (int)((n + kBlk - 1) / kBlk);
@@ -927,7 +928,7 @@ AttendPlan attend_plan(int64_t n, int B, int heads, int layers, int ncl)
     for (int k = 1; k <= std::min(nblk, 64); ++k) {
         const int blocks = (nblk + k - 1) / k;
         if ((nblk + blocks - 1) / blocks != k) continue;  // the last splits would be empty
-        const double cost = (double)((a.rest * (int64_t)k + ncl - 1) / ncl) * (blocks + 2.5) + (k > 1 ? 2.0 + 0.07 * k * a.rest : 0.0);
+        const double cost = (double)((a.rest * (int64_t)k + ncl - 1) / ncl) * (blocks + 2.5) + (k > 1 ? 2.0 + 0.07 * k * a.rest + 0.8 * ((k - 1) / 12) : 0.0);
         if (cost < least) {
             least = cost;
             a.splits = k;
