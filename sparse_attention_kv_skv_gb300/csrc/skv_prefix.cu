@@ -67,14 +67,15 @@ __device__ __forceinline__ void give_up(uint32_t* abort, uint32_t* err)
     }
 }
 
-// The end of a kernel of a CTA pair, by all threads of both; rank 0 has committed `fin` behind its last product.
+// The end of a kernel of a CTA pair, by all threads of both; rank 0 has committed `fin` behind its last product.  What other
+// pairs of the cluster commit to a CTA it has waited for before it comes here.
 // `owner`: the warp that holds the tensor memory.
 __device__ __forceinline__ void pair_exit(uint64_t* fin, uint32_t* abort, uint32_t* err, uint32_t tbase, bool owner, uint32_t cols)
 {
     tc::fence_before_sync();
     __syncthreads();
     if (threadIdx.x == 0) {
-        // no product, and no arrival of one, is left when either CTA leaves
+        // no product of the pair, and no arrival of one, is left when either CTA leaves
         if (!tc::mbar_wait(fin, 0, 1u << 22)) give_up(abort, err);
         if (*(volatile uint32_t*)abort)  // copies of a call that gave up may still be landing: they take microseconds
             for (int i = 0; i < 256; ++i) __nanosleep(1000);
@@ -444,7 +445,7 @@ struct alignas(16) AttendCtl {
     uint64_t x_full[2];                        // the other pair's half of a P tile has arrived (16 KB)
     uint64_t p_full[2];                        // a P tile is complete (leader: a warp of either CTA, and the second CTA once x_full)
     uint64_t pv_done[2];                       // O += P V of a block has completed in both pairs (all four CTAs)
-    uint64_t item_done;                        // the last of an item's, as well (a waiter that does not follow the blocks)
+    uint64_t item_done;                        // the last of an item's, as well, where another item follows (a waiter that does not follow the blocks)
     uint64_t l_full;                           // the other pair's shares of the sums have arrived (1024 bytes)
     uint64_t o_free;                           // an item's output has been read (leader, a warp of either CTA)
     uint64_t fin;                              // every product of the pair has completed (both streams)
@@ -668,7 +669,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
                 }
                 if (!ok) break;
                 tc::mma2_commit_warp(&c.pv_done[g & 1], 15);
-                if (b + 1 == w.b1) tc::mma2_commit_warp(&c.item_done, 15);
+                // only where its waiter comes: an arrival that nobody waits for could reach a CTA that has left
+                if (b + 1 == w.b1 && i + ncl < pieces) tc::mma2_commit_warp(&c.item_done, 15);
             }
         }
         if (!ok && lane == 0) give_up(&c.abort, err);
