@@ -462,7 +462,9 @@ SKV_API skv_status skv_select(skv_ctx *ctx, const skv_index *index, const int32_
  * of their KV); the pages give no operator for it. */
 typedef struct {
     const void *rows;      /* 16-byte aligned; may be null where n is 0 */
-    int64_t layer_stride;  /* multiples of 16, > 0, < 2^40 (free where the axis has one entry) */
+    int64_t layer_stride;  /* multiples of 16, > 0, < 2^40 (free where the axis has one entry).  Calls on all layers are
+                              one launch where the layers lie a whole number of rows apart, or side by side within a
+                              row's stride (a cache [n][L][576]), and one for each layer else. */
     int64_t row_stride;    /* >= 1152 */
     int64_t n;             /* tokens, 0 <= n <= 2^30 */
 } skv_prefix;

@@ -30,7 +30,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 struct PrefixShape {
     const uint8_t* rows;
     int64_t layer_stride, row_stride;
-    int n, B, heads, layers, layer0;  // layers of the call; layer0: the first of them
+    int n, B, heads, layers, layer0;  // layers of the launch; layer0: the first of them
+    int unit_layers;                  // layers of the call: an entry has that many units
+    int map_x, map_z;                 // where layer l of the launch begins in the rows' tensor map: column l * map_x, plane l * map_z
     __device__ __forceinline__ const uint4* row(int l, int j) const
     {
         return reinterpret_cast<const uint4*>(rows + (layer0 + l) * layer_stride + j * row_stride);
@@ -88,11 +90,12 @@ __device__ __forceinline__ void pair_exit(uint64_t* fin, uint32_t* abort, uint32
     }
 }
 
-// The query row that lies in row r of tile `tile`: its unit's first head's row plus its head, or -1.
+// The query row that lies in row r of tile `tile`: its unit's first head's row plus its head, or -1.  (Of a launch on one of
+// several layers, counted from that layer's first unit.)
 __device__ __forceinline__ int64_t tile_row(const PrefixShape& p, int l, int tile, int r)
 {
     const int per = entries_a_tile(p.heads), e = r / p.heads, b = tile * per + e;
-    return e < per && b < p.B ? ((int64_t)b * p.layers + l) * p.heads + (r - e * p.heads) : -1;
+    return e < per && b < p.B ? ((int64_t)b * p.unit_layers + l) * p.heads + (r - e * p.heads) : -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -198,8 +201,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
                         if (pr == p0) {
                             if (n > 0 && !(ok = wait_phase(&c.a_free[x], (n - 1) & 1, abort))) break;
                             if (rank == 0) tc::mbar_arrive_expect_tx(&c.a_full[x], 2 * kTileBox);
-                            tc::tma2_load3(tc::smem_u32(smem) + x * kTileBox, &key_map, 64 * x, 256 * tile + 128 * (int)rank,
-                                           p.layer0 + l, af + 8 * x);
+                            tc::tma2_load3(tc::smem_u32(smem) + x * kTileBox, &key_map, 64 * x + l * p.map_x, 256 * tile + 128 * (int)rank,
+                                           l * p.map_z, af + 8 * x);
                         }
                         const int st = g % kWRing;
                         if (g >= kWRing && !(ok = wait_phase(&c.b_free[st], ((g / kWRing) - 1) & 1, abort))) break;
@@ -342,18 +345,57 @@ WeighPlan weigh_plan(int64_t n, int B, int heads, int layers, int device_sms)
     return best;
 }
 
-// The prefix as [layers][n][576], box `box` rows by 64 columns; the queries as [B][layers][heads][576], box the
+// How a tensor map holds the rows of a launch's layers.  Every stride of a map has to be a multiple of the one before it, so
+// planes [layers][n][576] where a layer's stride is a multiple of a row's; where the layers lie side by side within a row's
+// stride (a cache [n][layers][576]) columns of one plane; else (layers padded by a part of a row) a launch takes one layer.
+enum class RowsMap { kPlanes, kColumns, kOneLayer };
+int64_t columns_bytes(const PrefixShape& p) { return (p.layers - 1) * p.layer_stride + kRowBytes; }
+RowsMap rows_map(const PrefixShape& p)
+{
+    const int64_t row = p.row_stride, layer = p.layer_stride;
+    if (p.layers == 1 || p.n == 0) return RowsMap::kPlanes;
+    if (p.n == 1) return layer >= kRowBytes ? RowsMap::kPlanes : RowsMap::kOneLayer;
+    if (row < kRowBytes || layer % row == 0) return RowsMap::kPlanes;  // (fewer bytes a row are refused where the rows are read)
+    // (a column's number has 32 bits)
+    const bool beside = layer >= kRowBytes && layer <= INT32_MAX && row >= columns_bytes(p) && columns_bytes(p) <= INT32_MAX;
+    return beside ? RowsMap::kColumns : RowsMap::kOneLayer;
+}
+int launch_layers(const PrefixShape& p) { return rows_map(p) == RowsMap::kOneLayer ? 1 : p.layers; }
+
+// Calls f(the shape of a launch, units before its first one) for each launch on a tensor map that the call takes.
+template <typename F>
+cudaError_t for_each_launch(PrefixShape p, F f)
+{
+    if (launch_layers(p) == p.layers) {
+        p.map_x = rows_map(p) == RowsMap::kColumns ? (int)(p.layer_stride / 2) : 0;
+        p.map_z = p.map_x ? 0 : 1;
+        return f(p, (int64_t)0);
+    }
+    cudaError_t e = cudaSuccess;
+    const int layer0 = p.layer0, layers = p.layers;
+    p.layers = 1;
+    p.map_x = p.map_z = 0;
+    for (int l = 0; l < layers && e == cudaSuccess; ++l) {
+        p.layer0 = layer0 + l;
+        e = f(p, (int64_t)l);
+    }
+    return e;
+}
+
+// The rows of a launch's layers, box `box` rows by 64 columns; the queries as [B][layers][heads][576], box the
 // entries of a tile by 64 columns.  128-byte swizzle; what lies outside reads as zeros.
-cudaError_t encode_rows(const PrefixShape& p, int all_layers, int box, CUtensorMap* map)
+cudaError_t encode_rows(const PrefixShape& p, int box, CUtensorMap* map)
 {
     TensorMapEncoder encode = nullptr;
     const cudaError_t e = tensor_map_encoder(&encode);
     if (e != cudaSuccess) return e;
-    const cuuint64_t dims[3] = {kDim, (cuuint64_t)p.n, (cuuint64_t)all_layers};
-    // the stride of an axis with one entry is never used
-    const cuuint64_t strides[2] = {(cuuint64_t)(p.n > 1 ? p.row_stride : kRowBytes), (cuuint64_t)(all_layers > 1 ? p.layer_stride : kRowBytes)};
+    const bool columns = p.map_x != 0;
+    const cuuint64_t dims[3] = {(cuuint64_t)(columns ? columns_bytes(p) / 2 : kDim), (cuuint64_t)p.n, (cuuint64_t)(columns ? 1 : p.layers)};
+    // the stride of an axis with one entry is never used: the next one's, or the one's before
+    const int64_t row = p.n > 1 ? p.row_stride : p.layers > 1 ? p.layer_stride : kRowBytes;
+    const cuuint64_t strides[2] = {(cuuint64_t)row, (cuuint64_t)(columns || p.layers == 1 ? row : p.layer_stride)};
     const cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(p.rows), dims, strides, boxes, ones,
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(p.rows) + p.layer0 * p.layer_stride, dims, strides, boxes, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
@@ -365,7 +407,7 @@ cudaError_t encode_queries(const PrefixShape& p, const void* q, CUtensorMap* map
     const cudaError_t e = tensor_map_encoder(&encode);
     if (e != cudaSuccess) return e;
     const cuuint64_t dims[4] = {kDim, (cuuint64_t)p.heads, (cuuint64_t)p.layers, (cuuint64_t)p.B};
-    const cuuint64_t strides[3] = {kRowBytes, (cuuint64_t)kRowBytes * p.heads, (cuuint64_t)kRowBytes * p.heads * p.layers};
+    const cuuint64_t strides[3] = {kRowBytes, (cuuint64_t)kRowBytes * p.heads, (cuuint64_t)kRowBytes * p.heads * p.unit_layers};
     const cuuint32_t boxes[4] = {64, (cuuint32_t)p.heads, 1, (cuuint32_t)entries_a_tile(p.heads)}, ones[4] = {1, 1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, boxes, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -374,24 +416,29 @@ cudaError_t encode_queries(const PrefixShape& p, const void* q, CUtensorMap* map
                : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_weigh(const PrefixShape& p, int all_layers, const void* q, const float* lse, const float* weights,
+dim3 weigh_sum_grid(const PrefixShape& p) { return dim3((unsigned)((p.n + 255) / 256), (unsigned)p.layers); }
+// The weights as they are (an empty batch).
+cudaError_t launch_weigh_nothing(const PrefixShape& p, const float* weights, int64_t weights_stride, float* out, int64_t out_stride,
+                                 cudaStream_t st)
+{
+    return launch_chained(weigh_sum_kernel, weigh_sum_grid(p), 256, 0, st, p, 0, static_cast<const float*>(nullptr), weights, weights_stride,
+                          out, out_stride, 0.0f);
+}
+
+cudaError_t launch_weigh(const PrefixShape& p, const void* q, const float* lse, const float* weights,
                          int64_t weights_stride, float* out, int64_t out_stride, float sm_scale, float gain, float* part,
                          uint32_t* err, int device_sms, cudaStream_t st, bool withhold = false)
 {
-    const dim3 sum_grid((unsigned)((p.n + 255) / 256), (unsigned)p.layers);
-    if (p.B == 0)  // the weights as they are
-        return launch_chained(weigh_sum_kernel, sum_grid, 256, 0, st, p, 0, static_cast<const float*>(nullptr), weights, weights_stride,
-                              out, out_stride, gain);
     const WeighPlan plan = weigh_plan(p.n, p.B, p.heads, p.layers, device_sms);
     CUtensorMap key_map, q_map;
-    cudaError_t e = encode_rows(p, all_layers, kTileRows, &key_map);
+    cudaError_t e = encode_rows(p, kTileRows, &key_map);
     if (e == cudaSuccess) e = encode_queries(p, q, &q_map);
     if (e != cudaSuccess) return e;
     const unsigned grid = 2u * (unsigned)std::min(plan.pieces, std::max(1, device_sms / 2));
     e = launch_chained(weigh_kernel, dim3(grid), kWThreads, kWSmem, st, key_map, q_map, p, plan, lse, weights, weights_stride, out,
                        out_stride, part, sm_scale * kLog2e, gain, err, withhold ? 1 : 0);
     if (e != cudaSuccess || plan.shares == 1) return e;
-    return launch_chained(weigh_sum_kernel, sum_grid, 256, 0, st, p, plan.shares,
+    return launch_chained(weigh_sum_kernel, weigh_sum_grid(p), 256, 0, st, p, plan.shares,
                           static_cast<const float*>(part), weights, weights_stride, out, out_stride, gain);
 }
 
@@ -557,8 +604,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
                     if (r == 0) tc::mbar_arrive_expect_tx(&c.k_full[st], 2 * kKStage);
 #pragma unroll 1
                     for (int x = 0; x < kBoxes; ++x)
-                        tc::tma2_load3(tc::smem_u32(smem) + kAOffK + st * kKStage + x * kKBox, &key_map, 64 * x,
-                                       kBlk * b + kHalfBlk * (int)half + 32 * (int)r, p.layer0 + w.l, kf + 8 * st);
+                        tc::tma2_load3(tc::smem_u32(smem) + kAOffK + st * kKStage + x * kKBox, &key_map, 64 * x + w.l * p.map_x,
+                                       kBlk * b + kHalfBlk * (int)half + 32 * (int)r, w.l * p.map_z, kf + 8 * st);
                     if (b == w.b0) {  // the item's queries: most of them by way of the P and V tiles, once those are free
                         if (n > 0 && !(ok = wait_phase(&c.q_free, (n - 1) & 1, abort) &&
                                             wait_phase(&c.item_done, (n - 1) & 1, abort)))
@@ -590,7 +637,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kAThreads, 1)
 #pragma unroll 1
                     for (int x = 0; x < 2; ++x)
                         tc::tma2_load3(tc::smem_u32(smem) + kAOffV + st * kVStage + x * kVBox, &value_map,
-                                       kVHalf * (int)half + 128 * (int)r + 64 * x, 64 * b, p.layer0 + w.l, vf + 8 * st);
+                                       kVHalf * (int)half + 128 * (int)r + 64 * x + w.l * p.map_x, 64 * b, w.l * p.map_z, vf + 8 * st);
                 }
             }
             if (!ok) give_up(&c.abort, err);
@@ -945,20 +992,22 @@ AttendPlan attend_plan(int64_t n, int B, int heads, int layers, int ncl)
 }
 int64_t attend_bytes(const AttendPlan& a) { return (int64_t)a.rest * a.splits * 2 * kTileRows * (kVDim + 1) * 4; }
 
-cudaError_t launch_attend_prefix(const PrefixShape& p, int all_layers, const void* q, void* out, float* lse, float sm_scale,
+cudaError_t launch_attend_nothing(const PrefixShape& p, void* out, float* lse, cudaStream_t st)
+{
+    const int64_t rows = (int64_t)p.B * p.layers * p.heads;
+    nothing_kernel<<<(unsigned)std::min<int64_t>((rows * (kVDim / 8) + 255) / 256, 1 << 16), 256, 0, st>>>(rows, static_cast<uint4*>(out), lse);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attend_prefix(const PrefixShape& p, const void* q, void* out, float* lse, float sm_scale,
                                  void* workspace, uint32_t* err, int clusters, cudaStream_t st, bool withhold = false)
 {
-    if (p.n == 0) {
-        const int64_t rows = (int64_t)p.B * p.layers * p.heads;
-        nothing_kernel<<<(unsigned)std::min<int64_t>((rows * (kVDim / 8) + 255) / 256, 1 << 16), 256, 0, st>>>(rows, static_cast<uint4*>(out), lse);
-        return cudaGetLastError();
-    }
     AttendPlan plan = attend_plan(p.n, p.B, p.heads, p.layers, clusters);
     plan.o = static_cast<float*>(workspace);
     plan.lse = plan.o + (int64_t)plan.rest * plan.splits * 2 * kTileRows * kVDim;
     CUtensorMap key_map, value_map, q_map;
-    cudaError_t e = encode_rows(p, all_layers, 32, &key_map);
-    if (e == cudaSuccess) e = encode_rows(p, all_layers, 64, &value_map);
+    cudaError_t e = encode_rows(p, 32, &key_map);
+    if (e == cudaSuccess) e = encode_rows(p, 64, &value_map);
     if (e == cudaSuccess) e = encode_queries(p, q, &q_map);
     if (e != cudaSuccess) return e;
     e = launch_chained(attend_prefix_kernel, dim3(4u * (unsigned)std::min(plan.pieces(), clusters)), kAThreads, kASmem, st, key_map, value_map,
@@ -1527,21 +1576,23 @@ int attend_clusters(const skv_ctx* ctx)
 {
     return ctx->attend_sms > 0 ? std::max(1, std::min(ctx->prefix_clusters, ctx->attend_sms / 4)) : ctx->prefix_clusters;
 }
+int call_layers(const skv_ctx* ctx, int32_t layer) { return layer < 0 ? ctx->cfg.num_layers : 1; }
 PrefixShape shape_of(const skv_ctx* ctx, const skv_prefix& x, int32_t B, int32_t heads, int32_t layer)
 {
+    const int layers = call_layers(ctx, layer);
     return PrefixShape{static_cast<const uint8_t*>(x.rows), x.layer_stride, x.row_stride, (int)x.n, B, heads,
-                       layer < 0 ? ctx->cfg.num_layers : 1, layer < 0 ? 0 : layer};
+                       layers, layer < 0 ? 0 : layer, layers, 0, 1};
 }
-int call_layers(const skv_ctx* ctx, int32_t layer) { return layer < 0 ? ctx->cfg.num_layers : 1; }
 int64_t attend_workspace(const skv_ctx* ctx, const skv_prefix& x, int32_t B, int32_t heads, int32_t layer)
 {
     if (B == 0 || x.n == 0) return 16;
-    return std::max<int64_t>(16, skv::attend_bytes(skv::attend_plan(x.n, B, heads, call_layers(ctx, layer), attend_clusters(ctx))));
+    const int layers = skv::launch_layers(shape_of(ctx, x, B, heads, layer));
+    return std::max<int64_t>(16, skv::attend_bytes(skv::attend_plan(x.n, B, heads, layers, attend_clusters(ctx))));
 }
 int64_t weigh_workspace(const skv_ctx* ctx, const skv_prefix& x, int32_t B, int32_t heads, int32_t layer)
 {
     if (B == 0 || x.n == 0) return 16;
-    const int layers = call_layers(ctx, layer), shares = skv::weigh_plan(x.n, B, heads, layers, ctx->device_sms).shares;
+    const int layers = skv::launch_layers(shape_of(ctx, x, B, heads, layer)), shares = skv::weigh_plan(x.n, B, heads, layers, ctx->device_sms).shares;
     return shares > 1 ? skv::align16((int64_t)shares * layers * x.n * 4) : 16;
 }
 
@@ -1557,8 +1608,13 @@ skv_status attend_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_
         return SKV_ERR_INVALID_ARG;
     const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);
     return on_device(ctx, "skv_attend_prefix", [&] {
-        return skv::launch_attend_prefix(p, ctx->cfg.num_layers, q_dev, out_dev, lse_dev, sm_scale, workspace_dev,
-                                         &ctx->d.ctl[skv::CTL_ERR], attend_clusters(ctx), stream, withhold);
+        if (p.n == 0) return skv::launch_attend_nothing(p, out_dev, lse_dev, stream);
+        return skv::for_each_launch(p, [&](const PrefixShape& part, int64_t units) {
+            const int64_t row = units * heads;
+            return skv::launch_attend_prefix(part, static_cast<const uint8_t*>(q_dev) + row * skv::kRowBytes,
+                                             static_cast<uint16_t*>(out_dev) + row * skv::kVDim, lse_dev ? lse_dev + row : nullptr, sm_scale,
+                                             workspace_dev, &ctx->d.ctl[skv::CTL_ERR], attend_clusters(ctx), stream, withhold);
+        });
     });
 }
 
@@ -1581,8 +1637,13 @@ skv_status weigh_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_t
         return SKV_ERR_INVALID_ARG;
     const PrefixShape p = shape_of(ctx, *prefix, B, heads, layer);
     return on_device(ctx, "skv_weigh_prefix", [&] {
-        return skv::launch_weigh(p, ctx->cfg.num_layers, q_dev, lse_dev, weights_dev, weights_stride, out_dev, out_stride, sm_scale,
-                                 gain, static_cast<float*>(workspace_dev), &ctx->d.ctl[skv::CTL_ERR], ctx->device_sms, stream, withhold);
+        if (B == 0) return skv::launch_weigh_nothing(p, weights_dev, weights_stride, out_dev, out_stride, stream);
+        return skv::for_each_launch(p, [&](const PrefixShape& part, int64_t units) {
+            const int64_t row = units * heads;
+            return skv::launch_weigh(part, static_cast<const uint8_t*>(q_dev) + row * skv::kRowBytes, lse_dev + row, weights_dev,
+                                     weights_stride, out_dev, out_stride, sm_scale, gain, static_cast<float*>(workspace_dev),
+                                     &ctx->d.ctl[skv::CTL_ERR], ctx->device_sms, stream, withhold);
+        });
     });
 }
 }  // namespace
