@@ -1136,7 +1136,9 @@ __global__ void __launch_bounds__(256) keep_all_kernel(Heaviest h, int32_t* kept
 // Short rows: a CTA a layer, its words in shared memory.  The range of the words is narrowed by histograms of 2048
 // equal parts until the part that holds the threshold has few enough to be ranked directly; the first range is that of the
 // words themselves, so mostly the first histogram is the only one.  Bound by latency: some ten barriers; 5 us at 4096 tokens,
-// 13 at 8 x 16001.
+// 10 at 8 x 16001 (replayed from a graph).  Short is what shared memory holds; the passes for long rows, swept over 1 to 61 layers: 15 to 24 us
+// where this takes 10 (16001 tokens), 16 to 27 where it takes 13 (24000), 17 to 29 where it takes 16 to 17 (32768).  With the rows moved as
+// well that is within 6 % from 24000 tokens on, either way.
 constexpr int kShort = 32768, kShortThreads = 1024, kBins = 2048, kFew = 256;
 __global__ void __launch_bounds__(kShortThreads) heaviest_short_kernel(Heaviest h, int32_t* kept)
 {
@@ -1445,7 +1447,7 @@ __global__ void __launch_bounds__(kLongThreads) place_kernel(Heaviest h, const L
 // The tokens that stay (kept, ascending, -1 behind the last): their rows and weights moved together.  A warp
 // moves four rows, nine 16-byte pieces a lane.  Bound by HBM: 181 us at 2 x 262144 rows (1.21 GB, 6.7 TB/s, a copy's rate; 192 with
 // a CTA for every 32 rows, 224 with streaming stores or loads that pass L1 by, 200 in pieces of 32 bytes).
-constexpr int kKeepGrid = 152 * 24;  // CTAs a layer, at most
+constexpr int kKeepCtas = 24;  // CTAs a layer for every SM, at most
 __global__ void __launch_bounds__(256) keep_kernel(PrefixShape p, const float* weights, int64_t weights_stride, int keep,
                                                    const int32_t* kept, uint4* rows_out, float* weights_out)
 {
@@ -1481,7 +1483,7 @@ int64_t evict_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
 int64_t evict_bytes(int64_t n, int layers) { return n <= kShort ? 16 : layers * ((int64_t)sizeof(LongState) + evict_chunks(n) * (int64_t)sizeof(uint2)); }
 
 cudaError_t launch_evict(const PrefixShape& p, const float* weights, int64_t weights_stride, int keep, int first, int last,
-                         int32_t* kept, void* rows_out, float* weights_out, void* workspace, const uint32_t* err, cudaStream_t st)
+                         int32_t* kept, void* rows_out, float* weights_out, void* workspace, const uint32_t* err, int device_sms, cudaStream_t st)
 {
     const Heaviest h{p.n ? weights + p.layer0 * weights_stride : nullptr, weights_stride, p.n, keep, first, last, err};
     const unsigned layers = (unsigned)p.layers;
@@ -1503,7 +1505,7 @@ cudaError_t launch_evict(const PrefixShape& p, const float* weights, int64_t wei
             e = launch_chained(place_kernel, grid, kLongThreads, 0, st, h, static_cast<const LongState*>(states), static_cast<const uint2*>(counts), kept);
     }
     if (e != cudaSuccess || (!rows_out && !weights_out) || p.n == 0) return e;
-    return launch_chained(keep_kernel, dim3((unsigned)std::min<int64_t>(((int64_t)keep + 31) / 32, kKeepGrid), layers), 256, 0, st, p, weights,
+    return launch_chained(keep_kernel, dim3((unsigned)std::min<int64_t>(((int64_t)keep + 31) / 32, kKeepCtas * device_sms), layers), 256, 0, st, p, weights,
                           weights_stride, keep, static_cast<const int32_t*>(kept), static_cast<uint4*>(rows_out), weights_out);
 }
 
@@ -1735,7 +1737,7 @@ skv_status skv_evict_prefix(skv_ctx* ctx, const skv_prefix* prefix, int32_t laye
     const PrefixShape p = shape_of(ctx, *prefix, 1, 1, layer);
     return on_device(ctx, "skv_evict_prefix", [&] {
         return skv::launch_evict(p, weights_dev, weights_stride, keep, first, last, kept_dev, rows_out_dev, weights_out_dev, workspace_dev,
-                                 &ctx->d.ctl[skv::CTL_ERR], stream);
+                                 &ctx->d.ctl[skv::CTL_ERR], ctx->device_sms, stream);
     });
 }
 
