@@ -514,8 +514,8 @@ SKV_API skv_status skv_weigh_prefix_workspace(skv_ctx *ctx, const skv_prefix *pr
  *   out[l][j] = weights[l][j] + gain * sum_{units of l} sum_h exp(s_hj - lse[unit][h])
  * lse_dev [units][heads] fp32 is the log of the sum the weights are shares of: that of skv_join for shares of
  * a request's whole attention, that of skv_attend_prefix for shares within the prefix.  A head whose lse is -inf adds nothing.
- * weights_dev (null: zeros) and out_dev (may be the same) hold row l at l*weights_stride and l*out_stride
- * floats, in calls on one layer too; nothing behind out[l][n - 1] is written.  gain finite (a gain
+ * weights_dev (null: zeros) and out_dev hold row l at l*weights_stride and l*out_stride floats, in calls on one layer
+ * too; a row of out may be the same layer's row of weights, and overlaps no other one (SKV_ERR_INVALID_ARG); nothing behind out[l][n - 1] is written.  gain finite (a gain
  * that grows from step to step lets older weights fade).  q_dev 16-byte aligned; the rest as in skv_attend_prefix.
  * B == 0: out is weights.  Sums are fp32 in a fixed order: the same call gives the same result. */
 SKV_API skv_status skv_weigh_prefix(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads, int32_t layer,

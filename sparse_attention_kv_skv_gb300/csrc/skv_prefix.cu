@@ -1620,6 +1620,20 @@ skv_status attend_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_
     });
 }
 
+// A layer's new weights may take its old ones' place, and lie on nothing else that the call reads.
+bool in_place_ok(const float* weights, int64_t weights_stride, const float* out, int64_t out_stride, int64_t n, int64_t layer0, int64_t layers)
+{
+    if (!weights || (weights == out && weights_stride == out_stride)) return true;
+    const int64_t last = layer0 + layers - 1, bytes = 4 * n;
+    auto read = [&](int64_t l) { return (int64_t)(reinterpret_cast<uintptr_t>(weights) + (uint64_t)(4 * l * weights_stride)); };
+    auto written = [&](int64_t l) { return (int64_t)(reinterpret_cast<uintptr_t>(out) + (uint64_t)(4 * l * out_stride)); };
+    if (read(last) + bytes <= written(layer0) || written(last) + bytes <= read(layer0)) return true;
+    for (int64_t l = layer0; l <= last; ++l)
+        for (int64_t o = layer0; o <= last; ++o)
+            if (read(l) < written(o) + bytes && written(o) < read(l) + bytes && !(l == o && read(l) == written(o))) return false;
+    return true;
+}
+
 skv_status weigh_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_t heads, int32_t layer,
                       const void* q_dev, const float* lse_dev, const float* weights_dev, int64_t weights_stride,
                       float* out_dev, int64_t out_stride, float sm_scale, float gain, void* workspace_dev,
@@ -1633,6 +1647,8 @@ skv_status weigh_impl(skv_ctx* ctx, const skv_prefix* prefix, int32_t B, int32_t
     if (!rows_ok(ctx, *prefix) || !out_dev || !aligned(weights_dev, 4) || !aligned(out_dev, 4) ||
         (many && (out_stride < prefix->n || (weights_dev && weights_stride < prefix->n))) || out_stride >= (int64_t)1 << 40 ||
         weights_stride >= (int64_t)1 << 40)
+        return SKV_ERR_INVALID_ARG;
+    if (!in_place_ok(weights_dev, weights_stride, out_dev, out_stride, prefix->n, layer < 0 ? 0 : layer, call_layers(ctx, layer)))
         return SKV_ERR_INVALID_ARG;
     if (B > 0 && (!q_dev || !lse_dev || !workspace_dev || workspace_bytes < weigh_workspace(ctx, *prefix, B, heads, layer) ||
                   !aligned(q_dev, 16) || !aligned(workspace_dev, 16) || !aligned(lse_dev, 4)))
