@@ -485,11 +485,14 @@ SKV_API skv_status skv_attend_prefix_workspace(skv_ctx *ctx, const skv_prefix *p
  * aligned; sm_scale finite and > 0.  Products on the tensor cores in fp32, P
  * rounded to bf16; the output is divided by the sum of the rounded P, lse is that of the
  * unrounded ones.  A head with a NaN score has NaN results.  With skv_join the result
- * combines with those of skv_attend or skv_attend_q4 over the request's own tokens.
+ * combines with those of skv_attend or skv_attend_q4 over the request's own tokens; these
+ * have 128 heads.
  * The context gives the device, L and max_batch (B <= max_batch) and the error word
- * (SKV_DEVERR_TIMEOUT); its requests and its row_bytes do not matter.  The workspace is the caller's and
+ * (SKV_DEVERR_TIMEOUT); its requests and its row_bytes do not matter.  An entry of the batch is a query, so the
+ * tokens of a prompt may be entries too; a context's step buffers grow with max_batch * L * topk, so calls with many are
+ * best made on one of their own with topk 1.  The workspace is the caller's and
  * holds nothing between calls: two calls, or two captured graphs, that may run at the same time need
- * one each.  Few units are split along the prefix, so results may differ in rounding with B and the SM budget,
+ * one each.  Few units are split along the prefix, so results may differ in rounding with B, the SM budget and how the layers lie,
  * never from call to call.  B == 0 enqueues nothing.  Captures into a CUDA graph. */
 SKV_API skv_status skv_attend_prefix(skv_ctx *ctx, const skv_prefix *prefix, int32_t B, int32_t heads, int32_t layer,
                                      const void *q_dev, void *out_dev, float *lse_dev, float sm_scale,

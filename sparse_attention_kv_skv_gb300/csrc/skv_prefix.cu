@@ -5,6 +5,11 @@
 // For unit (b, l) with `heads` query heads, rows k_j (576 bf16) of layer l, j < n:
 //   s_hj = scale * q_h . k_j;   out_h = sum_j softmax_j(s_h) k_j[0..512);   lse_h = log sum_j exp s_hj
 // Units that share a layer read the same rows, so their heads are rows of one product.
+//
+// Times in this file are of calls replayed from a CUDA graph one after the other, in bursts of some milliseconds at 2.07 GHz,
+// unless said otherwise.  "Among others": a program's call through the Python binding, with others around it.  The difference is
+// the host's and, for products of hundreds of microseconds, the power limit, under which a large library product falls from 1.95
+// PFLOP/s to 1.71.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -43,7 +48,7 @@ struct PrefixShape {
 // The kernels on the tensor cores run as clusters of two CTAs that multiply as one
 // (cta_group::2).  Query rows go in tiles of 128: the heads of 128 / heads entries
 // of a layer, in order; rows that are left over are zeros.
-constexpr uint32_t kMaxSleepPolls = 1u << 20;  // bound of a wait whose polls may each sleep (about 2 s)
+constexpr uint32_t kMaxSleepPolls = 1u << 20;  // bound of a wait whose polls may each sleep (4 s, measured; the longest, for a whole item, is some 3 s with rows that fill the GPU's memory)
 constexpr int kTileRows = 128;
 constexpr int kBoxes = kDim / 64;              // 64-dim columns of a row, 128 bytes wide
 constexpr uint32_t kTileBox = kTileRows * 128; // such a column of a tile of 128 rows
@@ -109,9 +114,9 @@ __device__ __forceinline__ int64_t tile_row(const PrefixShape& p, int l, int til
 // What bounds it: the products, 128 cycles each of 256 x 256 x 16, 4608 a pair of tiles; beside them go 32 bytes a cycle
 // from L2 and 96 of the 128 bytes a cycle that shared memory gives (with a CTA by itself, not a pair, 192 would), and an
 // epilogue of 256 exponentials a thread, 2048 cycles.
-// Measured: 443 us at 192 x 2 units of 128 heads over 16K tokens, 2.1 PFLOP/s, more than the 1.95 of a large library product; 9.1 us
-// at 4 units over 4096 tokens, 11.0 at 5 x 3 of 40 heads over 10007: launch, set-up, 147 KB of keys a CTA, one or two products.
-// (-lse log2 e and the scale in two floats each: 453 us and the same error, which is the tensor core's own.)
+// Measured: 447 us at 192 x 2 units of 128 heads over 16K tokens, 2.07 PFLOP/s (among others 491, 1.89); 9.1 us (9.5)
+// at 4 units over 4096 tokens, 11.5 (13.8) at 5 x 3 of 40 heads over 10007: launch, set-up, 147 KB of keys a CTA, one or two products.
+// (-lse log2 e and the scale in two floats each: 453 us for 443 and the same error, which is the tensor core's own.)
 constexpr int kWRing = 4;                      // query columns in flight (16 KB each)
 constexpr int kWEpilogue = 128, kWLoadWarp = 4, kWMmaWarp = 5, kWThreads = 192;
 constexpr uint32_t kWTmemCols = 512;           // two products of 256 columns
@@ -452,7 +457,9 @@ cudaError_t launch_weigh(const PrefixShape& p, const void* q, const float* lse, 
 // so nothing is multiplied twice.  The CTAs (0, r) and (1, r) swap their row maxima (both take the same reference
 // maximum) and their halves of P, and at an item's end their shares of the sums.
 // The softmax has a query row a thread (the row's tensor-memory lane).  It takes the exponentials with the
-// reference there is while the maxima travel, and again if it has risen.  P goes into shared memory, by
+// reference there is while the maxima travel, and again if it has risen.  P is rounded to bf16, which is what the tensor cores take at full
+// rate; the output is divided by the sum of the rounded values.  With the output's own rounding it is all that the result is off by: 1.7e-3 to
+// 1.9e-3 of its size against 64 bits, 1.65e-3 to 1.7e-3 with P in fp32.  P goes into shared memory, by
 // a bulk copy into the other pair's as well.
 // Items that do not fill the clusters evenly are split along the keys; combine_prefix_kernel joins their parts.
 // An item's queries are its products' first operand, 384 of their 576 dims in tensor memory; those come by way of the P and V tiles,
@@ -460,8 +467,9 @@ cudaError_t launch_weigh(const PrefixShape& p, const void* q, const float* lse, 
 // PV(g) is issued once S(g + 1) is (s_issued), so that the two streams of products take turns and the softmax of g + 1 starts early.
 // What bounds it: the products, 2176 cycles a block (36 of 256 x 64 x 16, 8 of 256 x 256 x 16), beside which shared memory
 // moves 265 KB (2070 cycles); from S to P there are an exchange of maxima, 64 exponentials a thread and the copy of P, some 2500 cycles, which
-// the products of the next scores cover.  Measured: 920 us at 192 x 2 units over 16K tokens, 1.90 PFLOP/s, 98 % of a
-// large library product's rate; 173 us at 8 units over 128K (1.69); 12.8 us at 2 over 1000, 18.1 at 7 x 3 of 16 heads over 5003, where a
+// the products of the next scores cover.  Measured: 913 to 933 us at 192 x 2 units over 16K tokens, 1.88 to 1.92 PFLOP/s in a burst of 2 ms
+// (970 to 996 in one of 15 ms; among others 1046, 1.68); 174 us at 8 units over 128K, 1.68 (among others 189, 1.55); 12.9 us (14.2) at 2 over
+// 1000, 17.9 (18.7) at 7 x 3 of 16 heads over 5003, where a
 // launch, the queries' way into tensor memory (2 us), one block's chain, the parts' way out (2 us) and the joining kernel (3 us) are all there is.
 // On the way here, at 192 x 2 units: a pair for each half of the value dims, both taking all scores, 1539 us; this decomposition
 // with one warp for both streams of products 1075; waits and arrivals at cluster scope and the scores' columns in stages of their
@@ -1024,8 +1032,8 @@ struct JoinParts {
 };
 
 // A warp a row, 16 columns a lane.  All of a row is read before any of it is written, so the result may
-// take a part's place.  Bound by HBM: 91 us at two parts of 192 x 8 units of 128 heads (606 MB, 6.66 TB/s, a copy's
-// rate); at 21 units 2.4 us, a launch and a row's latency.
+// take a part's place.  Bound by HBM: 90 us at two parts of 192 x 8 units of 128 heads (606 MB, 6.7 TB/s, a copy's
+// rate); at 21 units 2.4 us (among others 7.4), a launch and a row's latency.
 template <int kParts>
 __global__ void __launch_bounds__(256) join_kernel(JoinParts parts, int64_t rows, uint4* out, float* lse)
 {
@@ -1136,7 +1144,7 @@ __global__ void __launch_bounds__(256) keep_all_kernel(Heaviest h, int32_t* kept
 // Short rows: a CTA a layer, its words in shared memory.  The range of the words is narrowed by histograms of 2048
 // equal parts until the part that holds the threshold has few enough to be ranked directly; the first range is that of the
 // words themselves, so mostly the first histogram is the only one.  Bound by latency: some ten barriers; 5 us at 4096 tokens,
-// 10 at 8 x 16001 (replayed from a graph).  Short is what shared memory holds; the passes for long rows, swept over 1 to 61 layers: 15 to 24 us
+// 10 at 8 x 16001.  Short is what shared memory holds; the passes for long rows, swept over 1 to 61 layers: 15 to 24 us
 // where this takes 10 (16001 tokens), 16 to 27 where it takes 13 (24000), 17 to 29 where it takes 16 to 17 (32768).  With the rows moved as
 // well that is within 6 % from 24000 tokens on, either way.
 constexpr int kShort = 32768, kShortThreads = 1024, kBins = 2048, kFew = 256;
